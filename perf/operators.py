@@ -420,40 +420,42 @@ def _plain_scored(s):
         dq, dk = torch.empty_like(s["q"]), torch.zeros((B, Hk, S, D), device=DEV)
         dv = torch.zeros((B, Hk, S, D), device=DEV)
     scale = 1.0 / math.sqrt(D)
+    kv_of = torch.arange(H, device=DEV) // (H // Hk)
+    some = max(1, (1 << 29) // (S * S))  # heads at once: scores of at most 2 GB
     for b in range(B):
         ok = _allowed(s, b)
         dist = None
         if s["slopes"] is not None:
             p = s["pos"][b].float()
             dist = (p[:, None] - p[None, :]).abs()
-        for h in range(H):
-            hk = h // (H // Hk)
-            q, k, v = s["q"][b, h].float(), s["k"][b, hk].float(), s["v"][b, hk].float()
-            z = (q @ k.T) * scale
+        for heads in torch.arange(H, device=DEV).split(some):
+            kv = kv_of[heads]
+            q, k, v = s["q"][b, heads].float(), s["k"][b, kv].float(), s["v"][b, kv].float()
+            z = (q @ k.mT) * scale
             t = None
             if cap:
                 t = torch.tanh(z / cap)
                 z = t * cap
             if dist is not None:
-                z = z - s["slopes"][h] * dist
+                z = z - s["slopes"][heads, None, None] * dist
             z = torch.where(ok, z, -math.inf)
-            m = z.amax(dim=1, keepdim=True)
+            m = z.amax(dim=2, keepdim=True)
             m = torch.where(m == -math.inf, 0.0, m)
             p = torch.exp(z - m)
-            l = p.sum(dim=1, keepdim=True)
+            l = p.sum(dim=2, keepdim=True)
             p = p / torch.where(l > 0, l, 1.0)
-            o[b, h] = p @ v
-            lse[b, h] = (m + torch.log(l))[:, 0]
+            o[b, heads] = (p @ v).to(o.dtype)
+            lse[b, heads] = (m + torch.log(l))[..., 0]
             if not train:
                 continue
-            do = s["do"][b, h].float()
-            dv[b, hk] += p.T @ do
-            dp = do @ v.T
-            ds = p * (dp - (p * dp).sum(dim=1, keepdim=True))
+            do = s["do"][b, heads].float()
+            dv[b].index_add_(0, kv, p.mT @ do)
+            dp = do @ v.mT
+            ds = p * (dp - (p * dp).sum(dim=2, keepdim=True))
             if t is not None:
                 ds = ds * (1 - t * t)
-            dq[b, h] = (ds @ k) * scale
-            dk[b, hk] += (ds.T @ q) * scale
+            dq[b, heads] = ((ds @ k) * scale).to(dq.dtype)
+            dk[b].index_add_(0, kv, (ds.mT @ q) * scale)
     if not train:
         return o, lse
     return o, lse, dq, dk.to(torch.bfloat16), dv.to(torch.bfloat16)
@@ -490,29 +492,32 @@ def _plain_rope(s):
 
 def _plain_paged(s):
     case = s["case"]
-    H, Hk, D, cap = case["heads"], case["kv_heads"], case["head_dim"], case["softcap"]
+    H, Hk, cap = case["heads"], case["kv_heads"], case["softcap"]
     o, lse = s["o"], s["lse"]
     at = 0
     for i, (nq, nkv) in enumerate(s["lens"]):
         pages = s["table"][i, :-(-nkv // case["page_slots"])].long()
-        k = s["k"][pages].flatten(0, 1)[:nkv].float()
-        v = s["v"][pages].flatten(0, 1)[:nkv].float()
+        k = s["k"][pages].flatten(0, 1)[:nkv].float().transpose(0, 1)
+        v = s["v"][pages].flatten(0, 1)[:nkv].float().transpose(0, 1)
+        q = s["q"][at:at + nq].float().transpose(0, 1).unflatten(0, (Hk, H // Hk))
         q_pos = torch.arange(nkv - nq, nkv, device=DEV)
         k_pos = torch.arange(nkv, device=DEV)
-        ok = k_pos[None, :] <= q_pos[:, None]
-        for hk in range(Hk):
-            heads = slice(hk * (H // Hk), (hk + 1) * (H // Hk))
-            z = torch.matmul(s["q"][at:at + nq, heads].float().transpose(0, 1), k[:, hk].T) / math.sqrt(D)
+        dist = (q_pos[:, None] - k_pos[None, :]).float()
+        some = max(1, (1 << 30) // (H // Hk * nq * nkv))  # K/V heads at once: scores of at most 4 GB
+        for kv in range(0, Hk, some):
+            qs, ks, vs = q[kv:kv + some], k[kv:kv + some, None], v[kv:kv + some, None]
+            z = torch.matmul(qs, ks.mT) / math.sqrt(case["head_dim"])
             if cap:
                 z = torch.tanh(z / cap) * cap
             if s["slopes"] is not None:
-                z = z - s["slopes"][heads, None, None] * (q_pos[:, None] - k_pos[None, :]).float()
-            z = torch.where(ok, z, -math.inf)
-            m = z.amax(dim=2, keepdim=True)
+                z = z - s["slopes"].unflatten(0, (Hk, -1))[kv:kv + some, :, None, None] * dist
+            z = torch.where(dist >= 0, z, -math.inf)
+            m = z.amax(dim=3, keepdim=True)
             p = torch.exp(z - m)
-            l = p.sum(dim=2, keepdim=True)
-            o[at:at + nq, heads] = (torch.matmul(p, v[:, hk]) / l).transpose(0, 1).to(o.dtype)
-            lse[at:at + nq, heads] = (m + torch.log(l))[:, :, 0].T
+            l = p.sum(dim=3, keepdim=True)
+            heads = slice(kv * (H // Hk), (kv + some) * (H // Hk))
+            o[at:at + nq, heads] = (torch.matmul(p, vs) / l).flatten(0, 1).transpose(0, 1).to(o.dtype)
+            lse[at:at + nq, heads] = (m + torch.log(l))[..., 0].flatten(0, 1).T
         at += nq
     return o, lse
 
