@@ -40,6 +40,7 @@ ENTRY_POINTS = (
     "spattn_profile_read", "spattn_plan_pages", "spattn_plan_qblocks", "spattn_plan_work", "spattn_plan_destroy",
     "spattn_status_string", "spattn_wait_selftest", "spattn_plan_set_graph_device", "spattn_plan_entry_heads",
     "spattn_quantize_fp8", "spattn_fwd_fp8",
+    "spattn_fwd_scored", "spattn_bwd_scored", "spattn_rope",
 )
 
 
@@ -57,6 +58,21 @@ class _Layout(ctypes.Structure):
         ("n_q_groups", ctypes.c_int32), ("n_kv_groups", ctypes.c_int32), ("scale", ctypes.c_float),
         ("kv_heads", ctypes.c_int32), ("graph_batches", ctypes.c_int32),
     ]
+
+
+class _Score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("q_pos", ctypes.c_void_p),
+                ("k_pos", ctypes.c_void_p), ("q_last", ctypes.c_void_p), ("q_doc", ctypes.c_void_p),
+                ("k_doc", ctypes.c_void_p), ("batches", ctypes.c_int32)]
+
+
+class _RopeLayout(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "batch", "heads", "kv_heads", "head_dim", "rot_dim",
+                                              "interleaved", "inverse")] + [
+        ("slots", ctypes.c_int64)] + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "q_out_stride",
+                                                                       "k_out_stride")] + [
+        ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3), ("pos_batch_stride", ctypes.c_int64),
+        ("mscale", ctypes.c_float)]
 
 
 class _Graph(ctypes.Structure):
@@ -91,6 +107,9 @@ def _lib():
         lib.spattn_plan.argtypes = [ctypes.POINTER(_Layout), ctypes.POINTER(_Graph), ctypes.POINTER(P)]
         lib.spattn_fwd.argtypes = [P, P, P, P, P, P, P]
         lib.spattn_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P]
+        lib.spattn_fwd_scored.argtypes = [P, P, P, P, ctypes.POINTER(_Score), P, P, P]
+        lib.spattn_bwd_scored.argtypes = [P, P, P, P, P, P, P, ctypes.POINTER(_Score), P, P, P, P]
+        lib.spattn_rope.argtypes = [ctypes.POINTER(_RopeLayout), P, P, P, P, P, P, P]
         lib.spattn_quantize_fp8.argtypes = [P, I64, I64, ctypes.c_int, P, P, P]
         lib.spattn_fwd_fp8.argtypes = [P, P, P, P, P, P, P, P, P]
         lib.spattn_bwd_noalloc.argtypes = [P, P, P, P, P, P, P, P, P, P, P]
@@ -336,6 +355,243 @@ def spattn_bwd(q, k, v, o, lse, do, plan: Plan, dq=None, dk=None, dv=None, strea
     _check(_lib().spattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), plan.handle, _ptr(dq), _ptr(dk),
                              _ptr(dv), _stream_handle(stream)), "spattn_bwd")
     return dq, dk, dv
+
+
+class Score:
+    """Score modification of :func:`spattn_fwd_scored` / :func:`spattn_bwd_scored` (``spattn_score``).
+
+    ``softcap`` c > 0 caps scores as ``c tanh(x / c)`` (0: none); ``slopes``
+    (fp32 [heads]) subtracts ``slopes[h] |q_pos - k_pos|``; ``q_last`` allows only
+    keys with ``k_pos <= q_last`` (``q_pos`` itself for a causal mask,
+    ``maximum(q_pos, prefix - 1)`` for one with a prefix); ``q_doc`` / ``k_doc``
+    allow only keys of the query's own document (negative ids attend nothing).
+    ``q_*`` are int32 CUDA tensors [q_slots] or [batch, q_slots], ``k_*`` the same
+    over kv_slots, all contiguous and all with or all without the batch dimension.
+    """
+
+    def __init__(self, softcap=0.0, slopes=None, q_pos=None, k_pos=None, q_last=None, q_doc=None, k_doc=None):
+        self.softcap = float(softcap)
+        self.slopes, self.q_pos, self.k_pos, self.q_last, self.q_doc, self.k_doc = slopes, q_pos, k_pos, q_last, q_doc, k_doc
+
+    def _c_struct(self, plan: Plan, device) -> _Score:
+        import torch
+
+        c = _Score(softcap=self.softcap, batches=1)
+        if self.slopes is not None:
+            _need(self.slopes, "slopes", (plan.heads,), torch.float32)
+            _same_device(self.slopes, "slopes", device)
+            c.slopes = self.slopes.data_ptr()
+        dims = set()
+        for name, slots in (("q_pos", plan.q_slots), ("k_pos", plan.kv_slots), ("q_last", plan.q_slots),
+                            ("q_doc", plan.q_slots), ("k_doc", plan.kv_slots)):
+            t = getattr(self, name)
+            if t is None:
+                continue
+            batched = isinstance(t, torch.Tensor) and t.dim() == 2
+            _need(t, name, (plan.batch, slots) if batched else (slots,), torch.int32)
+            _same_device(t, name, device)
+            dims.add(batched)
+            setattr(c, name, t.data_ptr())
+        if len(dims) > 1:
+            raise ValueError("score arrays: either all or none have a batch dimension")
+        c.batches = plan.batch if dims == {True} else 1
+        return c
+
+
+def _same_device(t, name, device):
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
+
+
+def spattn_fwd_scored(q, k, v, plan: Plan, score: Score, o=None, lse=None, stream=None):
+    """O [B,H,Sq,D] bf16 and LSE [B,H,Sq] fp32 for the plan's sparse graph with modified scores."""
+    import torch
+
+    qs = (plan.batch, plan.heads, plan.q_slots, plan.head_dim)
+    ks = (plan.batch, plan.kv_heads, plan.kv_slots, plan.head_dim)
+    _need(q, "q", qs, torch.bfloat16)
+    _need(k, "k", ks, torch.bfloat16)
+    _need(v, "v", ks, torch.bfloat16)
+    sc = score._c_struct(plan, q.device)
+    if o is None:
+        o = torch.empty(qs, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty(qs[:3], dtype=torch.float32, device=q.device)
+    _need(o, "o", qs, torch.bfloat16)
+    _need(lse, "lse", qs[:3], torch.float32)
+    for t, nm in ((k, "k"), (v, "v"), (o, "o"), (lse, "lse")):
+        _same_device(t, nm, q.device)
+    _check(_lib().spattn_fwd_scored(_ptr(q), _ptr(k), _ptr(v), plan.handle, ctypes.byref(sc), _ptr(o), _ptr(lse),
+                                    _stream_handle(stream)), "spattn_fwd_scored")
+    return o, lse
+
+
+def spattn_bwd_scored(q, k, v, o, lse, do, plan: Plan, score: Score, dq=None, dk=None, dv=None, stream=None):
+    """dQ, dK, dV (bf16) of :func:`spattn_fwd_scored` with the same score, given its O and LSE and the loss gradient dO."""
+    import torch
+
+    qs = (plan.batch, plan.heads, plan.q_slots, plan.head_dim)
+    ks = (plan.batch, plan.kv_heads, plan.kv_slots, plan.head_dim)
+    for t, nm, sh in ((q, "q", qs), (k, "k", ks), (v, "v", ks), (o, "o", qs), (do, "do", qs)):
+        _need(t, nm, sh, torch.bfloat16)
+    _need(lse, "lse", qs[:3], torch.float32)
+    sc = score._c_struct(plan, q.device)
+    dq = torch.empty(qs, dtype=torch.bfloat16, device=q.device) if dq is None else dq
+    dk = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dk is None else dk
+    dv = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dv is None else dv
+    _need(dq, "dq", qs, torch.bfloat16)
+    _need(dk, "dk", ks, torch.bfloat16)
+    _need(dv, "dv", ks, torch.bfloat16)
+    for t, nm in ((k, "k"), (v, "v"), (o, "o"), (lse, "lse"), (do, "do"), (dq, "dq"), (dk, "dk"), (dv, "dv")):
+        _same_device(t, nm, q.device)
+    _check(_lib().spattn_bwd_scored(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), plan.handle,
+                                    ctypes.byref(sc), _ptr(dq), _ptr(dk), _ptr(dv), _stream_handle(stream)),
+           "spattn_bwd_scored")
+    return dq, dk, dv
+
+
+def rope_freqs(sections, base=10000.0, scaling=None, factor=1.0, original_slots=4096, beta_fast=32.0, beta_slow=1.0,
+               device="cuda"):
+    """(freqs, mscale) for :func:`rope`: fp64 radians per position of every pair.
+
+    ``sections``: pairs per position axis (an int for one axis); each axis has its
+    own ladder ``base ** (-i / n)``.  ``scaling`` for contexts ``factor`` times the
+    trained one: ``None``; ``"linear"`` divides every frequency by the factor;
+    ``"ntk"`` raises the base by ``factor ** (n / (n - 1))``, so that the slowest
+    pair is divided by the factor and the fastest kept; ``"yarn"`` divides pairs
+    that make fewer than ``beta_slow`` turns over ``original_slots`` positions, keeps
+    those above ``beta_fast`` turns, blends between, and sets mscale = 0.1
+    ln(factor) + 1.
+    """
+    import math
+
+    import torch
+
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"rope_freqs: unknown scaling {scaling!r}")
+    if not (base > 0 and factor > 0):
+        raise ValueError("rope_freqs: base and factor must be positive")
+    sections = [int(sections)] if isinstance(sections, (int, np.integer)) else [int(n) for n in sections]
+    if any(n < 0 for n in sections):
+        raise ValueError("rope_freqs: sections must not be negative")
+    ladders, mscale = [], 1.0
+    for n in sections:
+        i = np.arange(n, dtype=np.float64)
+        b = base * factor ** (n / (n - 1)) if scaling == "ntk" and n > 1 else base
+        f = float(b) ** (-i / n) if n else i
+        if scaling == "linear":
+            f = f / factor
+        elif scaling == "yarn":
+            turns = original_slots * f / (2 * math.pi)
+            keep = np.clip((turns - beta_slow) / (beta_fast - beta_slow), 0.0, 1.0)
+            f = f * keep + f / factor * (1 - keep)
+            mscale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+        ladders.append(f)
+    return torch.from_numpy(np.concatenate(ladders) if ladders else np.zeros(0)).to(device), mscale
+
+
+def _span(t):
+    """[first, end) byte addresses that a tensor's elements touch."""
+    last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _rope(name, inverse, q, k, pos, freqs, rot_dim, interleaved, sections, mscale, q_out, k_out, stream):
+    import torch
+
+    types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+    def rows(t, what, shape=None):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4 or t.dtype not in types:
+            raise ValueError(f"{name}: {what} must be a CUDA bf16, fp16 or fp32 tensor [B, H, S, D]")
+        if t.shape[3] > 1 and t.stride(3) != 1:
+            raise ValueError(f"{name}: {what} must be contiguous in its last dimension")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: {what} must have shape {tuple(shape)}")
+        if t.dtype != q.dtype or t.device != q.device:
+            raise ValueError(f"{name}: {what} must have the type and device of q")
+
+    rows(q, "q")
+    B, H, S, D = q.shape
+    if H < 1 or D < 1:
+        raise ValueError(f"{name}: q must have at least one head and one element per row")
+    if k is not None:
+        rows(k, "k", (B, k.shape[1], S, D) if isinstance(k, torch.Tensor) and k.dim() == 4 else None)
+        if k.shape[1] < 1:
+            raise ValueError(f"{name}: k must have at least one head")
+    elif k_out is not None:
+        raise ValueError(f"{name}: an output for k without k")
+    rot = D if rot_dim is None else int(rot_dim)
+    if rot < 0 or rot > D or rot % 2:
+        raise ValueError(f"{name}: rot_dim must be even and between 0 and {D}")
+    sec = [rot // 2] if sections is None else [int(n) for n in sections]
+    if not 1 <= len(sec) <= 3 or any(n < 0 for n in sec) or sum(sec) != rot // 2:
+        raise ValueError(f"{name}: sections must be one to three counts that sum to rot_dim / 2 = {rot // 2}")
+    if not isinstance(pos, torch.Tensor) or pos.dtype != torch.int32 or pos.device != q.device or not pos.is_contiguous():
+        raise ValueError(f"{name}: pos must be a contiguous int32 tensor on {q.device}")
+    want = ((S,), (len(sec), S), (B, len(sec), S))
+    if tuple(pos.shape) not in (want if len(sec) == 1 else want[1:]):
+        raise ValueError(f"{name}: pos must have shape {want[1]} or {want[2]}" + (f" or {want[0]}" if len(sec) == 1 else ""))
+    if not isinstance(freqs, torch.Tensor) or freqs.dtype != torch.float64 or freqs.device != q.device \
+            or not freqs.is_contiguous() or tuple(freqs.shape) != (rot // 2,):
+        raise ValueError(f"{name}: freqs must be a contiguous fp64 tensor [{rot // 2}] on {q.device}")
+    ins, outs = [q] + ([k] if k is not None else []), []
+    with torch.cuda.device(q.device):
+        for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
+            if x is None:
+                continue
+            if y is None:
+                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            rows(y, f"the output for {what}", x.shape)
+            if any(n > 1 and st == 0 for n, st in zip(y.shape, y.stride())):
+                raise ValueError(f"{name}: the output for {what} has elements that share an address")
+            outs.append(y)
+        own = [y.data_ptr() == x.data_ptr() and all(a == b or n == 1 for a, b, n in zip(x.stride(), y.stride(), x.shape))
+               for x, y in zip(ins, outs)]
+        if q.numel():
+            for i, y in enumerate(outs):
+                for j, x in enumerate(ins):
+                    (a0, a1), (b0, b1) = _span(y), _span(x)
+                    # views of one packed buffer interleave; both in place is the case that is allowed
+                    if a0 < b1 and b0 < a1 and not (own[i] and (i == j or own[j])):
+                        raise ValueError(f"{name}: an output overlaps an input without being in place of it")
+            if len(outs) == 2 and outs[0].data_ptr() == outs[1].data_ptr():
+                raise ValueError(f"{name}: the two outputs share an address")
+        lay = _RopeLayout(dtype=types[q.dtype], batch=B, heads=H, kv_heads=0 if k is None else k.shape[1], head_dim=D,
+                          rot_dim=rot, interleaved=int(bool(interleaved)), inverse=int(inverse), slots=S,
+                          n_axes=len(sec), pos_batch_stride=len(sec) * S if pos.dim() == 3 else 0,
+                          mscale=float(mscale))
+        for i, n in enumerate(sec):
+            lay.sections[i] = n
+        for field, t in (("q_stride", q), ("k_stride", k), ("q_out_stride", outs[0]),
+                         ("k_out_stride", outs[1] if len(outs) > 1 else None)):
+            for i in range(3):
+                getattr(lay, field)[i] = 0 if t is None else t.stride(i)
+        null = ctypes.c_void_p()
+        _check(_lib().spattn_rope(ctypes.byref(lay), _ptr(q), null if k is None else _ptr(k), _ptr(pos), _ptr(freqs),
+                                  _ptr(outs[0]), null if k is None else _ptr(outs[1]), _stream_handle(stream)),
+               "spattn_rope")
+    return outs[0], outs[1] if len(outs) > 1 else None
+
+
+def rope(q, k, pos, freqs, *, rot_dim=None, interleaved=False, sections=None, mscale=1.0, q_out=None, k_out=None,
+         stream=None):
+    """Rotary positions of Q [B,H,S,D] and K [B,Hk,S,D] (or None) in one launch; returns both.
+
+    Inputs and outputs may be strided views (bf16, fp16 or fp32; the last dimension
+    contiguous), an output may be its input; new outputs are contiguous, as
+    spattn_fwd wants them.  ``pos``: int32 [S], [axes, S] or [B, axes, S];
+    ``sections``: pairs per position axis (one axis by default); ``freqs``, ``mscale``:
+    see :func:`rope_freqs`.  ``interleaved`` pairs elements 2p and 2p + 1, else p
+    and p + rot_dim / 2; elements from ``rot_dim`` on are copied.
+    """
+    return _rope("rope", False, q, k, pos, freqs, rot_dim, interleaved, sections, mscale, q_out, k_out, stream)
+
+
+def rope_bwd(dq_out, dk_out, pos, freqs, *, rot_dim=None, interleaved=False, sections=None, mscale=1.0, dq=None,
+             dk=None, stream=None):
+    """Gradient of :func:`rope`: dQ and dK of its inputs from those of its outputs (same arguments)."""
+    return _rope("rope_bwd", True, dq_out, dk_out, pos, freqs, rot_dim, interleaved, sections, mscale, dq, dk, stream)
 
 
 def spattn_check(plan: Plan, stream=None):

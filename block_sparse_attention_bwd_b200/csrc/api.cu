@@ -156,6 +156,103 @@ TileArgs tile_args(const spattn_plan_s* P, const WorkList& w, int64_t own_slots,
   return a;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checked kernel arguments of a spattn_score; *any is false when it changes nothing.
+int score_args(const spattn_plan_s* P, const spattn_score* s, ScoreArgs* a, bool* any) {
+  if (!s || !std::isfinite(s->softcap) || s->softcap < 0.f || (s->batches != 1 && s->batches != P->batch))
+    return SPATTN_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(s->slopes), static_cast<const void*>(s->q_pos),
+                        static_cast<const void*>(s->k_pos), static_cast<const void*>(s->q_last),
+                        static_cast<const void*>(s->q_doc), static_cast<const void*>(s->k_doc)})
+    if (!aligned4(p)) return SPATTN_ERR_INVALID_ARG;
+  if ((s->slopes && (!s->q_pos || !s->k_pos)) || (s->q_last && !s->k_pos) || !s->q_doc != !s->k_doc)
+    return SPATTN_ERR_INVALID_ARG;
+  a->cap = s->softcap;
+  a->slopes = s->slopes;
+  a->q_pos = s->q_pos;
+  a->k_pos = s->k_pos;
+  a->q_last = s->q_last;
+  a->q_doc = s->q_doc;
+  a->k_doc = s->k_doc;
+  a->q_batch = s->batches > 1 ? P->q.slots : 0;
+  a->k_batch = s->batches > 1 ? P->k.slots : 0;
+  *any = s->softcap > 0.f || s->slopes || s->q_last || s->q_doc;
+  return SPATTN_OK;
+}
+
+int run_fwd(const void* q, const void* k, const void* v, spattn_plan_s* plan, const ScoreArgs* sc, void* o, float* lse,
+            void* stream) {
+  if (!plan) return SPATTN_ERR_INVALID_ARG;
+  int st = check_plan_device(plan);
+  if (st) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return SPATTN_ERR_INVALID_ARG;
+  const int D = plan->head_dim;
+  const int64_t bh = static_cast<int64_t>(plan->batch) * plan->heads;
+  const int64_t bh_kv = static_cast<int64_t>(plan->batch) * plan->kv_heads;
+  TmaPages tq, tk, tv;
+  if (!make_pages(&tq, q, D, plan->q.slots, bh) || !make_pages(&tk, k, D, plan->k.slots, bh_kv) ||
+      !make_pages(&tv, v, D, plan->k.slots, bh_kv))
+    return SPATTN_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto* O = static_cast<__nv_bfloat16*>(o);
+  cudaError_t e = timed(plan, SPATTN_K_FWD, s, [&] {
+    return launch_fwd(D, tq, tk, tv, tile_args(plan, plan->wq, plan->q.slots, plan->k.slots), sc, O, lse, s);
+  });
+  if (e == cudaSuccess && !plan->q_fill.empty())
+    e = timed(plan, SPATTN_K_FILL, s, [&] {
+      return launch_fill(D, plan->d_q_fill, static_cast<int64_t>(plan->q_fill.size() / 2), bh, plan->q.slots, O,
+                         nullptr, lse, s);
+    });
+  return e == cudaSuccess ? SPATTN_OK : SPATTN_ERR_CUDA;
+}
+
+int run_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
+            spattn_plan_s* plan, const ScoreArgs* sc, void* dq, void* dk, void* dv, void* stream) {
+  if (!plan) return SPATTN_ERR_INVALID_ARG;
+  int st = check_plan_device(plan);
+  if (st) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(d_o) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return SPATTN_ERR_INVALID_ARG;
+  const int D = plan->head_dim;
+  const int64_t bh = static_cast<int64_t>(plan->batch) * plan->heads;
+  const int64_t bh_kv = static_cast<int64_t>(plan->batch) * plan->kv_heads;
+  TmaPages tq, tk, tv, tdo;
+  if (!make_pages(&tq, q, D, plan->q.slots, bh) || !make_pages(&tk, k, D, plan->k.slots, bh_kv) ||
+      !make_pages(&tv, v, D, plan->k.slots, bh_kv) || !make_pages(&tdo, d_o, D, plan->q.slots, bh))
+    return SPATTN_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto* dQ = static_cast<__nv_bfloat16*>(dq);
+  auto* dK = static_cast<__nv_bfloat16*>(dk);
+  auto* dV = static_cast<__nv_bfloat16*>(dv);
+  cudaError_t e = timed(plan, SPATTN_K_DELTA, s, [&] {
+    return launch_delta(D, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), plan->d_delta,
+                        bh * plan->q.slots, s);
+  });
+  if (e == cudaSuccess)
+    e = timed(plan, SPATTN_K_DKDV, s, [&] {
+      return launch_dkdv(D, tk, tv, tq, tdo, tile_args(plan, plan->wk, plan->k.slots, plan->q.slots), sc, lse,
+                         plan->d_delta, dK, dV, s);
+    });
+  if (e == cudaSuccess)
+    e = timed(plan, SPATTN_K_DQ, s, [&] {
+      return launch_dq(D, static_cast<const __nv_bfloat16*>(q), tdo, tk, tv, tile_args(plan, plan->wq, plan->q.slots, plan->k.slots), sc,
+                       lse, plan->d_delta, dQ, s);
+    });
+  if (e == cudaSuccess && !plan->k_fill.empty())
+    e = timed(plan, SPATTN_K_FILL, s, [&] {
+      return launch_fill(D, plan->d_k_fill, static_cast<int64_t>(plan->k_fill.size() / 2), bh_kv, plan->k.slots, dK,
+                         dV, nullptr, s);
+    });
+  if (e == cudaSuccess && !plan->q_fill.empty())
+    e = timed(plan, SPATTN_K_FILL, s, [&] {
+      return launch_fill(D, plan->d_q_fill, static_cast<int64_t>(plan->q_fill.size() / 2), bh, plan->q.slots, dQ,
+                         nullptr, nullptr, s);
+    });
+  return e == cudaSuccess ? SPATTN_OK : SPATTN_ERR_CUDA;
+}
+
 }  // namespace
 
 // Entry points for other translation units of the library.
@@ -203,28 +300,17 @@ int spattn_plan(const spattn_layout* layout, const spattn_graph* graph, spattn_p
 }
 
 int spattn_fwd(const void* q, const void* k, const void* v, spattn_plan_t plan, void* o, float* lse, void* stream) {
+  return run_fwd(q, k, v, plan, nullptr, o, lse, stream);
+}
+
+int spattn_fwd_scored(const void* q, const void* k, const void* v, spattn_plan_t plan, const spattn_score* score,
+                      void* o, float* lse, void* stream) {
   if (!plan) return SPATTN_ERR_INVALID_ARG;
-  int st = check_plan_device(plan);
+  ScoreArgs sc;
+  bool any = false;
+  const int st = score_args(plan, score, &sc, &any);
   if (st) return st;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return SPATTN_ERR_INVALID_ARG;
-  const int D = plan->head_dim;
-  const int64_t bh = static_cast<int64_t>(plan->batch) * plan->heads;
-  const int64_t bh_kv = static_cast<int64_t>(plan->batch) * plan->kv_heads;
-  TmaPages tq, tk, tv;
-  if (!make_pages(&tq, q, D, plan->q.slots, bh) || !make_pages(&tk, k, D, plan->k.slots, bh_kv) ||
-      !make_pages(&tv, v, D, plan->k.slots, bh_kv))
-    return SPATTN_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  auto* O = static_cast<__nv_bfloat16*>(o);
-  cudaError_t e = timed(plan, SPATTN_K_FWD, s, [&] {
-    return launch_fwd(D, tq, tk, tv, tile_args(plan, plan->wq, plan->q.slots, plan->k.slots), O, lse, s);
-  });
-  if (e == cudaSuccess && !plan->q_fill.empty())
-    e = timed(plan, SPATTN_K_FILL, s, [&] {
-      return launch_fill(D, plan->d_q_fill, static_cast<int64_t>(plan->q_fill.size() / 2), bh, plan->q.slots, O,
-                         nullptr, lse, s);
-    });
-  return e == cudaSuccess ? SPATTN_OK : SPATTN_ERR_CUDA;
+  return run_fwd(q, k, v, plan, any ? &sc : nullptr, o, lse, stream);
 }
 
 int spattn_quantize_fp8(const void* x, int64_t bh, int64_t rows, int head_dim, void* x8, float* descale,
@@ -270,48 +356,17 @@ int spattn_fwd_fp8(const void* q8, const void* k8, const float* q_descale, const
 
 int spattn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
                spattn_plan_t plan, void* dq, void* dk, void* dv, void* stream) {
+  return run_bwd(q, k, v, o, lse, d_o, plan, nullptr, dq, dk, dv, stream);
+}
+
+int spattn_bwd_scored(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
+                      spattn_plan_t plan, const spattn_score* score, void* dq, void* dk, void* dv, void* stream) {
   if (!plan) return SPATTN_ERR_INVALID_ARG;
-  int st = check_plan_device(plan);
+  ScoreArgs sc;
+  bool any = false;
+  const int st = score_args(plan, score, &sc, &any);
   if (st) return st;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(d_o) ||
-      !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
-    return SPATTN_ERR_INVALID_ARG;
-  const int D = plan->head_dim;
-  const int64_t bh = static_cast<int64_t>(plan->batch) * plan->heads;
-  const int64_t bh_kv = static_cast<int64_t>(plan->batch) * plan->kv_heads;
-  TmaPages tq, tk, tv, tdo;
-  if (!make_pages(&tq, q, D, plan->q.slots, bh) || !make_pages(&tk, k, D, plan->k.slots, bh_kv) ||
-      !make_pages(&tv, v, D, plan->k.slots, bh_kv) || !make_pages(&tdo, d_o, D, plan->q.slots, bh))
-    return SPATTN_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  auto* dQ = static_cast<__nv_bfloat16*>(dq);
-  auto* dK = static_cast<__nv_bfloat16*>(dk);
-  auto* dV = static_cast<__nv_bfloat16*>(dv);
-  cudaError_t e = timed(plan, SPATTN_K_DELTA, s, [&] {
-    return launch_delta(D, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), plan->d_delta,
-                        bh * plan->q.slots, s);
-  });
-  if (e == cudaSuccess)
-    e = timed(plan, SPATTN_K_DKDV, s, [&] {
-      return launch_dkdv(D, tk, tv, tq, tdo, tile_args(plan, plan->wk, plan->k.slots, plan->q.slots), lse,
-                         plan->d_delta, dK, dV, s);
-    });
-  if (e == cudaSuccess)
-    e = timed(plan, SPATTN_K_DQ, s, [&] {
-      return launch_dq(D, static_cast<const __nv_bfloat16*>(q), tdo, tk, tv, tile_args(plan, plan->wq, plan->q.slots, plan->k.slots), lse,
-                       plan->d_delta, dQ, s);
-    });
-  if (e == cudaSuccess && !plan->k_fill.empty())
-    e = timed(plan, SPATTN_K_FILL, s, [&] {
-      return launch_fill(D, plan->d_k_fill, static_cast<int64_t>(plan->k_fill.size() / 2), bh_kv, plan->k.slots, dK,
-                         dV, nullptr, s);
-    });
-  if (e == cudaSuccess && !plan->q_fill.empty())
-    e = timed(plan, SPATTN_K_FILL, s, [&] {
-      return launch_fill(D, plan->d_q_fill, static_cast<int64_t>(plan->q_fill.size() / 2), bh, plan->q.slots, dQ,
-                         nullptr, nullptr, s);
-    });
-  return e == cudaSuccess ? SPATTN_OK : SPATTN_ERR_CUDA;
+  return run_bwd(q, k, v, o, lse, d_o, plan, any ? &sc : nullptr, dq, dk, dv, stream);
 }
 
 int spattn_wait_selftest(spattn_plan_t plan, int64_t deadline_cycles, void* stream) {

@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "kernels.cuh"
+#include "score.cuh"
 #include "tile.cuh"
 
 namespace spattn {
@@ -115,6 +116,8 @@ struct DkvCfg {
   static constexpr int kQStages = (D == 128) ? 4 : 6;
   static constexpr int kDStages = (D == 128) ? 4 : 6;
   static constexpr int kSmem = 2 * kTile + (kQStages + kDStages) * (kStageTile + kAugStage) + kOnesBytes + 1024 + 512;
+  // scored form: each row warp's lines of 32 column LSEs and positions
+  static constexpr int kScoreBytes = 8 * 2 * 32 * 4;
 };
 
 // 12 warps: 0 and 11 = TMA producers, 1 = TMEM owner and issuer of the MMAs
@@ -148,7 +151,11 @@ constexpr int kItemQueue = 4;
 // readers of a queue slot: warps 1, 10, 11 and the 8 row-thread warps
 constexpr int kItemReaders = 11;
 
-template <int D>
+// SC: the form whose scores are modified (score.cuh).  A cap has to be applied
+// to the bare products, so LSE is not folded into S^T there: the row threads
+// read it per column, with the columns' positions, from their warp's lines in
+// shared memory (the Delta slice stays).
+template <int D, bool SC>
 __global__ void __launch_bounds__(kDkvThreads, 1)
     dkdv_kernel(const __grid_constant__ TmaPages tm_k, const __grid_constant__ TmaPages tm_v,
                 const __grid_constant__ TmaPages tm_q, const __grid_constant__ TmaPages tm_do,
@@ -156,7 +163,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 const int32_t* __restrict__ col_pages, const uint64_t* __restrict__ col_masks,
                 const float* __restrict__ lse, const float* __restrict__ delta, __nv_bfloat16* __restrict__ out_dk,
                 __nv_bfloat16* __restrict__ out_dv, int64_t kv_slots, int64_t q_slots, float sl2, float scale,
-                int heads, int kv_heads, int kv_group, const uint16_t* __restrict__ col_heads, int* err) {
+                int heads, int kv_heads, int kv_group, const uint16_t* __restrict__ col_heads, int* err,
+                const ScoreArgs sc) {
   using C = DkvCfg<D>;
   constexpr int QS = C::kQStages, DS = C::kDStages, NP = kBwdStepPages, SP = C::kStagePages;
   static_assert(SP == NP, "one MMA step per stage");
@@ -422,7 +430,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         for (int kk = 0; kk < D / 16; ++kk)
           umma_ss_w(tmem, sdesc_add(dk0, (kk >> 2) * kChunkBytes + (kk & 3) * 32),
                     sdesc_add(bq, (kk >> 2) * kStageChunk + (kk & 3) * 32), idesc_s, kk > 0);
-        umma_ss_w(tmem, d_ones, sdesc_add(d_qa, qs * kAugStage), idesc_s, 1u);
+        if constexpr (!SC) umma_ss_w(tmem, d_ones, sdesc_add(d_qa, qs * kAugStage), idesc_s, 1u);
         if (!__all_sync(0xffffffffu, mbar_wait(&do_full[ds], (G / DS) & 1, ab))) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
@@ -481,7 +489,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const int q4 = warp & 3;
     const int row = q4 * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+    // scored form: the scores are in log2 units by then
+    const uint64_t sl2x2 = SC ? f2_pack(1.f, 1.f) : f2_pack(sl2, sl2);
     int G = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -494,6 +503,42 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       const int seg = code < 8 ? static_cast<int>(code) : -1;
       StepMasks<NP> raw;
       if (n_steps > 0) raw.fetch(col_masks, wk.e0, min(NP, n_cols), seg);
+      // scored form: lane l holds column 32 grp + l of the step, loaded a step
+      // ahead (its page reference and head two ahead)
+      float* col_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512) + 64 * (warp - 2);
+      float* col_pos = col_lse + 32;
+      QueryCol qc;
+      int32_t ref = 0;
+      int ref_h = 0, key_pos = 0, key_doc = -1;
+      auto col_ref = [&](int st) {
+        const int e = st * NP + 2 * grp + (lane >> 4);
+        ref = e < n_cols ? __ldg(col_pages + wk.e0 + e) : 0;
+        ref_h = (e < n_cols && col_heads) ? static_cast<int>(__ldg(col_heads + wk.e0 + e)) : 0;
+      };
+      auto col_load = [&](int st) {
+        const int64_t slot = pref_slot(ref, lane & 15);
+        const int bi = wk.bh / kv_heads;
+        const int h = (wk.bh % kv_heads) * kv_group + ref_h;
+        const int64_t off = bi * sc.q_batch + slot;
+        qc.live = st * NP + 2 * grp + (lane >> 4) < n_cols && slot < q_slots;
+        qc.last = (qc.live && sc.q_last) ? __ldg(sc.q_last + off) : 0;
+        qc.doc = (qc.live && sc.q_doc) ? __ldg(sc.q_doc + off) : -1;
+        qc.pos = (qc.live && sc.slopes) ? static_cast<float>(__ldg(sc.q_pos + off)) : 0.f;
+        qc.slope2 = sc.slopes ? __ldg(sc.slopes + h) * kLog2e : 0.f;
+        // a column behind the list: P = 0 whatever its score
+        qc.lse2 = qc.live ? __ldg(lse + (static_cast<int64_t>(bi) * heads + h) * q_slots + slot) * kLog2e : INFINITY;
+      };
+      if constexpr (SC) {
+        const int64_t slot = row < 16 * wk.n_own ? pref_slot(wk.own_page(row >> 4), row & 15) : kv_slots;
+        if (slot < kv_slots) {
+          const int64_t off = (wk.bh / kv_heads) * sc.k_batch + slot;
+          if (sc.k_pos) key_pos = __ldg(sc.k_pos + off);
+          if (sc.k_doc) key_doc = __ldg(sc.k_doc + off);
+        }
+        col_ref(0);
+        col_load(0);
+        col_ref(1);
+      }
       for (int st = 0; st < n_steps; ++st, ++G) {
         const int b = G & 1;
         const int N = 16 * min(NP, n_cols - st * NP);
@@ -502,6 +547,32 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         raw.bits(mw);
         // mask words of the next step load while this one computes
         if (st + 1 < n_steps) raw.fetch(col_masks, wk.e0 + (st + 1) * NP, min(NP, n_cols - (st + 1) * NP), seg);
+        float slope_lo = 0.f, slope_hi = 0.f;
+        if constexpr (SC) {
+          if (sc.q_last || sc.q_doc) {
+            QueryRange rg;
+            rg.of(qc);
+            const bool none = seg < 0 || (sc.q_last && key_pos > rg.last_max) ||
+                              (sc.q_doc && (key_doc < 0 || key_doc < rg.doc_min || key_doc > rg.doc_max));
+            const bool all = (!sc.q_last || key_pos <= rg.last_min) && (!sc.q_doc || rg.doc_min == rg.doc_max);
+            if (none) mw[0] = mw[1] = 0u;
+            if (__any_sync(0xffffffffu, !none && !all)) {
+              const uint32_t bits = query_bits(qc, sc.q_last, key_pos, sc.q_doc, key_doc);
+              mw[0] &= bits;
+              mw[1] &= bits;
+            }
+          }
+          __syncwarp();
+          col_lse[lane] = qc.lse2;
+          col_pos[lane] = qc.pos;
+          __syncwarp();
+          slope_lo = __shfl_sync(0xffffffffu, qc.slope2, 0);
+          slope_hi = __shfl_sync(0xffffffffu, qc.slope2, 16);
+          if (st + 1 < n_steps) {
+            col_load(st + 1);
+            col_ref(st + 2);
+          }
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(st_full, G & 1, ab));
         if (!ok) break;
         tc_fence_after();
@@ -515,6 +586,16 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         mbar_arrive(st_free);
         // a = S^T - LSE/scale, d = dP^T - Delta (fp32, from the augmented MMAs)
         uint32_t pp[16], pd[16];
+        if constexpr (SC) {
+          if (active) {
+            // a = S^T: z in log2 units less LSE, so that log2 P^T = a below
+            if (sc.cap > 0.f) cap_scores<true>(a, d, scale / sc.cap, sc.cap * kLog2e);
+            if (sc.slopes)
+              bias_scores(a, col_pos, static_cast<float>(key_pos), sc.cap > 0.f ? 1.0f : sl2, slope_lo, slope_hi);
+            const float mul = (sc.cap > 0.f || sc.slopes) ? 1.0f : sl2;
+            sub_columns(a, col_lse, mul);
+          }
+        }
         if (active) {
           const uint32_t m = grp ? mw[1] : mw[0];
           if (m == 0xFFFFFFFFu) {
@@ -547,7 +628,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                         s1);
               pp[i] = pack_bf16(p0, p1);
               // masked entries: p = 0 exactly, so dS = 0 unless dP - Delta is not finite
-              pd[i] = pack_bf16(p0 != 0.f ? s0 : 0.f, p1 != 0.f ? s1 : 0.f);
+              if constexpr (SC)
+                pd[i] = pack_bf16(live_weight(p0) ? s0 : 0.f, live_weight(p1) ? s1 : 0.f);
+              else
+                pd[i] = pack_bf16(p0 != 0.f ? s0 : 0.f, p1 != 0.f ? s1 : 0.f);
             }
           }
         }
@@ -623,16 +707,19 @@ struct DqCfg {
   static constexpr int kKStages = (D == 128) ? 3 : 5;
   static constexpr int kVStages = (D == 128) ? 3 : 5;
   static constexpr int kSmem = kTile + (kKStages + kVStages) * kStageTile + 1024 + 512;
+  // scored form: each row warp's line of 32 column positions
+  static constexpr int kScoreBytes = 8 * 32 * 4;
 };
 
-template <int D>
+// SC: the form whose scores are modified (score.cuh).
+template <int D, bool SC>
 __global__ void __launch_bounds__(kDkvThreads, 1)
     dq_kernel(const __nv_bfloat16* __restrict__ q, const __grid_constant__ TmaPages tm_do,
               const __grid_constant__ TmaPages tm_k, const __grid_constant__ TmaPages tm_v,
               const int32_t* __restrict__ work, const int32_t* __restrict__ col_pages,
               const uint64_t* __restrict__ col_masks, const float* __restrict__ lse, const float* __restrict__ delta,
               __nv_bfloat16* __restrict__ out_dq, int64_t q_slots, float sl2, float scale, int heads, int kv_group,
-              int* err) {
+              int* err, const ScoreArgs sc, int64_t kv_slots) {
   using C = DqCfg<D>;
   constexpr int KS = C::kKStages, VS = C::kVStages, NP = kBwdStepPages, SP = C::kStagePages;
   constexpr int SPS = SP / NP;  // steps per stage
@@ -836,12 +923,42 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     }
     const float lse2 = (valid_slot && seg >= 0) ? __ldg(lse + roff) * kLog2e : 0.f;
     const float dl = (valid_slot && seg >= 0) ? __ldg(delta + roff) : 0.f;
-    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+    // after the cap or the bias the scores are in log2 units already
+    const float mul = SC && (sc.cap > 0.f || sc.slopes) ? 1.0f : sl2;
+    const uint64_t sl2x2 = f2_pack(mul, mul);
     const uint64_t nl2 = f2_pack(-lse2, -lse2);
-    const uint64_t ndl = f2_pack(-dl, -dl);
+    const float dl_left = SC && sc.cap > 0.f ? 0.f : dl;  // a cap's gradient has taken Delta off already
+    const uint64_t ndl = f2_pack(-dl_left, -dl_left);
     bool ok = true;
     StepMasks<NP> raw;
     if (n_steps > 0) raw.fetch(col_masks, wk.e0, min(NP, n_cols), seg);
+    // scored form: lane l holds column 32 grp + l of the step, loaded a step
+    // ahead (its page reference two ahead)
+    float* col_pos = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512) + 32 * (warp - 2);
+    KeyCol kc;
+    int32_t ref = 0;
+    RowRule rule{0, 0};
+    float row_pos = 0.f, slope2 = 0.f;
+    auto col_ref = [&](int st) {
+      const int e = st * NP + 2 * grp + (lane >> 4);
+      return e < n_cols ? __ldg(col_pages + wk.e0 + e) : 0;
+    };
+    auto col_load = [&](int st) {
+      return load_key_col(sc, (wk.bh / heads) * sc.k_batch, st * NP + 2 * grp + (lane >> 4) < n_cols, ref, lane & 15,
+                          kv_slots);
+    };
+    if constexpr (SC) {
+      if (loaded) {
+        const int64_t off = (wk.bh / heads) * sc.q_batch + slot;
+        if (sc.q_last) rule.last = __ldg(sc.q_last + off);
+        if (sc.q_doc) rule.doc = __ldg(sc.q_doc + off);
+        if (sc.slopes) row_pos = static_cast<float>(__ldg(sc.q_pos + off));
+      }
+      if (sc.slopes) slope2 = __ldg(sc.slopes + wk.bh % heads) * kLog2e;
+      ref = col_ref(0);
+      kc = col_load(0);
+      ref = col_ref(1);
+    }
     for (int st = 0; st < n_steps; ++st) {
       const int b = st & 1;
       const int N = 16 * min(NP, n_cols - st * NP);
@@ -850,6 +967,32 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       raw.bits(mw);
       // mask words of the next step load while this one computes
       if (st + 1 < n_steps) raw.fetch(col_masks, wk.e0 + (st + 1) * NP, min(NP, n_cols - (st + 1) * NP), seg);
+      if constexpr (SC) {
+        if (sc.q_last || sc.q_doc) {
+          ColRange rg;
+          rg.reset();
+          rg.add(kc);
+          rg.reduce();
+          const bool none = seg < 0 || (sc.q_last && rg.pos_min > rule.last) ||
+                            (sc.q_doc && (rule.doc < 0 || rule.doc < rg.doc_min || rule.doc > rg.doc_max));
+          const bool all = (!sc.q_last || rg.pos_max <= rule.last) && (!sc.q_doc || rg.doc_min == rg.doc_max);
+          if (none) mw[0] = mw[1] = 0u;
+          if (__any_sync(0xffffffffu, !none && !all)) {
+            const uint32_t bits = key_bits(kc, sc.q_last, rule.last, sc.q_doc, rule.doc);
+            mw[0] &= bits;
+            mw[1] &= bits;
+          }
+        }
+        if (sc.slopes) {
+          __syncwarp();
+          col_pos[lane] = static_cast<float>(kc.pos);
+          __syncwarp();
+        }
+        if (st + 1 < n_steps) {
+          kc = col_load(st + 1);
+          ref = col_ref(st + 2);
+        }
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(&sd_full[b], (st >> 1) & 1, ab));
       if (!ok) break;
       tc_fence_after();
@@ -862,6 +1005,17 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tc_fence_before();
       mbar_arrive(&s_free[b]);
       uint32_t pd[16];
+      if constexpr (SC) {
+        if (active) {
+          if (sc.cap > 0.f) {
+            // dZ / dX = 1 - tanh^2 goes onto dP - Delta
+#pragma unroll
+            for (int i = 0; i < 32; ++i) d[i] = __float_as_uint(__uint_as_float(d[i]) - dl);
+            cap_scores<true>(a, d, scale / sc.cap, sc.cap * kLog2e);
+          }
+          if (sc.slopes) bias_scores(a, col_pos, row_pos, sc.cap > 0.f ? 1.0f : sl2, slope2, slope2);
+        }
+      }
       if (active) {
         const uint32_t m = grp ? mw[1] : mw[0];
         if (m == 0xFFFFFFFFu) {
@@ -889,7 +1043,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             float g0, g1;
             f2_unpack(f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), ndl)),
                       g0, g1);
-            pd[i] = pack_bf16(p0 != 0.f ? g0 : 0.f, p1 != 0.f ? g1 : 0.f);
+            if constexpr (SC)
+              pd[i] = pack_bf16(live_weight(p0) ? g0 : 0.f, live_weight(p1) ? g1 : 0.f);
+            else
+              pd[i] = pack_bf16(p0 != 0.f ? g0 : 0.f, p1 != 0.f ? g1 : 0.f);
           }
         }
       }
@@ -950,12 +1107,13 @@ cudaError_t launch_delta(int head_dim, const __nv_bfloat16* o, const __nv_bfloat
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool SC>
 static cudaError_t launch_dkdv_t(const TmaPages& tk, const TmaPages& tv, const TmaPages& tq,
-                                 const TmaPages& tdo, const TileArgs& a, const float* lse, const float* delta,
-                                 __nv_bfloat16* dk, __nv_bfloat16* dv, cudaStream_t st) {
+                                 const TmaPages& tdo, const TileArgs& a, const ScoreArgs& sc, const float* lse,
+                                 const float* delta, __nv_bfloat16* dk, __nv_bfloat16* dv, cudaStream_t st) {
   using C = DkvCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  constexpr int kSmem = C::kSmem + (SC ? C::kScoreBytes : 0);
+  cudaError_t e = cudaFuncSetAttribute(dkdv_kernel<D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess || a.n_work == 0) return e;
   // one persistent CTA per SM (at most one item each when there are fewer items)
   int dev = 0, sms = 0;
@@ -964,37 +1122,44 @@ static cudaError_t launch_dkdv_t(const TmaPages& tk, const TmaPages& tv, const T
   if (e == cudaSuccess) e = cudaMemsetAsync(a.sched, 0, sizeof(int), st);
   if (e != cudaSuccess) return e;
   const int64_t grid = std::min<int64_t>(a.n_work, std::max(sms, 1));
-  dkdv_kernel<D><<<static_cast<unsigned>(grid), kDkvThreads, C::kSmem, st>>>(
+  dkdv_kernel<D, SC><<<static_cast<unsigned>(grid), kDkvThreads, kSmem, st>>>(
       tk, tv, tq, tdo, a.work, a.n_work, a.sched, a.pages, a.masks, lse, delta, dk, dv, a.own_slots, a.col_slots,
-      a.scale * kLog2e, a.scale, a.heads, a.kv_heads, a.kv_group, a.col_heads, a.err);
+      a.scale * kLog2e, a.scale, a.heads, a.kv_heads, a.kv_group, a.col_heads, a.err, sc);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool SC>
 static cudaError_t launch_dq_t(const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
-                               const TmaPages& tv, const TileArgs& a, const float* lse, const float* delta,
-                               __nv_bfloat16* dq, cudaStream_t st) {
+                               const TmaPages& tv, const TileArgs& a, const ScoreArgs& sc, const float* lse,
+                               const float* delta, __nv_bfloat16* dq, cudaStream_t st) {
   using C = DqCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  constexpr int kSmem = C::kSmem + (SC ? C::kScoreBytes : 0);
+  cudaError_t e = cudaFuncSetAttribute(dq_kernel<D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess || a.n_work == 0) return e;
-  dq_kernel<D><<<static_cast<unsigned>(a.n_work), kDkvThreads, C::kSmem, st>>>(
+  dq_kernel<D, SC><<<static_cast<unsigned>(a.n_work), kDkvThreads, kSmem, st>>>(
       q, tdo, tk, tv, a.work, a.pages, a.masks, lse, delta, dq, a.own_slots, a.scale * kLog2e, a.scale, a.heads,
-      a.kv_group, a.err);
+      a.kv_group, a.err, sc, a.col_slots);
   return cudaGetLastError();
 }
 
 cudaError_t launch_dkdv(int head_dim, const TmaPages& tk, const TmaPages& tv, const TmaPages& tq, const TmaPages& tdo,
-                        const TileArgs& a, const float* lse, const float* delta, __nv_bfloat16* dk,
-                        __nv_bfloat16* dv, cudaStream_t st) {
-  return head_dim == 128 ? launch_dkdv_t<128>(tk, tv, tq, tdo, a, lse, delta, dk, dv, st)
-                         : launch_dkdv_t<64>(tk, tv, tq, tdo, a, lse, delta, dk, dv, st);
+                        const TileArgs& a, const ScoreArgs* sc, const float* lse, const float* delta,
+                        __nv_bfloat16* dk, __nv_bfloat16* dv, cudaStream_t st) {
+  if (sc)
+    return head_dim == 128 ? launch_dkdv_t<128, true>(tk, tv, tq, tdo, a, *sc, lse, delta, dk, dv, st)
+                           : launch_dkdv_t<64, true>(tk, tv, tq, tdo, a, *sc, lse, delta, dk, dv, st);
+  return head_dim == 128 ? launch_dkdv_t<128, false>(tk, tv, tq, tdo, a, ScoreArgs(), lse, delta, dk, dv, st)
+                         : launch_dkdv_t<64, false>(tk, tv, tq, tdo, a, ScoreArgs(), lse, delta, dk, dv, st);
 }
 
 cudaError_t launch_dq(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
-                      const TmaPages& tv, const TileArgs& a, const float* lse, const float* delta,
-                      __nv_bfloat16* dq, cudaStream_t st) {
-  return head_dim == 128 ? launch_dq_t<128>(q, tdo, tk, tv, a, lse, delta, dq, st)
-                         : launch_dq_t<64>(q, tdo, tk, tv, a, lse, delta, dq, st);
+                      const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, const float* lse,
+                      const float* delta, __nv_bfloat16* dq, cudaStream_t st) {
+  if (sc)
+    return head_dim == 128 ? launch_dq_t<128, true>(q, tdo, tk, tv, a, *sc, lse, delta, dq, st)
+                           : launch_dq_t<64, true>(q, tdo, tk, tv, a, *sc, lse, delta, dq, st);
+  return head_dim == 128 ? launch_dq_t<128, false>(q, tdo, tk, tv, a, ScoreArgs(), lse, delta, dq, st)
+                         : launch_dq_t<64, false>(q, tdo, tk, tv, a, ScoreArgs(), lse, delta, dq, st);
 }
 
 }  // namespace spattn

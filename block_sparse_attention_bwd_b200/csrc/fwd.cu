@@ -26,6 +26,7 @@
 // offsets 0 and 16 (row r of half h at lane 16h + r % 16 + 32 (r / 16)),
 // and two M = 64 P.V products that read P from those lanes.
 #include "kernels.cuh"
+#include "score.cuh"
 #include "tile.cuh"
 
 namespace spattn {
@@ -52,6 +53,8 @@ struct FwdCfg {
   static constexpr int kKStages = (D == 128 && !F8) ? 2 : 4;  // K ring depth
   static constexpr int kVStages = (D == 128) ? 2 : 4;         // V ring depth
   static constexpr int kSmem = kTile + kKStages * kKStage + kVStages * kVStage + 1024 + 512;
+  // scored form: each row warp's line of 64 column positions
+  static constexpr int kScoreBytes = 4 * 64 * 4;
   static_assert(!F8 || D == 128, "the E4M3 forward has D = 128 (one 128-byte row per chunk)");
 };
 
@@ -65,14 +68,16 @@ constexpr int kFwdThreads = 192;
 
 // ROUTE: the form that reads each item's route flag (the 64-row route of
 // Work::halves); without it every item runs as 128 rows over its whole list.
-template <int D, bool F8, bool ROUTE>
+// SC: the form whose scores are modified (score.cuh); its row threads hold
+// the next step's column positions and documents, one or two per lane.
+template <int D, bool F8, bool ROUTE, bool SC>
 __global__ void __launch_bounds__(kFwdThreads, 2)
     fwd_kernel(const __grid_constant__ TmaPages tm_q, const __grid_constant__ TmaPages tm_k,
                const __grid_constant__ TmaPages tm_v, const int32_t* __restrict__ work,
                const int32_t* __restrict__ col_pages, const uint64_t* __restrict__ col_masks,
                __nv_bfloat16* __restrict__ out_o, float* __restrict__ out_lse, int64_t q_slots, float sl2,
                int heads, int kv_group, const float* __restrict__ q_descale, const float* __restrict__ k_descale,
-               int* err) {
+               int* err, const ScoreArgs sc, int64_t kv_slots, float scale) {
   using C = FwdCfg<D, F8>;
   constexpr int KS = C::kKStages, VS = C::kVStages, NP = kFwdStepPages;
   extern __shared__ uint8_t smem_raw[];
@@ -273,11 +278,46 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     const uint32_t code = wk.row_code(row);
     const int seg = code < 8 ? static_cast<int>(code) : -1;
     if constexpr (F8) sl2 *= __ldg(q_descale + wk.bh) * __ldg(k_descale + kv_bh);  // scores of the dequantised Q, K
-    const uint64_t sl2x2 = f2_pack(sl2, sl2);
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     StepMasks<NP> raw;
     if (n_steps > 0) raw.fetch(col_masks, wk.e0, min(NP, n_cols), seg);
+    // scored form: lane l holds columns l and l + 32 of the step, loaded a step
+    // ahead (their page references two ahead)
+    float* col_pos = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512) + 64 * q4;
+    KeyCol kc[2];
+    int32_t ref[2];
+    int64_t kb = 0;
+    RowRule rule{0, 0};
+    float row_pos = 0.f, slope2 = 0.f;
+    auto col_ref = [&](int st, int h) {
+      const int e = st * NP + (lane >> 4) + 2 * h;
+      return e < n_cols ? __ldg(col_pages + wk.e0 + e) : 0;
+    };
+    auto col_load = [&](int st, int h) {
+      return load_key_col(sc, kb, st * NP + (lane >> 4) + 2 * h < n_cols, ref[h], lane & 15, kv_slots);
+    };
+    if constexpr (SC) {
+      const int bi = wk.bh / heads;
+      kb = bi * sc.k_batch;
+      const int64_t slot = row < 16 * wk.n_own ? pref_slot(wk.own_page(row >> 4), row & 15) : q_slots;
+      if (slot < q_slots) {
+        const int64_t off = bi * sc.q_batch + slot;
+        if (sc.q_last) rule.last = __ldg(sc.q_last + off);
+        if (sc.q_doc) rule.doc = __ldg(sc.q_doc + off);
+        if (sc.slopes) row_pos = static_cast<float>(__ldg(sc.q_pos + off));
+      }
+      if (sc.slopes) slope2 = __ldg(sc.slopes + wk.bh % heads) * kLog2e;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ref[h] = col_ref(0, h);
+        kc[h] = col_load(0, h);
+        ref[h] = col_ref(1, h);
+      }
+    }
+    // after the cap or the bias the scores are in log2 units already
+    const float mul = SC && (sc.cap > 0.f || sc.slopes) ? 1.0f : sl2;
+    const uint64_t mul2 = f2_pack(mul, mul);
     for (int st = 0; st < n_steps; ++st) {
       const int b = st & 1;
       // the 64-row route: 32 columns (this half's two pages) in the low half of S
@@ -287,6 +327,38 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       if (halves && hh) mw[0] = mw[1];
       // mask words of the next step load while this one computes
       if (st + 1 < n_steps) raw.fetch(col_masks, wk.e0 + (st + 1) * NP, min(NP, n_cols - (st + 1) * NP), seg);
+      if constexpr (SC) {
+        if (sc.q_last || sc.q_doc) {
+          ColRange rg;
+          rg.reset();
+          rg.add(kc[0]);
+          rg.add(kc[1]);
+          rg.reduce();
+          const bool none = seg < 0 || (sc.q_last && rg.pos_min > rule.last) ||
+                            (sc.q_doc && (rule.doc < 0 || rule.doc < rg.doc_min || rule.doc > rg.doc_max));
+          const bool all = (!sc.q_last || rg.pos_max <= rule.last) && (!sc.q_doc || rg.doc_min == rg.doc_max);
+          if (none) mw[0] = mw[1] = 0u;
+          if (__any_sync(0xffffffffu, !none && !all)) {
+            const uint32_t b0 = key_bits(kc[0], sc.q_last, rule.last, sc.q_doc, rule.doc);
+            const uint32_t b1 = key_bits(kc[1], sc.q_last, rule.last, sc.q_doc, rule.doc);
+            mw[0] &= halves && hh ? b1 : b0;
+            mw[1] &= b1;
+          }
+        }
+        if (sc.slopes) {
+          __syncwarp();
+          col_pos[lane] = static_cast<float>(kc[0].pos);
+          col_pos[lane + 32] = static_cast<float>(kc[1].pos);
+          __syncwarp();
+        }
+        if (st + 1 < n_steps) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            kc[h] = col_load(st + 1, h);
+            ref[h] = col_ref(st + 2, h);
+          }
+        }
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (st >> 1) & 1, ab));
       if (!ok) break;
       tc_fence_after();
@@ -295,6 +367,17 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       for (int pc = 0; pc < 2; ++pc)
         if (pc * 32 < N) tmem_ld32(tmem + 64 * b + lane_off + pc * 32, sr[pc]);
       tmem_wait_ld();
+      if constexpr (SC) {
+#pragma unroll
+        for (int pc = 0; pc < 2; ++pc) {
+          if (pc * 32 < N) {
+            if (sc.cap > 0.f) cap_scores<false>(sr[pc], sr[pc], scale / sc.cap, sc.cap * kLog2e);
+            if (sc.slopes)
+              bias_scores(sr[pc], col_pos + (halves ? 32 * hh : 32 * pc), row_pos, sc.cap > 0.f ? 1.0f : sl2, slope2,
+                          slope2);
+          }
+        }
+      }
       // masked row max over four independent chains
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -314,7 +397,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           }
         }
       }
-      const float mx2 = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * sl2;  // log2 units (scale > 0)
+      const float mx2 = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * mul;  // log2 units (scale > 0)
       const bool resc = mx2 > m_used + kRescaleThreshold;
       const float m_new = resc ? mx2 : m_used;
       const float alpha = resc ? ex2(m_used - m_new) : 1.0f;
@@ -334,7 +417,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[pc][2 * i]), __uint_as_float(sr[pc][2 * i + 1])), sl2x2, nmu2),
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[pc][2 * i]), __uint_as_float(sr[pc][2 * i + 1])), mul2, nmu2),
                         x0, x1);
               const float p0 = ex2(x0), p1 = ex2(x1);
               ls2[i & 1] = f2_add(ls2[i & 1], f2_pack(p0, p1));
@@ -429,41 +512,48 @@ __global__ void fill_kernel(const int32_t* __restrict__ fill, int64_t n_bh, int6
   }
 }
 
-template <int D, bool F8, bool ROUTE>
+template <int D, bool F8, bool ROUTE, bool SC>
 cudaError_t launch_fwd_r(const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
-                         __nv_bfloat16* o, float* lse, const float* q_descale, const float* k_descale,
-                         cudaStream_t st) {
+                         const ScoreArgs& sc, __nv_bfloat16* o, float* lse, const float* q_descale,
+                         const float* k_descale, cudaStream_t st) {
   using C = FwdCfg<D, F8>;
+  constexpr int kSmem = C::kSmem + (SC ? C::kScoreBytes : 0);
   cudaError_t e =
-      cudaFuncSetAttribute(fwd_kernel<D, F8, ROUTE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      cudaFuncSetAttribute(fwd_kernel<D, F8, ROUTE, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   if (a.n_work == 0) return cudaSuccess;
-  fwd_kernel<D, F8, ROUTE><<<static_cast<unsigned>(a.n_work), kFwdThreads, C::kSmem, st>>>(
+  fwd_kernel<D, F8, ROUTE, SC><<<static_cast<unsigned>(a.n_work), kFwdThreads, kSmem, st>>>(
       tq, tk, tv, a.work, a.pages, a.masks, o, lse, a.own_slots, a.scale * kLog2e, a.heads, a.kv_group, q_descale,
-      k_descale, a.err);
+      k_descale, a.err, sc, a.col_slots, a.scale);
   return cudaGetLastError();
 }
 
 template <int D, bool F8>
 cudaError_t launch_fwd_t(const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
-                         __nv_bfloat16* o, float* lse, const float* q_descale, const float* k_descale,
-                         cudaStream_t st) {
-  return a.route64 ? launch_fwd_r<D, F8, true>(tq, tk, tv, a, o, lse, q_descale, k_descale, st)
-                   : launch_fwd_r<D, F8, false>(tq, tk, tv, a, o, lse, q_descale, k_descale, st);
+                         const ScoreArgs* sc, __nv_bfloat16* o, float* lse, const float* q_descale,
+                         const float* k_descale, cudaStream_t st) {
+  if constexpr (!F8) {
+    if (sc)
+      return a.route64 ? launch_fwd_r<D, F8, true, true>(tq, tk, tv, a, *sc, o, lse, q_descale, k_descale, st)
+                       : launch_fwd_r<D, F8, false, true>(tq, tk, tv, a, *sc, o, lse, q_descale, k_descale, st);
+  }
+  const ScoreArgs none;
+  return a.route64 ? launch_fwd_r<D, F8, true, false>(tq, tk, tv, a, none, o, lse, q_descale, k_descale, st)
+                   : launch_fwd_r<D, F8, false, false>(tq, tk, tv, a, none, o, lse, q_descale, k_descale, st);
 }
 
 }  // namespace
 
 cudaError_t launch_fwd(int head_dim, const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
-                       __nv_bfloat16* o, float* lse, cudaStream_t st) {
-  return head_dim == 128 ? launch_fwd_t<128, false>(tq, tk, tv, a, o, lse, nullptr, nullptr, st)
-                         : launch_fwd_t<64, false>(tq, tk, tv, a, o, lse, nullptr, nullptr, st);
+                       const ScoreArgs* sc, __nv_bfloat16* o, float* lse, cudaStream_t st) {
+  return head_dim == 128 ? launch_fwd_t<128, false>(tq, tk, tv, a, sc, o, lse, nullptr, nullptr, st)
+                         : launch_fwd_t<64, false>(tq, tk, tv, a, sc, o, lse, nullptr, nullptr, st);
 }
 
 cudaError_t launch_fwd_e4m3(const TmaPages& tq8, const TmaPages& tk8, const TmaPages& tv, const TileArgs& a,
                             const float* q_descale, const float* k_descale, __nv_bfloat16* o, float* lse,
                             cudaStream_t st) {
-  return launch_fwd_t<128, true>(tq8, tk8, tv, a, o, lse, q_descale, k_descale, st);
+  return launch_fwd_t<128, true>(tq8, tk8, tv, a, nullptr, o, lse, q_descale, k_descale, st);
 }
 
 cudaError_t launch_fill(int head_dim, const int32_t* fill, int64_t n, int64_t bh, int64_t slots,

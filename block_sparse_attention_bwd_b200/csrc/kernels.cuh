@@ -50,9 +50,21 @@ struct TileArgs {
   bool route64 = false;
 };
 
-// K1: O, LSE for every query-owned work item.
+// Score modification (spattn_score): device arrays, null where unused.
+struct ScoreArgs {
+  float cap = 0.f;                  // 0: no cap
+  const float* slopes = nullptr;    // [heads]
+  const int32_t* q_pos = nullptr;
+  const int32_t* k_pos = nullptr;
+  const int32_t* q_last = nullptr;
+  const int32_t* q_doc = nullptr;
+  const int32_t* k_doc = nullptr;
+  int64_t q_batch = 0, k_batch = 0;  // elements between batch entries (0: shared)
+};
+
+// K1: O, LSE for every query-owned work item; `sc` (may be null) modifies the scores.
 cudaError_t launch_fwd(int head_dim, const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
-                       __nv_bfloat16* o, float* lse, cudaStream_t st);
+                       const ScoreArgs* sc, __nv_bfloat16* o, float* lse, cudaStream_t st);
 
 // K1 with E4M3 Q and K (head_dim 128): tq8 / tk8 map the one-byte codes (128
 // per 128-byte row), S is scaled by q_descale[bh] * k_descale[kv_bh].
@@ -72,13 +84,13 @@ cudaError_t launch_delta(int head_dim, const __nv_bfloat16* o, const __nv_bfloat
 
 // K3: dK, dV for every key-owned work item.
 cudaError_t launch_dkdv(int head_dim, const TmaPages& tk, const TmaPages& tv, const TmaPages& tq, const TmaPages& tdo,
-                        const TileArgs& a, const float* lse, const float* delta, __nv_bfloat16* dk,
-                        __nv_bfloat16* dv, cudaStream_t st);
+                        const TileArgs& a, const ScoreArgs* sc, const float* lse, const float* delta,
+                        __nv_bfloat16* dk, __nv_bfloat16* dv, cudaStream_t st);
 
 // K4: dQ for every query-owned work item (Q rows are read directly into TMEM).
 cudaError_t launch_dq(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
-                      const TmaPages& tv, const TileArgs& a, const float* lse, const float* delta,
-                      __nv_bfloat16* dq, cudaStream_t st);
+                      const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, const float* lse,
+                      const float* delta, __nv_bfloat16* dq, cudaStream_t st);
 
 // K5: zero the rows that no work item writes (and LSE = -inf).
 // One CTA whose warp 0 waits, with the given deadline, on an mbarrier that

@@ -85,10 +85,10 @@ extern "C" int spattn_bwd_noalloc(const void* q, const void* k, const void* v, c
   cudaError_t e = launch_delta(D, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), delta,
                                bh * plan->q.slots, s);
   if (e == cudaSuccess)
-    e = launch_dkdv(D, tk, tv, tq, tdo, make_tile_args(plan, plan->wk, plan->k.slots, plan->q.slots), lse, delta, dK,
+    e = launch_dkdv(D, tk, tv, tq, tdo, make_tile_args(plan, plan->wk, plan->k.slots, plan->q.slots), nullptr, lse, delta, dK,
                     dV, s);
   if (e == cudaSuccess)
-    e = launch_dq(D, static_cast<const __nv_bfloat16*>(q), tdo, tk, tv, make_tile_args(plan, plan->wq, plan->q.slots, plan->k.slots), lse, delta, dQ, s);
+    e = launch_dq(D, static_cast<const __nv_bfloat16*>(q), tdo, tk, tv, make_tile_args(plan, plan->wq, plan->q.slots, plan->k.slots), nullptr, lse, delta, dQ, s);
   if (e == cudaSuccess && !plan->k_fill.empty())
     e = launch_fill(D, plan->d_k_fill, static_cast<int64_t>(plan->k_fill.size() / 2), bh_kv, plan->k.slots, dK, dV,
                     nullptr, s);

@@ -230,6 +230,83 @@ int spattn_bwd(const void* q, const void* k, const void* v, const void* o, const
 int spattn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, const float* lse,
                        const void* d_o, spattn_plan_t plan, void* dq, void* dk, void* dv, void* stream);
 
+/* Modification of the scores of spattn_fwd_scored / spattn_bwd_scored.  With
+ * x = scale * q_i . k_j, the score of an allowed pair is
+ *   z = softcap * tanh(x / softcap) - slopes[h] * |q_pos[i] - k_pos[j]|
+ * (softcap = 0: no cap; slopes NULL: no bias), and a pair that the plan's graph
+ * allows stays allowed only if
+ *   k_pos[j] <= q_last[i]                 (q_last given), and
+ *   q_doc[i] == k_doc[j] and q_doc[i] >= 0 (q_doc and k_doc given).
+ * q_last = q_pos is a causal mask, q_last = max(q_pos, prefix - 1) one with a
+ * prefix that every query sees; documents are any ids (a negative one attends
+ * and is attended by nothing).  The graph decides which tiles are computed:
+ * it must list every group pair that may hold an allowed pair, and the masks
+ * only narrow it.  All pointers are DEVICE arrays, 4-byte aligned, read on the
+ * call's stream: slopes fp32 [heads] (query heads); q_* int32
+ * [batches, q_slots], k_* int32 [batches, kv_slots].  Positions that a bias
+ * reads must lie within +-2^24 (exact in fp32); masks compare the full int32
+ * range.  Values on padded slots are not used. */
+typedef struct {
+  float softcap;          /* > 0, or 0 for none */
+  const float* slopes;    /* needs q_pos and k_pos */
+  const int32_t* q_pos;
+  const int32_t* k_pos;
+  const int32_t* q_last;  /* needs k_pos */
+  const int32_t* q_doc;   /* both or neither */
+  const int32_t* k_doc;
+  int32_t batches;        /* 1: the arrays serve every batch entry; batch: one row per entry */
+} spattn_score;
+
+/* Forward and backward of the plan's attention with modified scores (above).
+ * Layouts, alignment, outputs of empty rows (O = 0, LSE = -inf, dQ = 0) and
+ * errors are those of spattn_fwd / spattn_bwd; a row that the masks leave
+ * empty counts as empty.  LSE is that of the modified scores, and the backward
+ * takes the O and LSE of spattn_fwd_scored with the same score: with P =
+ * exp(z - LSE) and dZ = P * (dP - Delta), dS = dZ * (1 - tanh^2(x / softcap)).
+ * No gradient of slopes is formed.  Masked K and V rows, like padded ones, may
+ * hold any finite values.  A score that modifies nothing runs the plain
+ * kernels.  (Score caps, distance biases and packed documents have no
+ * counterpart in the paper.) */
+int spattn_fwd_scored(const void* q, const void* k, const void* v, spattn_plan_t plan, const spattn_score* score,
+                      void* o, float* lse, void* stream);
+int spattn_bwd_scored(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
+                      spattn_plan_t plan, const spattn_score* score, void* dq, void* dk, void* dv, void* stream);
+
+/* Layout of a spattn_rope call.  Tensors are [batch, heads, slots, head_dim]
+ * with the strides given (elements; the last dimension is contiguous), so Q
+ * and K may be views of a projection's [batch, slots, heads, head_dim] or of a
+ * packed QKV, on either side. */
+typedef struct {
+  int32_t dtype;          /* 0 bf16, 1 fp16, 2 fp32 (inputs and outputs) */
+  int32_t batch, heads;
+  int32_t kv_heads;       /* heads of K; 0: Q only, k and k_out unused */
+  int32_t head_dim;       /* 1 .. 1024 */
+  int32_t rot_dim;        /* even, <= head_dim: elements turned; the rest is copied */
+  int32_t interleaved;    /* pair p: elements 2p, 2p + 1 (nonzero) or p, p + rot_dim / 2 (0) */
+  int32_t inverse;        /* nonzero: turn by the negative angle (the backward pass) */
+  int64_t slots;
+  int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3]; /* batch, head, slot */
+  int32_t n_axes;         /* position axes, 1 .. 3 */
+  int32_t sections[3];    /* pairs per axis, in pair order; they sum to rot_dim / 2 */
+  int64_t pos_batch_stride; /* elements between batch entries of pos; 0: one set for all */
+  float mscale;           /* factor on the turned elements (1 for none) */
+} spattn_rope_layout;
+
+/* Rotary positions of Q and K in one launch: pair (a, b) of a row becomes
+ * mscale * (a cos t - b sin t, a sin t + b cos t) with t = pos[axis, slot] *
+ * freqs[pair]; freqs (DEVICE fp64 [rot_dim / 2], 8-byte aligned) holds radians
+ * per position, with any scaling for long contexts already in it, and pos
+ * (DEVICE int32 [n_axes, slots] per batch entry) any int32 positions.  Angles are
+ * formed and reduced in fp64, the rotation is fp32, rounded once.  The
+ * gradient of the call is the call on dQ and dK with `inverse` set.  An output
+ * may be its own input (same address and strides) but must not overlap
+ * anything else, and no two of its elements may share an address.  Alignment:
+ * the element size; 16-byte aligned rows are fastest.  Asynchronous on
+ * `stream`, on the current device.  (Rotary positions have no counterpart in
+ * the paper; they make the Q and K that spattn_fwd reads.) */
+int spattn_rope(const spattn_rope_layout* layout, const void* q, const void* k, const int32_t* pos,
+                const double* freqs, void* q_out, void* k_out, void* stream);
+
 /* Synchronise `stream` and report (then clear) any device-side error the
  * plan's kernels recorded: SPATTN_OK, SPATTN_ERR_TIMEOUT or SPATTN_ERR_DEVICE.
  * (Failure reporting; the paper has no counterpart.) */
