@@ -41,6 +41,7 @@ ENTRY_POINTS = (
     "spattn_status_string", "spattn_wait_selftest", "spattn_plan_set_graph_device", "spattn_plan_entry_heads",
     "spattn_quantize_fp8", "spattn_fwd_fp8",
     "spattn_fwd_scored", "spattn_bwd_scored", "spattn_rope",
+    "spattn_paged_create", "spattn_paged_destroy", "spattn_paged_workspace", "spattn_paged_fwd", "spattn_paged_check",
 )
 
 
@@ -73,6 +74,22 @@ class _RopeLayout(ctypes.Structure):
                                                                        "k_out_stride")] + [
         ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3), ("pos_batch_stride", ctypes.c_int64),
         ("mscale", ctypes.c_float)]
+
+
+class _PagedLayout(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads", "kv_heads", "head_dim", "page_slots", "max_seqs", "max_q",
+                                              "max_kv")] + [("scale", ctypes.c_float), ("softcap", ctypes.c_float)]
+
+
+class _PagedCall(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+                ("k_slot_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_slot_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64), ("n_pages", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("n_seqs", ctypes.c_int64),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("slopes", ctypes.c_void_p),
+                ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64)]
 
 
 class _Graph(ctypes.Structure):
@@ -110,6 +127,12 @@ def _lib():
         lib.spattn_fwd_scored.argtypes = [P, P, P, P, ctypes.POINTER(_Score), P, P, P]
         lib.spattn_bwd_scored.argtypes = [P, P, P, P, P, P, P, ctypes.POINTER(_Score), P, P, P, P]
         lib.spattn_rope.argtypes = [ctypes.POINTER(_RopeLayout), P, P, P, P, P, P, P]
+        lib.spattn_paged_create.argtypes = [ctypes.POINTER(_PagedLayout), ctypes.POINTER(P)]
+        lib.spattn_paged_workspace.argtypes = [P, I64, ctypes.POINTER(I64)]
+        lib.spattn_paged_fwd.argtypes = [P, ctypes.POINTER(_PagedCall), P]
+        lib.spattn_paged_check.argtypes = [P, P]
+        lib.spattn_paged_destroy.argtypes = [P]
+        lib.spattn_paged_destroy.restype = None
         lib.spattn_quantize_fp8.argtypes = [P, I64, I64, ctypes.c_int, P, P, P]
         lib.spattn_fwd_fp8.argtypes = [P, P, P, P, P, P, P, P, P]
         lib.spattn_bwd_noalloc.argtypes = [P, P, P, P, P, P, P, P, P, P, P]
@@ -131,7 +154,7 @@ def _lib():
         lib.spattn_status_string.argtypes = [ctypes.c_int]
         lib.spattn_status_string.restype = ctypes.c_char_p
         for name in ENTRY_POINTS:
-            if name not in ("spattn_plan_destroy", "spattn_status_string"):
+            if name not in ("spattn_plan_destroy", "spattn_paged_destroy", "spattn_status_string"):
                 getattr(lib, name).restype = ctypes.c_int
         _LIB = lib
     return _LIB
@@ -592,6 +615,119 @@ def rope_bwd(dq_out, dk_out, pos, freqs, *, rot_dim=None, interleaved=False, sec
              dk=None, stream=None):
     """Gradient of :func:`rope`: dQ and dK of its inputs from those of its outputs (same arguments)."""
     return _rope("rope_bwd", True, dq_out, dk_out, pos, freqs, rot_dim, interleaved, sections, mscale, dq, dk, stream)
+
+
+class PagedPlan:
+    """Owning wrapper of ``spattn_paged_t``: the bounds of paged attention calls.
+
+    ``page_slots``: slots per page (a multiple of 16); ``max_seqs``, ``max_q`` (new
+    tokens of one sequence; 1 for decoding) and ``max_kv`` (cache slots of one
+    sequence) bound every call; ``softcap`` and ``slopes`` (fp32 [heads] on the GPU)
+    modify the scores as in :class:`Score`.  Lives on the current CUDA device.
+    """
+
+    def __init__(self, *, heads, kv_heads, head_dim, page_slots, max_seqs, max_q, max_kv, scale=0.0, softcap=0.0,
+                 slopes=None):
+        import torch
+
+        lay = _PagedLayout(heads, kv_heads, head_dim, page_slots, max_seqs, max_q, max_kv, float(scale), float(softcap))
+        h = ctypes.c_void_p()
+        _check(_lib().spattn_paged_create(ctypes.byref(lay), ctypes.byref(h)), "spattn_paged_create")
+        self.handle = h
+        self.heads, self.kv_heads, self.head_dim, self.page_slots = heads, kv_heads, head_dim, page_slots
+        self.max_seqs, self.max_q, self.max_kv = max_seqs, max_q, max_kv
+        if slopes is not None:
+            _need(slopes, "slopes", (heads,), torch.float32)
+        self.slopes = slopes
+        self._bytes = {}
+
+    def workspace_bytes(self, n_seqs: int) -> int:
+        """Bytes of workspace of a call with ``n_seqs`` sequences."""
+        if n_seqs not in self._bytes:
+            n = ctypes.c_int64()
+            _check(_lib().spattn_paged_workspace(self.handle, n_seqs, ctypes.byref(n)), "spattn_paged_workspace")
+            self._bytes[n_seqs] = n.value
+        return self._bytes[n_seqs]
+
+    def close(self):
+        if getattr(self, "handle", None) is not None and self.handle.value:
+            _lib().spattn_paged_destroy(self.handle)
+            self.handle = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def spattn_paged_fwd(q, k_cache, v_cache, page_table, q_start, kv_len, paged: PagedPlan, o=None, lse=None,
+                     workspace=None, stream=None):
+    """Attention of each sequence's new tokens over a paged cache; returns O [T, H, D] bf16 and LSE [T, H] fp32.
+
+    ``q`` [T, H, D] bf16 (token and head strides free); ``k_cache`` / ``v_cache``
+    [pages, page_slots, kv_heads, D] bf16, or a permuted view of [kv_heads, slots, D];
+    ``page_table`` int32 [n, P]; ``q_start`` int32 [n + 1]; ``kv_len`` int32 [n], the new
+    tokens included.  Rows of o and lse that no sequence names are left as they are
+    (undefined in the tensors that the call makes itself).  ``workspace``: a uint8
+    CUDA tensor of ``paged.workspace_bytes(n)`` bytes; by default the call allocates one.
+    """
+    import torch
+
+    H, Hk, D, ps = paged.heads, paged.kv_heads, paged.head_dim, paged.page_slots
+    dev = q.device
+    if not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[1] != H or q.shape[2] != D \
+            or q.stride(2) != 1:
+        raise ValueError(f"q: expected a CUDA bf16 tensor [tokens, {H}, {D}], contiguous in its last dimension")
+    T = q.shape[0]
+    strides = []
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.device != dev or t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape[1:] != (ps, Hk, D) \
+                or t.stride(3) != 1 or t.shape[0] != k_cache.shape[0]:
+            raise ValueError(f"{name}: expected a bf16 tensor [pages, {ps}, {Hk}, {D}] on {dev}, contiguous in its "
+                             "last dimension")
+        if t.shape[0] > 1 and t.stride(0) != ps * t.stride(1):
+            raise ValueError(f"{name}: pages must follow each other (page stride = {ps} slot strides)")
+        strides += [t.stride(1), t.stride(2) if Hk > 1 else 0]
+    n = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    if page_table.dim() != 2 or page_table.shape[0] != n:
+        raise ValueError(f"page_table: expected an int32 tensor [{max(n, 0)}, pages]")
+    for t, name, shape in ((page_table, "page_table", tuple(page_table.shape)), (q_start, "q_start", (n + 1,)),
+                           (kv_len, "kv_len", (n,))):
+        _need(t, name, shape, torch.int32)
+        _same_device(t, name, dev)
+    if paged.slopes is not None:
+        _same_device(paged.slopes, "slopes", dev)
+    if o is None:
+        o = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(o, "o", (T, H, D), torch.bfloat16)
+        _same_device(o, "o", dev)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", (T, H), torch.float32)
+        _same_device(lse, "lse", dev)
+    need = paged.workspace_bytes(n)
+    if workspace is None:
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            if stream is not None:
+                workspace.record_stream(stream)
+    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous uint8 tensor on {dev}")
+    c = _PagedCall(q.data_ptr(), q.stride(0), q.stride(1), T, k_cache.data_ptr(), v_cache.data_ptr(), *strides,
+                   k_cache.shape[0], page_table.data_ptr(), page_table.shape[1], n, q_start.data_ptr(),
+                   kv_len.data_ptr(), None if paged.slopes is None else paged.slopes.data_ptr(), o.data_ptr(),
+                   lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+                   0 if workspace is None else workspace.numel())
+    _check(_lib().spattn_paged_fwd(paged.handle, ctypes.byref(c), _stream_handle(stream)), "spattn_paged_fwd")
+    return o, lse
+
+
+def spattn_paged_check(paged: PagedPlan, stream=None):
+    """Synchronise the stream and raise if a paged call recorded a device-side error."""
+    _check(_lib().spattn_paged_check(paged.handle, _stream_handle(stream)), "spattn_paged_check")
 
 
 def spattn_check(plan: Plan, stream=None):

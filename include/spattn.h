@@ -307,6 +307,76 @@ typedef struct {
 int spattn_rope(const spattn_rope_layout* layout, const void* q, const void* k, const int32_t* pos,
                 const double* freqs, void* q_out, void* k_out, void* stream);
 
+/* Attention over a paged cache.
+ *
+ * The cache is a pool of n_pages pages of page_slots slots; slot s of page p is
+ * row p * page_slots + s of k_cache / v_cache, bf16, found at
+ * row * slot_stride + kv_head * head_stride (elements), so a pool may be
+ * [pages, page_slots, kv_heads, head_dim] or [kv_heads, slots, head_dim].
+ * page_table[i][j] names the page of slots j * page_slots .. of sequence i.
+ * The new tokens of sequence i are rows q_start[i] .. q_start[i + 1] of q and
+ * are the last ones of its kv_len[i] cache slots (their K and V are in the
+ * cache already): new token t of n stands at position kv_len - n + t and
+ * attends the slots up to its own.  Scores are those of spattn_score: a tanh
+ * cap and, with slopes, a bias of -slopes[h] * distance.  Query head h reads
+ * K/V head h / (heads / kv_heads). */
+typedef struct spattn_paged_s* spattn_paged_t; /* opaque, owned by the library */
+
+typedef struct {
+  int32_t heads, kv_heads; /* heads % kv_heads == 0 */
+  int32_t head_dim;        /* 64 or 128 */
+  int32_t page_slots;      /* multiple of 16 */
+  int32_t max_seqs;        /* bounds of any call: sequences, */
+  int32_t max_q;           /* new tokens of one sequence (1: decoding), */
+  int32_t max_kv;          /* cache slots of one sequence (>= max_q) */
+  float scale;             /* softmax scale > 0; 0 selects 1/sqrt(head_dim) */
+  float softcap;           /* > 0, or 0 for none */
+} spattn_paged_layout;
+
+/* Everything of one call; all pointers are DEVICE pointers.  Lengths and tables
+ * are read on the stream, so a captured call may be replayed with new ones. */
+typedef struct {
+  const void* q;           /* bf16 rows [tokens, heads, head_dim], 16-byte aligned, */
+  int64_t q_token_stride, q_head_stride; /* strides in elements, multiples of 8 */
+  int64_t tokens;          /* rows of q, o and lse; rows no sequence names are left as they are */
+  const void* k_cache;     /* 16-byte aligned, strides multiples of 8 */
+  const void* v_cache;
+  int64_t k_slot_stride, k_head_stride, v_slot_stride, v_head_stride;
+  int64_t n_pages;         /* n_pages * page_slots < 2^31 */
+  const int32_t* page_table; /* [n_seqs, table_stride] */
+  int64_t table_stride;
+  int64_t n_seqs;          /* <= max_seqs */
+  const int32_t* q_start;  /* [n_seqs + 1], non-decreasing */
+  const int32_t* kv_len;   /* [n_seqs] */
+  const float* slopes;     /* fp32 [heads], or NULL */
+  void* o;                 /* bf16 [tokens, heads, head_dim], contiguous, 16-byte aligned */
+  float* lse;              /* fp32 [tokens, heads] (natural log), or NULL */
+  void* workspace;         /* spattn_paged_workspace bytes, 16-byte aligned; not shared by calls in flight */
+  int64_t workspace_bytes;
+} spattn_paged_call;
+
+/* Create a handle on the current device (on a machine without one, for checks
+ * and workspace sizes only).  The handle holds the bounds and a device error
+ * word, no per-call state: calls on several streams may overlap if each has its
+ * own workspace. */
+int spattn_paged_create(const spattn_paged_layout* layout, spattn_paged_t* out);
+/* The caller makes sure that no call is still running (NULL is a no-op). */
+void spattn_paged_destroy(spattn_paged_t paged);
+/* Bytes of workspace of a call with n_seqs sequences (0: none needed).  It holds
+ * the partial rows of long caches that are split over CTAs. */
+int spattn_paged_workspace(spattn_paged_t paged, int64_t n_seqs, int64_t* bytes);
+/* One call (one kernel, and a second that joins split rows).  A sequence whose
+ * lengths leave the bounds, whose rows leave q, whose cache is shorter than
+ * its new tokens or longer than its table is skipped, and a page outside the
+ * pool is read as page 0; both are reported by spattn_paged_check.  Cache slots
+ * behind kv_len may hold anything, NaN included.  (The paper has no
+ * counterpart; pages are gathered as the KPage abstract's 16-row pages are,
+ * zhuanzhiai.com paper page.) */
+int spattn_paged_fwd(spattn_paged_t paged, const spattn_paged_call* call, void* stream);
+/* As spattn_check, for the handle's calls: SPATTN_ERR_DEVICE for a rejected
+ * sequence or page, SPATTN_ERR_TIMEOUT for a wait that ran out. */
+int spattn_paged_check(spattn_paged_t paged, void* stream);
+
 /* Synchronise `stream` and report (then clear) any device-side error the
  * plan's kernels recorded: SPATTN_OK, SPATTN_ERR_TIMEOUT or SPATTN_ERR_DEVICE.
  * (Failure reporting; the paper has no counterpart.) */
