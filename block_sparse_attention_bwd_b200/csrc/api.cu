@@ -186,6 +186,31 @@ TileArgs tile_args(const spattn_plan_s* P, const WorkList& w, int64_t own_slots,
   return a;
 }
 
+}  // namespace
+
+// tanh(u) / u = 1 + v (t1 + t2 v + t3 v^2 + t4 v^3), v = u^2: minimax on
+// |u| <= 1/2 (relative error 1.5e-8), with u = scale s / c put in.
+CapArgs cap_args(float cap, float scale) {
+  CapArgs r{};
+  if (!(cap > 0.f)) return r;
+  constexpr double kLog2E = 1.4426950408889634, t[5] = {1.0, -0.33333149552345276, 0.1332598626613617,
+                                                        -0.05305291339755058, 0.017256902530789375};
+  const double k = static_cast<double>(scale) / cap, cap2 = cap * kLog2E;
+  double p = cap2 * k;
+  bool fits = true;
+  for (int i = 0; i < 5; ++i, p *= k * k) {
+    r.a[i] = static_cast<float>(t[i] * p);
+    fits = fits && std::fabs(t[i] * p) < 1e30;
+  }
+  r.w_max = fits ? static_cast<float>(0.25 / (k * k)) : -1.f;  // never the polynomial where a coefficient overflows
+  r.k2 = static_cast<float>(2 * kLog2E * k);
+  r.cap2 = static_cast<float>(cap2);
+  r.ng = static_cast<float>(-1.0 / (cap2 * cap2));
+  return r;
+}
+
+namespace {
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Checked kernel arguments of a spattn_score; *any is false when it changes nothing.
@@ -199,6 +224,7 @@ int score_args(const spattn_plan_s* P, const spattn_score* s, ScoreArgs* a, bool
   if ((s->slopes && (!s->q_pos || !s->k_pos)) || (s->q_last && !s->k_pos) || !s->q_doc != !s->k_doc)
     return SPATTN_ERR_INVALID_ARG;
   a->cap = s->softcap;
+  a->c = cap_args(s->softcap, P->scale);
   a->slopes = s->slopes;
   a->q_pos = s->q_pos;
   a->k_pos = s->k_pos;

@@ -18,6 +18,7 @@
 // and warps 2..9 turn each step's scores into P / dS, one tile row per lane,
 // two warp groups per step (32 columns each).
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.cuh"
 #include "score.cuh"
@@ -116,8 +117,13 @@ struct DkvCfg {
   static constexpr int kQStages = (D == 128) ? 4 : 6;
   static constexpr int kDStages = (D == 128) ? 4 : 6;
   static constexpr int kSmem = 2 * kTile + (kQStages + kDStages) * (kStageTile + kAugStage) + kOnesBytes + 1024 + 512;
-  // scored form: each row warp's lines of 32 column LSEs and positions
-  static constexpr int kScoreBytes = 8 * 2 * 32 * 4;
+  // scored forms, per stage: -LSE, last position, document and fp32 position of
+  // its 64 query columns, the slopes of its pages, and the ranges of its halves.
+  // A stage's lines are rewritten when its tiles are, after the dV / dK products
+  // of its step, which wait for every row thread.
+  static constexpr int kColBytes = 4 * 64 * 4 + 16 + 32;
+  static constexpr int kScoreBytes = kQStages * kColBytes;
+  static_assert(kQStages == kDStages, "both producers fill the same line");
 };
 
 // 12 warps: 0 and 11 = TMA producers, 1 = TMEM owner and issuer of the MMAs
@@ -128,13 +134,23 @@ struct DkvCfg {
 // core accepts only a couple of MMAs ahead of the one it runs, so a single
 // issuing warp idles it whenever that warp waits; with two issuers one keeps
 // it busy while the other waits.
-constexpr int kAccWarp = 10;
-// Warp 11 is the second producer (dO stages for dK / dV, V stages for dQ;
-// warp 0 produces the Q or K stages): a TMA request holds its issuing thread
-// for hundreds of cycles, so one producer for both column tensors would set
-// the step time.
-constexpr int kDkvThreads = 384;
-constexpr int kDoWarp = 11;
+//
+// The scored forms do several times the arithmetic per pair; two row warps per
+// scheduler left most of its latency in the open (issue slots 0.38 busy), so they
+// split a step over four groups of 16 columns (16 row warps).
+// The producer of the second column tensor (dO stages for dK / dV, V stages for
+// dQ; warp 0 produces the Q or K stages) is the last warp: a TMA request holds
+// its issuing thread for hundreds of cycles, so one producer for both column
+// tensors would set the step time.
+template <bool SCORED>
+struct BwdWarps {
+  static constexpr int kGroups = SCORED ? 4 : 2;
+  static constexpr int kRowThreads = 128 * kGroups;
+  static constexpr int kAcc = 2 + 4 * kGroups;        // issuer of the accumulating products
+  static constexpr int kProd2 = kAcc + 1;
+  static constexpr int kThreads = 32 * (kProd2 + 1);
+  static constexpr int kItemReaders = 3 + 4 * kGroups;  // warps 1, kAcc, kProd2 and the row warps
+};
 
 // Persistent form: one CTA per SM takes work items from a device counter in
 // list order (longest first per head), so each SM keeps its rings and TMEM
@@ -148,15 +164,13 @@ constexpr int kDoWarp = 11;
 // dV; the accumulating products of the next item wait until those
 // accumulators have been read.
 constexpr int kItemQueue = 4;
-// readers of a queue slot: warps 1, 10, 11 and the 8 row-thread warps
-constexpr int kItemReaders = 11;
 
-// SC: the form whose scores are modified (score.cuh).  A cap has to be applied
-// to the bare products, so LSE is not folded into S^T there: the row threads
-// read it per column, with the columns' positions, from their warp's lines in
-// shared memory (the Delta slice stays).
-template <int D, bool SC>
-__global__ void __launch_bounds__(kDkvThreads, 1)
+// SC: the scored forms (score.cuh).  A cap has to be applied to the bare
+// products, so LSE is not folded into S^T there: the row threads read it per
+// column, with the columns' positions and documents, from lines in shared memory
+// that the producers fill with each stage (the Delta slice stays).
+template <int D, int SC>
+__global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     dkdv_kernel(const __grid_constant__ TmaPages tm_k, const __grid_constant__ TmaPages tm_v,
                 const __grid_constant__ TmaPages tm_q, const __grid_constant__ TmaPages tm_do,
                 const int32_t* __restrict__ work, int64_t n_work, int* __restrict__ sched,
@@ -166,6 +180,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 int heads, int kv_heads, int kv_group, const uint16_t* __restrict__ col_heads, int* err,
                 const ScoreArgs sc) {
   using C = DkvCfg<D>;
+  constexpr bool kScored = SC != kScoreNone;
+  using W = BwdWarps<kScored>;
   constexpr int QS = C::kQStages, DS = C::kDStages, NP = kBwdStepPages, SP = C::kStagePages;
   static_assert(SP == NP, "one MMA step per stage");
   constexpr int NH = SP * 16 / 32;  // stage columns per producer lane
@@ -200,6 +216,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   const Abort ab{abort_flag, err};
   const int warp = warp_id(), lane = lane_id();
+  // column lines of stage s (scored forms)
+  uint8_t* score_smem = reinterpret_cast<uint8_t*>(bars) + 512;
+  auto col_lse = [&](int s) { return reinterpret_cast<float*>(score_smem + s * C::kColBytes); };
+  auto col_posf = [&](int s) { return col_lse(s) + 64; };
+  auto col_last = [&](int s) { return reinterpret_cast<int*>(col_lse(s) + 128); };
+  auto col_doc = [&](int s) { return reinterpret_cast<int*>(col_lse(s) + 192); };
+  auto col_slope = [&](int s) { return col_lse(s) + 256; };                             // [4]
+  auto col_rng = [&](int s) { return reinterpret_cast<int4*>(col_lse(s) + 260); };     // [2]
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -217,14 +241,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       mbar_init(&do_empty[s], 1);
     }
     mbar_init(st_full, 1);
-    mbar_init(st_free, 256);
-    for (int b = 0; b < 2; ++b) mbar_init(&pt_full[b], 256);
+    mbar_init(st_free, W::kRowThreads);
+    for (int b = 0; b < 2; ++b) mbar_init(&pt_full[b], W::kRowThreads);
     mbar_init(acc_done, 1);
-    mbar_init(acc_free, 256);
+    mbar_init(acc_free, W::kRowThreads);
     mbar_init(drain, 1);
     for (int s = 0; s < kItemQueue; ++s) {
       mbar_init(&item_full[s], 1);
-      mbar_init(&item_empty[s], kItemReaders);
+      mbar_init(&item_empty[s], W::kItemReaders);
     }
     fence_barrier_init();
   }
@@ -234,7 +258,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     uint4* sl = reinterpret_cast<uint4*>(sQa);
     constexpr int kN16 = ((QS + DS) * kAugStage + kOnesBytes) / 16;
     constexpr int kOnes0 = (QS + DS) * kAugStage / 16;
-    for (int i = threadIdx.x; i < kN16; i += kDkvThreads) {
+    for (int i = threadIdx.x; i < kN16; i += W::kThreads) {
       const bool one = i >= kOnes0 && ((i - kOnes0) & 15) < 8;  // first K half of a ones row
       sl[i] = one ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
     }
@@ -258,7 +282,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     return idx;
   };
 
-  if (warp == 0 || warp == kDoWarp) {
+  if (warp == 0 || warp == W::kProd2) {
     // ---------------- producers (whole warps): warp 0 = Q stages, warp 11 = dO stages ----------------
     // Warp 0 also owns the item queue and loads each item's owned K / V rows.
     // Lane j < n owns page j of a stage: it holds the page id (fetched one
@@ -362,6 +386,29 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       float xc[NH];
       uint32_t livec;
       fetch_terms(0, pid, cbh, xc, livec);
+      // scored forms: the dO producer also holds the positions, last positions and
+      // documents of columns lane + 32h, the Q producer the slopes of the pages
+      int xpos[NH], xlast[NH], xdoc[NH];
+      float xslope = 0.f;
+      const bool masked = kScored && (sc.q_last || sc.q_doc);
+      auto fetch_cols = [&](int t, int pg_lane, int bh_lane) {
+        if (!is_q) {
+          if (!masked && !sc.slopes) return;
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const int idx2 = lane + 32 * h;
+            const int64_t slot = pref_slot(__shfl_sync(0xffffffffu, pg_lane, idx2 >> 4), idx2 & 15);
+            const bool okc = t < n_stages && (idx2 >> 4) < min(SP, n_cols - t * SP) && slot < q_slots;
+            const int64_t off = (wk.bh / kv_heads) * sc.q_batch + (okc ? slot : 0);
+            xpos[h] = sc.slopes ? __ldg(sc.q_pos + off) : 0;
+            xlast[h] = sc.q_last ? __ldg(sc.q_last + off) : 0;
+            xdoc[h] = sc.q_doc ? __ldg(sc.q_doc + off) : -1;
+          }
+        } else if (sc.slopes) {
+          xslope = __ldg(sc.slopes + bh_lane % heads);
+        }
+      };
+      if constexpr (kScored) fetch_cols(0, pid, cbh);
       for (int t = 0; t < n_stages; ++t, ++T) {
         const int s = T % NS;
         const int n = min(SP, n_cols - t * SP);
@@ -374,11 +421,35 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           ok = false;
           break;
         }
+        if (!kScored || !is_q) {
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
-          *reinterpret_cast<uint4*>(aug0 + s * kAugStage + aug_row_off(lane + 32 * h)) =
-              term_row(xc[h], (livec >> h) & 1u);
-        fence_proxy_async_smem();
+          for (int h = 0; h < NH; ++h)
+            *reinterpret_cast<uint4*>(aug0 + s * kAugStage + aug_row_off(lane + 32 * h)) =
+                term_row(xc[h], (livec >> h) & 1u);
+          fence_proxy_async_smem();
+        }
+        if constexpr (kScored) {
+          if (is_q) {
+            // -LSE; -inf for a column behind the list and for a query that attends
+            // nothing: its weights are 2^-inf = 0 whatever its scores
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+              col_lse(s)[lane + 32 * h] = ((livec >> h) & 1u) && xc[h] != -INFINITY ? -xc[h] * kLog2e : -INFINITY;
+            if (lane < SP) col_slope(s)[lane] = SC == kScoreCap ? xslope * kLog2e : xslope * kLog2e / sl2;
+          } else {
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              if (sc.slopes) col_posf(s)[lane + 32 * h] = static_cast<float>(xpos[h]);
+              if (masked) {
+                col_last(s)[lane + 32 * h] = xlast[h];
+                col_doc(s)[lane + 32 * h] = xdoc[h];
+                const int4 rg = column_range((livec >> h) & 1u, xlast[h], xdoc[h]);
+                if (lane == 0) col_rng(s)[h] = rg;
+              }
+            }
+          }
+          fetch_cols(t + 1, pid_next, cbh_next);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&full[s], n * C::kNch * 2048);
         __syncwarp();
@@ -430,7 +501,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         for (int kk = 0; kk < D / 16; ++kk)
           umma_ss_w(tmem, sdesc_add(dk0, (kk >> 2) * kChunkBytes + (kk & 3) * 32),
                     sdesc_add(bq, (kk >> 2) * kStageChunk + (kk & 3) * 32), idesc_s, kk > 0);
-        if constexpr (!SC) umma_ss_w(tmem, d_ones, sdesc_add(d_qa, qs * kAugStage), idesc_s, 1u);
+        if constexpr (!kScored) umma_ss_w(tmem, d_ones, sdesc_add(d_qa, qs * kAugStage), idesc_s, 1u);
         if (!__all_sync(0xffffffffu, mbar_wait(&do_full[ds], (G / DS) & 1, ab))) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
@@ -445,7 +516,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     }
     umma_commit_w(&drain[0]);
     mbar_wait_drain(&drain[0], 0);
-  } else if (warp == kAccWarp) {
+  } else if (warp == W::kAcc) {
     // ---------------- dV, dK issuer (warp-wide; one elected lane issues) ----------------
     const uint64_t dqm = sdesc_sw128(smem_u32(sQ), kStageChunk, 1024);    // Q stages, MN-major
     const uint64_t ddm = sdesc_sw128(smem_u32(sDO), kStageChunk, 1024);   // dO stages, MN-major
@@ -483,14 +554,127 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     }
     umma_commit_w(&drain[1]);
     mbar_wait_drain(&drain[1], 0);
+  } else if constexpr (kScored) {
+    // ---------------- scored P^T, dS^T (one key row per thread, one page of columns per group) + epilogue ----------------
+    constexpr int CW = 64 / W::kGroups;  // 16: group g's columns are page g of the step
+    const int grp = (warp - 2) >> 2;
+    const int q4 = warp & 3;
+    const int row = q4 * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+    int G = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int idx = read_item(k);
+      if (idx < 0) break;
+      const Work wk = load_work(work, idx);
+      const int n_cols = wk.e1 - wk.e0;
+      const int n_steps = (n_cols + NP - 1) / NP;
+      const uint32_t code = wk.row_code(row);
+      const int seg = code < 8 ? static_cast<int>(code) : -1;
+      int key_pos = 0, key_doc = -1;
+      {
+        const int64_t slot = row < 16 * wk.n_own ? pref_slot(wk.own_page(row >> 4), row & 15) : kv_slots;
+        if (slot < kv_slots) {
+          const int64_t off = (wk.bh / kv_heads) * sc.k_batch + slot;
+          if (sc.k_pos) key_pos = __ldg(sc.k_pos + off);
+          if (sc.k_doc) key_doc = __ldg(sc.k_doc + off);
+        }
+      }
+      // this row's mask of the group's page, fetched a step ahead
+      const uint16_t* mask = reinterpret_cast<const uint16_t*>(col_masks + 2 * static_cast<int64_t>(wk.e0)) + (seg < 0 ? 0 : seg);
+      auto mask_of = [&](int st) -> uint32_t {
+        return seg >= 0 && st * NP + grp < n_cols ? __ldg(mask + 8 * (st * NP + grp)) : 0u;
+      };
+      uint32_t m_next = mask_of(0);
+      for (int st = 0; st < n_steps; ++st, ++G) {
+        const int b = G & 1, qs = G % QS;
+        const bool active = st * NP + grp < n_cols;
+        uint32_t m = m_next;
+        m_next = st + 1 < n_steps ? mask_of(st + 1) : 0u;
+        ok = __all_sync(0xffffffffu, mbar_wait(st_full, G & 1, ab));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t a[CW], d[CW], pp[CW / 2], pd[CW / 2];
+        if (active) {
+          tmem_ld16(tmem + lane_off + grp * CW, a);
+          tmem_ld16(tmem + 64 + lane_off + grp * CW, d);
+          tmem_wait_ld();
+        }
+        tc_fence_before();
+        mbar_arrive(st_free);
+        // The stage's lines: both producers' writes are ordered by the barriers that
+        // announce its tiles (long complete: S^T and dP^T were made from them).
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&q_full[qs], (G / QS) & 1, ab) && mbar_wait(&do_full[qs], (G / QS) & 1, ab))) {
+          ok = false;
+          break;
+        }
+        if (active) {
+          if (sc.q_last || sc.q_doc) {
+            const int4 rg = col_rng(qs)[grp >> 1];
+            const bool none = seg < 0 || key_none(sc, rg, key_pos, key_doc);
+            if (none) m = 0u;
+            if (__builtin_expect(__any_sync(0xffffffffu, !none && !key_all(sc, rg, key_pos)), 0))
+              m &= column_bits<false, CW>(sc.q_last, sc.q_doc, col_last(qs) + CW * grp, col_doc(qs) + CW * grp, key_pos, key_doc);
+          }
+          // d = dP^T - Delta (from the augmented product); a = S^T -> log2 P^T
+          if constexpr (SC == kScoreCap) cap_scores<true>(a, d, sc.c);
+          constexpr bool kCap = SC == kScoreCap;
+          if (sc.slopes) bias_scores(a, col_posf(qs) + CW * grp, static_cast<float>(key_pos), col_slope(qs)[grp]);
+          add_columns(a, col_lse(qs) + CW * grp, kCap ? 1.0f : sl2);
+          weights_and_ds(a, d, m, pp, pd);
+        }
+        // Packed set b still feeds dV(G-2) / dK(G-2).  Every row thread waits, active
+        // or not, so that no arrival for step G can land in the pt_full phase of G-2.
+        if (G >= 2 && !__all_sync(0xffffffffu, mbar_wait(&acc_b[b], ((G - 2) >> 1) & 1, ab))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (active) {
+          tmem_st8(tmem + 128 + 64 * b + lane_off + grp * (CW / 2), pp);
+          tmem_st8(tmem + 160 + 64 * b + lane_off + grp * (CW / 2), pd);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&pt_full[b]);
+      }
+      if (!ok) break;
+      // acc_done completes once per item, after the item's last dV / dK products
+      ok = __all_sync(0xffffffffu, mbar_wait(acc_done, k & 1, ab));
+      if (!ok) break;
+      tc_fence_after();
+      {
+        // groups 0, 1 write the halves of dV, groups 2, 3 those of scale * dK
+        const bool owned = code != 15u && row < 16 * wk.n_own;
+        const int64_t slot = owned ? pref_slot(wk.own_page(row >> 4), row & 15) : 0;
+        const bool write = owned && slot < kv_slots;
+        const int half = (grp & 1) * (D / 2);
+        const int64_t base = (static_cast<int64_t>(wk.bh) * kv_slots + slot) * D + half;
+        const uint32_t tacc = (grp < 2 ? tDV : tDK) + half;
+        __nv_bfloat16* out = grp < 2 ? out_dv : out_dk;
+        const float mul = grp < 2 ? 1.0f : scale;
+#pragma unroll
+        for (int pc = 0; pc < D / 64; ++pc) {
+          uint32_t r[32] = {};
+          if (n_steps > 0) {
+            tmem_ld32(tacc + lane_off + pc * 32, r);
+            tmem_wait_ld();
+          }
+          if (write) store_row32(out + base + pc * 32, r, mul, n_steps == 0);
+        }
+      }
+      // the next item's dV / dK products may overwrite the accumulators
+      tc_fence_before();
+      mbar_arrive(acc_free);
+    }
   } else {
     // ---------------- P^T, dS^T (one key row per thread) + epilogue ----------------
     const int grp = (warp - 2) >> 2;  // column half of each step
     const int q4 = warp & 3;
     const int row = q4 * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    // scored form: the scores are in log2 units by then
-    const uint64_t sl2x2 = SC ? f2_pack(1.f, 1.f) : f2_pack(sl2, sl2);
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
     int G = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -503,42 +687,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       const int seg = code < 8 ? static_cast<int>(code) : -1;
       StepMasks<NP> raw;
       if (n_steps > 0) raw.fetch(col_masks, wk.e0, min(NP, n_cols), seg);
-      // scored form: lane l holds column 32 grp + l of the step, loaded a step
-      // ahead (its page reference and head two ahead)
-      float* col_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512) + 64 * (warp - 2);
-      float* col_pos = col_lse + 32;
-      QueryCol qc;
-      int32_t ref = 0;
-      int ref_h = 0, key_pos = 0, key_doc = -1;
-      auto col_ref = [&](int st) {
-        const int e = st * NP + 2 * grp + (lane >> 4);
-        ref = e < n_cols ? __ldg(col_pages + wk.e0 + e) : 0;
-        ref_h = (e < n_cols && col_heads) ? static_cast<int>(__ldg(col_heads + wk.e0 + e)) : 0;
-      };
-      auto col_load = [&](int st) {
-        const int64_t slot = pref_slot(ref, lane & 15);
-        const int bi = wk.bh / kv_heads;
-        const int h = (wk.bh % kv_heads) * kv_group + ref_h;
-        const int64_t off = bi * sc.q_batch + slot;
-        qc.live = st * NP + 2 * grp + (lane >> 4) < n_cols && slot < q_slots;
-        qc.last = (qc.live && sc.q_last) ? __ldg(sc.q_last + off) : 0;
-        qc.doc = (qc.live && sc.q_doc) ? __ldg(sc.q_doc + off) : -1;
-        qc.pos = (qc.live && sc.slopes) ? static_cast<float>(__ldg(sc.q_pos + off)) : 0.f;
-        qc.slope2 = sc.slopes ? __ldg(sc.slopes + h) * kLog2e : 0.f;
-        // a column behind the list: P = 0 whatever its score
-        qc.lse2 = qc.live ? __ldg(lse + (static_cast<int64_t>(bi) * heads + h) * q_slots + slot) * kLog2e : INFINITY;
-      };
-      if constexpr (SC) {
-        const int64_t slot = row < 16 * wk.n_own ? pref_slot(wk.own_page(row >> 4), row & 15) : kv_slots;
-        if (slot < kv_slots) {
-          const int64_t off = (wk.bh / kv_heads) * sc.k_batch + slot;
-          if (sc.k_pos) key_pos = __ldg(sc.k_pos + off);
-          if (sc.k_doc) key_doc = __ldg(sc.k_doc + off);
-        }
-        col_ref(0);
-        col_load(0);
-        col_ref(1);
-      }
       for (int st = 0; st < n_steps; ++st, ++G) {
         const int b = G & 1;
         const int N = 16 * min(NP, n_cols - st * NP);
@@ -547,32 +695,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         raw.bits(mw);
         // mask words of the next step load while this one computes
         if (st + 1 < n_steps) raw.fetch(col_masks, wk.e0 + (st + 1) * NP, min(NP, n_cols - (st + 1) * NP), seg);
-        float slope_lo = 0.f, slope_hi = 0.f;
-        if constexpr (SC) {
-          if (sc.q_last || sc.q_doc) {
-            QueryRange rg;
-            rg.of(qc);
-            const bool none = seg < 0 || (sc.q_last && key_pos > rg.last_max) ||
-                              (sc.q_doc && (key_doc < 0 || key_doc < rg.doc_min || key_doc > rg.doc_max));
-            const bool all = (!sc.q_last || key_pos <= rg.last_min) && (!sc.q_doc || rg.doc_min == rg.doc_max);
-            if (none) mw[0] = mw[1] = 0u;
-            if (__any_sync(0xffffffffu, !none && !all)) {
-              const uint32_t bits = query_bits(qc, sc.q_last, key_pos, sc.q_doc, key_doc);
-              mw[0] &= bits;
-              mw[1] &= bits;
-            }
-          }
-          __syncwarp();
-          col_lse[lane] = qc.lse2;
-          col_pos[lane] = qc.pos;
-          __syncwarp();
-          slope_lo = __shfl_sync(0xffffffffu, qc.slope2, 0);
-          slope_hi = __shfl_sync(0xffffffffu, qc.slope2, 16);
-          if (st + 1 < n_steps) {
-            col_load(st + 1);
-            col_ref(st + 2);
-          }
-        }
         ok = __all_sync(0xffffffffu, mbar_wait(st_full, G & 1, ab));
         if (!ok) break;
         tc_fence_after();
@@ -586,16 +708,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         mbar_arrive(st_free);
         // a = S^T - LSE/scale, d = dP^T - Delta (fp32, from the augmented MMAs)
         uint32_t pp[16], pd[16];
-        if constexpr (SC) {
-          if (active) {
-            // a = S^T: z in log2 units less LSE, so that log2 P^T = a below
-            if (sc.cap > 0.f) cap_scores<true>(a, d, scale / sc.cap, sc.cap * kLog2e);
-            if (sc.slopes)
-              bias_scores(a, col_pos, static_cast<float>(key_pos), sc.cap > 0.f ? 1.0f : sl2, slope_lo, slope_hi);
-            const float mul = (sc.cap > 0.f || sc.slopes) ? 1.0f : sl2;
-            sub_columns(a, col_lse, mul);
-          }
-        }
         if (active) {
           const uint32_t m = grp ? mw[1] : mw[0];
           if (m == 0xFFFFFFFFu) {
@@ -628,10 +740,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                         s1);
               pp[i] = pack_bf16(p0, p1);
               // masked entries: p = 0 exactly, so dS = 0 unless dP - Delta is not finite
-              if constexpr (SC)
-                pd[i] = pack_bf16(live_weight(p0) ? s0 : 0.f, live_weight(p1) ? s1 : 0.f);
-              else
-                pd[i] = pack_bf16(p0 != 0.f ? s0 : 0.f, p1 != 0.f ? s1 : 0.f);
+              pd[i] = pack_bf16(p0 != 0.f ? s0 : 0.f, p1 != 0.f ? s1 : 0.f);
             }
           }
         }
@@ -707,13 +816,16 @@ struct DqCfg {
   static constexpr int kKStages = (D == 128) ? 3 : 5;
   static constexpr int kVStages = (D == 128) ? 3 : 5;
   static constexpr int kSmem = kTile + (kKStages + kVStages) * kStageTile + 1024 + 512;
-  // scored form: each row warp's line of 32 column positions
-  static constexpr int kScoreBytes = 8 * 32 * 4;
+  // scored forms: fp32 positions of each K stage's 128 columns and the ranges of
+  // its four half steps.  The positions are all that fits at head_dim 128, so the
+  // ranges share the barriers' 512 bytes there.
+  static constexpr int kRangeBytes = kKStages * 64;
+  static constexpr int kScoreBytes = kKStages * 128 * 4 + (D == 64 ? kRangeBytes : 0);
 };
 
-// SC: the form whose scores are modified (score.cuh).
-template <int D, bool SC>
-__global__ void __launch_bounds__(kDkvThreads, 1)
+// SC: the scored forms (score.cuh).
+template <int D, int SC>
+__global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     dq_kernel(const __nv_bfloat16* __restrict__ q, const __grid_constant__ TmaPages tm_do,
               const __grid_constant__ TmaPages tm_k, const __grid_constant__ TmaPages tm_v,
               const int32_t* __restrict__ work, const int32_t* __restrict__ col_pages,
@@ -721,6 +833,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
               __nv_bfloat16* __restrict__ out_dq, int64_t q_slots, float sl2, float scale, int heads, int kv_group,
               int* err, const ScoreArgs sc, int64_t kv_slots) {
   using C = DqCfg<D>;
+  constexpr bool kScored = SC != kScoreNone, kCap = SC == kScoreCap;
+  using W = BwdWarps<kScored>;
   constexpr int KS = C::kKStages, VS = C::kVStages, NP = kBwdStepPages, SP = C::kStagePages;
   constexpr int SPS = SP / NP;  // steps per stage
   constexpr int kStageChunk = C::kStageChunk;
@@ -745,6 +859,15 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   const Abort ab{abort_flag, err};
+  // column lines of K stage s (scored forms); a stage's are rewritten when its
+  // tile is, after the dQ products of its steps, which wait for every row thread
+  auto col_posf = [&](int s) { return reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512) + 128 * s; };
+  static_assert(D == 64 || (13 + 2 * (KS + VS)) * 8 + 8 + C::kRangeBytes <= 512, "barriers and ranges share 512 bytes");
+  auto col_rng = [&](int s) {  // [4]
+    uint8_t* base = reinterpret_cast<uint8_t*>(bars) + 512;
+    return reinterpret_cast<int4*>(D == 64 ? base + KS * 512 : base - C::kRangeBytes) + 4 * s;
+  };
+  const bool use_cols = kScored && (sc.q_last || sc.q_doc || sc.slopes);
 
   const Work wk = load_work(work, blockIdx.x);
   // K/V head of this item's query head (grouped-query attention)
@@ -756,7 +879,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     mbar_init(own_full, 1);
-    mbar_init(q_ready, 256);
+    mbar_init(q_ready, W::kRowThreads);
     for (int s = 0; s < KS; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
@@ -767,8 +890,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sd_full[b], 1);
-      mbar_init(&s_free[b], 256);
-      mbar_init(&ds_full[b], 256);
+      mbar_init(&s_free[b], W::kRowThreads);
+      mbar_init(&ds_full[b], W::kRowThreads);
       mbar_init(&dq_done[b], 1);
     }
     mbar_init(acc_done, 1);
@@ -786,7 +909,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   auto tDP = [&](int b) { return tmem + 192 + 64 * b; };
   auto tPk = [&](int p) { return tmem + 320 + 32 * p; };
 
-  if (warp == 0 || warp == kDoWarp) {
+  if (warp == 0 || warp == W::kProd2) {
     // ---------------- producers (whole warps): warp 0 = K stages, warp 11 = V stages ----------------
     // Lane j owns page j of a 128-row stage; page ids are fetched one stage
     // ahead.
@@ -811,15 +934,55 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     }
     __syncwarp();
     const int n_stages = (n_cols + SP - 1) / SP;
-    int pid_next = (n_stages > 0 && lane < min(SP, n_cols)) ? __ldg(col_pages + wk.e0 + lane) : 0;
+    auto page_of = [&](int t) {
+      return (t < n_stages && lane < min(SP, n_cols - t * SP)) ? __ldg(col_pages + wk.e0 + t * SP + lane) : 0;
+    };
+    int pid_next = page_of(0);
+    // scored forms: the K producer's lane l also holds columns l + 32h of a stage,
+    // loaded a stage ahead from page ids that are fetched two ahead
+    int pid_next2 = 0;
+    int cpos[4] = {0, 0, 0, 0}, cdoc[4] = {-1, -1, -1, -1};
+    uint32_t clive = 0u;
+    auto load_cols = [&](int t, int pid_lane) {
+      clive = 0u;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int pg = (lane >> 4) + 2 * h;
+        const int64_t slot = pref_slot(__shfl_sync(0xffffffffu, pid_lane, pg), lane & 15);
+        const bool live = t < n_stages && t * SP + pg < n_cols && slot < kv_slots;
+        const int64_t off = (wk.bh / heads) * sc.k_batch + (live ? slot : 0);
+        cpos[h] = sc.k_pos ? __ldg(sc.k_pos + off) : 0;
+        cdoc[h] = sc.k_doc ? __ldg(sc.k_doc + off) : -1;
+        clive |= live ? 1u << h : 0u;
+      }
+    };
+    const bool cols = use_cols && is_k;
+    if (cols) {
+      pid_next2 = page_of(1);
+      load_cols(0, pid_next);
+    }
     int issued = 0;
     for (int t = 0; t < n_stages; ++t) {
       const int s = t % NS;
       const int n = min(SP, n_cols - t * SP);
       const int pid = pid_next;
-      if (t + 1 < n_stages)
-        pid_next = lane < min(SP, n_cols - (t + 1) * SP) ? __ldg(col_pages + wk.e0 + (t + 1) * SP + lane) : 0;
+      if (cols) {
+        pid_next = pid_next2;
+        pid_next2 = page_of(t + 2);
+      } else {
+        pid_next = page_of(t + 1);
+      }
       if (t >= NS && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((t / NS) - 1) & 1, ab))) break;
+      if (cols) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          col_posf(s)[lane + 32 * h] = static_cast<float>(cpos[h]);
+          const int4 rg = column_range((clive >> h) & 1u, cpos[h], cdoc[h]);
+          if (lane == 0) col_rng(s)[h] = rg;
+        }
+        load_cols(t + 1, pid_next);
+        __syncwarp();
+      }
       if (lane == 0) mbar_arrive_expect_tx(&full[s], n * C::kNch * 2048);
       __syncwarp();
       load_page_runs<C::kNch>(stage0 + s * C::kStageTile, kStageChunk, tm, pid, n, kv_bh, &full[s]);
@@ -861,7 +1024,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     }
     umma_commit_w(&drain[0]);
     mbar_wait_drain(&drain[0], 0);
-  } else if (warp == kAccWarp) {
+  } else if (warp == W::kAcc) {
     // ---------------- dQ issuer (warp-wide; one elected lane issues) ----------------
     const uint64_t dkm = sdesc_sw128(smem_u32(sK), kStageChunk, 1024);   // K stages, MN-major
     const uint32_t idesc_acc = idesc_bf16(128, D, false, true);
@@ -882,6 +1045,168 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     if (ok && n_steps > 0) umma_commit_w(acc_done);
     umma_commit_w(&drain[1]);
     mbar_wait_drain(&drain[1], 0);
+  } else if constexpr (kScored) {
+    // ---------------- scored dS (one query row per thread, one page of columns per group) + epilogue ----------------
+    constexpr int NG = W::kGroups, CW = 64 / NG;  // 16: group g's columns are page g of the step
+    const int grp = (warp - 2) >> 2;
+    const int q4 = warp & 3;
+    const int row = q4 * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t code = wk.row_code(row);
+    const int seg = code < 8 ? static_cast<int>(code) : -1;
+    const bool owned = code != 15u && row < 16 * wk.n_own;
+    const int64_t slot = row < 16 * wk.n_own ? pref_slot(wk.own_page(row >> 4), row & 15) : 0;
+    const bool loaded = row < 16 * wk.n_own && slot < q_slots;
+    const bool valid_slot = owned && slot < q_slots;
+    const int64_t roff = static_cast<int64_t>(wk.bh) * q_slots + slot;
+    // Q row into TMEM as bf16 pairs: group g stores pair columns [g*D/8, (g+1)*D/8)
+    {
+      constexpr int kCols = D / 2 / NG;  // 32-bit TMEM columns per group
+      uint32_t qr[kCols] = {};
+      if (loaded) {
+        const uint4* src = reinterpret_cast<const uint4*>(q + roff * D + grp * (D / NG));
+#pragma unroll
+        for (int i = 0; i < kCols / 4; ++i) {
+          const uint4 v = __ldg(src + i);
+          qr[4 * i] = v.x;
+          qr[4 * i + 1] = v.y;
+          qr[4 * i + 2] = v.z;
+          qr[4 * i + 3] = v.w;
+        }
+      }
+      if constexpr (kCols == 16)
+        tmem_st16(tQ + lane_off + grp * kCols, qr);
+      else
+        tmem_st8(tQ + lane_off + grp * kCols, qr);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(q_ready);
+    }
+    const float lse_row = (valid_slot && seg >= 0) ? __ldg(lse + roff) : 0.f;
+    const float nlse2 = lse_row == -INFINITY ? -INFINITY : -lse_row * kLog2e;  // -inf: no key, every weight 0
+    const float dl = (valid_slot && seg >= 0) ? __ldg(delta + roff) : 0.f;
+    // this row's side of the masks and the bias
+    int row_last = 0, row_doc = -1;
+    float row_pos = 0.f, slope = 0.f;
+    if (loaded) {
+      const int64_t off = (wk.bh / heads) * sc.q_batch + slot;
+      if (sc.q_last) row_last = __ldg(sc.q_last + off);
+      if (sc.q_doc) row_doc = __ldg(sc.q_doc + off);
+      if (sc.slopes) row_pos = static_cast<float>(__ldg(sc.q_pos + off));
+    }
+    const float mul = kCap ? 1.0f : sl2;  // after the cap the scores are in log2 units
+    if (sc.slopes) slope = __ldg(sc.slopes + wk.bh % heads) * kLog2e / mul;
+    const uint64_t m2 = f2_pack(mul, mul);
+    // Bits of this group's 16 columns of a step, compared pair by pair: lanes load
+    // one column each (the stage's lines hold fp32 positions only).
+    auto step_bits = [&](int st) -> uint32_t {
+      const int e = st * NP + grp;
+      const int64_t kslot = e < n_cols ? pref_slot(__ldg(col_pages + wk.e0 + e), lane & 15) : kv_slots;
+      const int64_t off = (wk.bh / heads) * sc.k_batch + (kslot < kv_slots ? kslot : 0);
+      uint32_t bits = (1u << CW) - 1u;
+      if (sc.q_last) {
+        const int p = __ldg(sc.k_pos + off);
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < CW; ++i) m |= __shfl_sync(0xffffffffu, p, i) <= row_last ? 1u << i : 0u;
+        bits = m;
+      }
+      if (sc.q_doc) {
+        const int dc = __ldg(sc.k_doc + off);
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < CW; ++i) m |= __shfl_sync(0xffffffffu, dc, i) == row_doc ? 1u << i : 0u;
+        bits &= row_doc >= 0 ? m : 0u;
+      }
+      return bits;
+    };
+    // this row's mask of the group's page, fetched a step ahead
+    const uint16_t* mask = reinterpret_cast<const uint16_t*>(col_masks + 2 * static_cast<int64_t>(wk.e0)) + (seg < 0 ? 0 : seg);
+    auto mask_of = [&](int st) -> uint32_t {
+      return seg >= 0 && st * NP + grp < n_cols ? __ldg(mask + 8 * (st * NP + grp)) : 0u;
+    };
+    const uint64_t ndl = f2_pack(-dl, -dl), nl2 = f2_pack(nlse2, nlse2);
+    bool ok = true;
+    uint32_t m_next = n_steps > 0 ? mask_of(0) : 0u;
+    for (int st = 0; st < n_steps; ++st) {
+      const int b = st & 1, t = st / SPS, ks = t % KS;
+      const bool active = st * NP + grp < n_cols;
+      uint32_t m = m_next;
+      m_next = st + 1 < n_steps ? mask_of(st + 1) : 0u;
+      if (use_cols) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&k_full[ks], (t / KS) & 1, ab))) {
+          ok = false;
+          break;
+        }
+        if (active && (sc.q_last || sc.q_doc)) {
+          const int4 rg = col_rng(ks)[2 * (st % SPS) + (grp >> 1)];
+          const bool none = seg < 0 || query_none(sc, rg, row_last, row_doc);
+          if (none) m = 0u;
+          if (__builtin_expect(__any_sync(0xffffffffu, !none && !query_all(sc, rg, row_last)), 0)) m &= step_bits(st);
+        }
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&sd_full[b], (st >> 1) & 1, ab));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t a[CW], d[CW], pp[CW / 2], pd[CW / 2];
+      if (active) {
+        tmem_ld16(tS(b) + lane_off + grp * CW, a);
+        tmem_ld16(tDP(b) + lane_off + grp * CW, d);
+        tmem_wait_ld();
+      }
+      tc_fence_before();
+      mbar_arrive(&s_free[b]);
+      if (active) {
+#pragma unroll
+        for (int i = 0; i < CW; i += 2) {
+          float x0, x1;
+          f2_unpack(f2_add(f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), ndl), x0, x1);
+          d[i] = __float_as_uint(x0);
+          d[i + 1] = __float_as_uint(x1);
+        }
+        if constexpr (kCap) cap_scores<true>(a, d, sc.c);
+        if (sc.slopes) bias_scores(a, col_posf(ks) + 64 * (st % SPS) + CW * grp, row_pos, slope);
+#pragma unroll
+        for (int i = 0; i < CW; i += 2) {
+          float x0, x1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), m2, nl2), x0, x1);
+          a[i] = __float_as_uint(x0);
+          a[i + 1] = __float_as_uint(x1);
+        }
+        weights_and_ds(a, d, m, pp, pd);
+      }
+      // Packed set b still feeds dQ(st-2).  Every row thread waits, active or not:
+      // dq_done(st-2) implies that ds_full finished the phase of step st-2.
+      if (st >= 2 && !__all_sync(0xffffffffu, mbar_wait(&dq_done[b], ((st - 2) >> 1) & 1, ab))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (active) {
+        tmem_st8(tPk(b) + lane_off + grp * (CW / 2), pd);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      mbar_arrive(&ds_full[b]);
+    }
+    if (ok && n_steps > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, ab));
+      tc_fence_after();
+    }
+    if (ok) {
+      // group g writes columns [g*D/4, (g+1)*D/4) of dQ
+      constexpr int kOut = D / NG;  // 32 or 16
+      const int col = grp * kOut;
+      uint32_t r[kOut] = {};
+      if (n_steps > 0) {
+        if constexpr (kOut == 32)
+          tmem_ld32(tDQ + lane_off + col, r);
+        else
+          tmem_ld16(tDQ + lane_off + col, r);
+        tmem_wait_ld();
+      }
+      if (valid_slot) store_row(out_dq + roff * D + col, r, scale, n_steps == 0);
+    }
   } else {
     const int grp = (warp - 2) >> 2;  // column half of each step
     const int q4 = warp & 3;
@@ -923,42 +1248,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     }
     const float lse2 = (valid_slot && seg >= 0) ? __ldg(lse + roff) * kLog2e : 0.f;
     const float dl = (valid_slot && seg >= 0) ? __ldg(delta + roff) : 0.f;
-    // after the cap or the bias the scores are in log2 units already
-    const float mul = SC && (sc.cap > 0.f || sc.slopes) ? 1.0f : sl2;
-    const uint64_t sl2x2 = f2_pack(mul, mul);
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
     const uint64_t nl2 = f2_pack(-lse2, -lse2);
-    const float dl_left = SC && sc.cap > 0.f ? 0.f : dl;  // a cap's gradient has taken Delta off already
-    const uint64_t ndl = f2_pack(-dl_left, -dl_left);
+    const uint64_t ndl = f2_pack(-dl, -dl);
     bool ok = true;
     StepMasks<NP> raw;
     if (n_steps > 0) raw.fetch(col_masks, wk.e0, min(NP, n_cols), seg);
-    // scored form: lane l holds column 32 grp + l of the step, loaded a step
-    // ahead (its page reference two ahead)
-    float* col_pos = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512) + 32 * (warp - 2);
-    KeyCol kc;
-    int32_t ref = 0;
-    RowRule rule{0, 0};
-    float row_pos = 0.f, slope2 = 0.f;
-    auto col_ref = [&](int st) {
-      const int e = st * NP + 2 * grp + (lane >> 4);
-      return e < n_cols ? __ldg(col_pages + wk.e0 + e) : 0;
-    };
-    auto col_load = [&](int st) {
-      return load_key_col(sc, (wk.bh / heads) * sc.k_batch, st * NP + 2 * grp + (lane >> 4) < n_cols, ref, lane & 15,
-                          kv_slots);
-    };
-    if constexpr (SC) {
-      if (loaded) {
-        const int64_t off = (wk.bh / heads) * sc.q_batch + slot;
-        if (sc.q_last) rule.last = __ldg(sc.q_last + off);
-        if (sc.q_doc) rule.doc = __ldg(sc.q_doc + off);
-        if (sc.slopes) row_pos = static_cast<float>(__ldg(sc.q_pos + off));
-      }
-      if (sc.slopes) slope2 = __ldg(sc.slopes + wk.bh % heads) * kLog2e;
-      ref = col_ref(0);
-      kc = col_load(0);
-      ref = col_ref(1);
-    }
     for (int st = 0; st < n_steps; ++st) {
       const int b = st & 1;
       const int N = 16 * min(NP, n_cols - st * NP);
@@ -967,32 +1262,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       raw.bits(mw);
       // mask words of the next step load while this one computes
       if (st + 1 < n_steps) raw.fetch(col_masks, wk.e0 + (st + 1) * NP, min(NP, n_cols - (st + 1) * NP), seg);
-      if constexpr (SC) {
-        if (sc.q_last || sc.q_doc) {
-          ColRange rg;
-          rg.reset();
-          rg.add(kc);
-          rg.reduce();
-          const bool none = seg < 0 || (sc.q_last && rg.pos_min > rule.last) ||
-                            (sc.q_doc && (rule.doc < 0 || rule.doc < rg.doc_min || rule.doc > rg.doc_max));
-          const bool all = (!sc.q_last || rg.pos_max <= rule.last) && (!sc.q_doc || rg.doc_min == rg.doc_max);
-          if (none) mw[0] = mw[1] = 0u;
-          if (__any_sync(0xffffffffu, !none && !all)) {
-            const uint32_t bits = key_bits(kc, sc.q_last, rule.last, sc.q_doc, rule.doc);
-            mw[0] &= bits;
-            mw[1] &= bits;
-          }
-        }
-        if (sc.slopes) {
-          __syncwarp();
-          col_pos[lane] = static_cast<float>(kc.pos);
-          __syncwarp();
-        }
-        if (st + 1 < n_steps) {
-          kc = col_load(st + 1);
-          ref = col_ref(st + 2);
-        }
-      }
       ok = __all_sync(0xffffffffu, mbar_wait(&sd_full[b], (st >> 1) & 1, ab));
       if (!ok) break;
       tc_fence_after();
@@ -1005,17 +1274,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tc_fence_before();
       mbar_arrive(&s_free[b]);
       uint32_t pd[16];
-      if constexpr (SC) {
-        if (active) {
-          if (sc.cap > 0.f) {
-            // dZ / dX = 1 - tanh^2 goes onto dP - Delta
-#pragma unroll
-            for (int i = 0; i < 32; ++i) d[i] = __float_as_uint(__uint_as_float(d[i]) - dl);
-            cap_scores<true>(a, d, scale / sc.cap, sc.cap * kLog2e);
-          }
-          if (sc.slopes) bias_scores(a, col_pos, row_pos, sc.cap > 0.f ? 1.0f : sl2, slope2, slope2);
-        }
-      }
       if (active) {
         const uint32_t m = grp ? mw[1] : mw[0];
         if (m == 0xFFFFFFFFu) {
@@ -1043,10 +1301,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             float g0, g1;
             f2_unpack(f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), ndl)),
                       g0, g1);
-            if constexpr (SC)
-              pd[i] = pack_bf16(live_weight(p0) ? g0 : 0.f, live_weight(p1) ? g1 : 0.f);
-            else
-              pd[i] = pack_bf16(p0 != 0.f ? g0 : 0.f, p1 != 0.f ? g1 : 0.f);
+            pd[i] = pack_bf16(p0 != 0.f ? g0 : 0.f, p1 != 0.f ? g1 : 0.f);
           }
         }
       }
@@ -1107,12 +1362,12 @@ cudaError_t launch_delta(int head_dim, const __nv_bfloat16* o, const __nv_bfloat
   return cudaGetLastError();
 }
 
-template <int D, bool SC>
+template <int D, int SC>
 static cudaError_t launch_dkdv_t(const TmaPages& tk, const TmaPages& tv, const TmaPages& tq,
                                  const TmaPages& tdo, const TileArgs& a, const ScoreArgs& sc, const float* lse,
                                  const float* delta, __nv_bfloat16* dk, __nv_bfloat16* dv, cudaStream_t st) {
   using C = DkvCfg<D>;
-  constexpr int kSmem = C::kSmem + (SC ? C::kScoreBytes : 0);
+  constexpr int kSmem = C::kSmem + (SC != kScoreNone ? C::kScoreBytes : 0);
   cudaError_t e = cudaFuncSetAttribute(dkdv_kernel<D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess || a.n_work == 0) return e;
   // one persistent CTA per SM (at most one item each when there are fewer items)
@@ -1122,44 +1377,56 @@ static cudaError_t launch_dkdv_t(const TmaPages& tk, const TmaPages& tv, const T
   if (e == cudaSuccess) e = cudaMemsetAsync(a.sched, 0, sizeof(int), st);
   if (e != cudaSuccess) return e;
   const int64_t grid = std::min<int64_t>(a.n_work, std::max(sms, 1));
-  dkdv_kernel<D, SC><<<static_cast<unsigned>(grid), kDkvThreads, kSmem, st>>>(
+  dkdv_kernel<D, SC><<<static_cast<unsigned>(grid), BwdWarps<SC != kScoreNone>::kThreads, kSmem, st>>>(
       tk, tv, tq, tdo, a.work, a.n_work, a.sched, a.pages, a.masks, lse, delta, dk, dv, a.own_slots, a.col_slots,
       a.scale * kLog2e, a.scale, a.heads, a.kv_heads, a.kv_group, a.col_heads, a.err, sc);
   return cudaGetLastError();
 }
 
-template <int D, bool SC>
+template <int D, int SC>
 static cudaError_t launch_dq_t(const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
                                const TmaPages& tv, const TileArgs& a, const ScoreArgs& sc, const float* lse,
                                const float* delta, __nv_bfloat16* dq, cudaStream_t st) {
   using C = DqCfg<D>;
-  constexpr int kSmem = C::kSmem + (SC ? C::kScoreBytes : 0);
+  constexpr int kSmem = C::kSmem + (SC != kScoreNone ? C::kScoreBytes : 0);
   cudaError_t e = cudaFuncSetAttribute(dq_kernel<D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess || a.n_work == 0) return e;
-  dq_kernel<D, SC><<<static_cast<unsigned>(a.n_work), kDkvThreads, kSmem, st>>>(
+  dq_kernel<D, SC><<<static_cast<unsigned>(a.n_work), BwdWarps<SC != kScoreNone>::kThreads, kSmem, st>>>(
       q, tdo, tk, tv, a.work, a.pages, a.masks, lse, delta, dq, a.own_slots, a.scale * kLog2e, a.scale, a.heads,
       a.kv_group, a.err, sc, a.col_slots);
   return cudaGetLastError();
 }
 
+// Calls `go` with the head size and the form of the scores as constants.
+template <typename F>
+static cudaError_t by_form(int head_dim, const ScoreArgs* sc, const F& go) {
+  const int form = !sc ? kScoreNone : sc->cap > 0.f ? kScoreCap : kScoreMask;
+  const auto pick = [&](auto d) {
+    return form == kScoreNone   ? go(d, std::integral_constant<int, kScoreNone>{})
+           : form == kScoreMask ? go(d, std::integral_constant<int, kScoreMask>{})
+                                : go(d, std::integral_constant<int, kScoreCap>{});
+  };
+  return head_dim == 128 ? pick(std::integral_constant<int, 128>{}) : pick(std::integral_constant<int, 64>{});
+}
+
 cudaError_t launch_dkdv(int head_dim, const TmaPages& tk, const TmaPages& tv, const TmaPages& tq, const TmaPages& tdo,
                         const TileArgs& a, const ScoreArgs* sc, const float* lse, const float* delta,
                         __nv_bfloat16* dk, __nv_bfloat16* dv, cudaStream_t st) {
-  if (sc)
-    return head_dim == 128 ? launch_dkdv_t<128, true>(tk, tv, tq, tdo, a, *sc, lse, delta, dk, dv, st)
-                           : launch_dkdv_t<64, true>(tk, tv, tq, tdo, a, *sc, lse, delta, dk, dv, st);
-  return head_dim == 128 ? launch_dkdv_t<128, false>(tk, tv, tq, tdo, a, ScoreArgs(), lse, delta, dk, dv, st)
-                         : launch_dkdv_t<64, false>(tk, tv, tq, tdo, a, ScoreArgs(), lse, delta, dk, dv, st);
+  const auto go = [&](auto d, auto form) {
+    return launch_dkdv_t<decltype(d)::value, decltype(form)::value>(tk, tv, tq, tdo, a, sc ? *sc : ScoreArgs(), lse,
+                                                                    delta, dk, dv, st);
+  };
+  return by_form(head_dim, sc, go);
 }
 
 cudaError_t launch_dq(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
                       const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, const float* lse,
                       const float* delta, __nv_bfloat16* dq, cudaStream_t st) {
-  if (sc)
-    return head_dim == 128 ? launch_dq_t<128, true>(q, tdo, tk, tv, a, *sc, lse, delta, dq, st)
-                           : launch_dq_t<64, true>(q, tdo, tk, tv, a, *sc, lse, delta, dq, st);
-  return head_dim == 128 ? launch_dq_t<128, false>(q, tdo, tk, tv, a, ScoreArgs(), lse, delta, dq, st)
-                         : launch_dq_t<64, false>(q, tdo, tk, tv, a, ScoreArgs(), lse, delta, dq, st);
+  const auto go = [&](auto d, auto form) {
+    return launch_dq_t<decltype(d)::value, decltype(form)::value>(q, tdo, tk, tv, a, sc ? *sc : ScoreArgs(), lse, delta,
+                                                                  dq, st);
+  };
+  return by_form(head_dim, sc, go);
 }
 
 }  // namespace spattn

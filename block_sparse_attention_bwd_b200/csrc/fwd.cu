@@ -53,8 +53,14 @@ struct FwdCfg {
   static constexpr int kKStages = (D == 128 && !F8) ? 2 : 4;  // K ring depth
   static constexpr int kVStages = (D == 128) ? 2 : 4;         // V ring depth
   static constexpr int kSmem = kTile + kKStages * kKStage + kVStages * kVStage + 1024 + 512;
-  // scored form: each row warp's line of 64 column positions
-  static constexpr int kScoreBytes = 4 * 64 * 4;
+  // scored forms: ring of column lines (positions, documents, fp32 positions of
+  // a step's 64 columns), the range of each, and their barriers.  The producer
+  // is at most kKStages steps ahead of S, and S(st) is issued after the rows have
+  // left step st - 2, so kKStages + 2 lines are never overwritten while read.
+  static constexpr int kColRing = 8;
+  static constexpr int kColBytes = 3 * 64 * 4;
+  static constexpr int kScoreBytes = kColRing * (kColBytes + 16 + 8) + 4 * 128 * 4 + 4 * 8;  // + the row pairs' exchange and barriers
+  static_assert(kColRing >= kKStages + 2, "column lines outlive their readers");
   static_assert(!F8 || D == 128, "the E4M3 forward has D = 128 (one 128-byte row per chunk)");
 };
 
@@ -64,20 +70,21 @@ constexpr float kRescaleThreshold = 8.0f;
 
 // 6 warps: 0 = TMA producer, 1 = TMEM owner and MMA issuer, 2..5 = row
 // threads (warp w reaches TMEM lanes 32*(w%4) .. 32*(w%4)+31).
-constexpr int kFwdThreads = 192;
+// The fixed scored form has two row threads per row (score.cuh): warps 2..9.
+template <int SC>
+constexpr int kFwdThreads = SC == kScoreFixed ? 320 : 192;
 
 // ROUTE: the form that reads each item's route flag (the 64-row route of
 // Work::halves); without it every item runs as 128 rows over its whole list.
-// SC: the form whose scores are modified (score.cuh); its row threads hold
-// the next step's column positions and documents, one or two per lane.
-template <int D, bool F8, bool ROUTE, bool SC>
-__global__ void __launch_bounds__(kFwdThreads, 2)
+// SC: the scored forms (score.cuh).
+template <int D, bool F8, bool ROUTE, int SC>
+__global__ void __launch_bounds__(kFwdThreads<SC>, 2)
     fwd_kernel(const __grid_constant__ TmaPages tm_q, const __grid_constant__ TmaPages tm_k,
                const __grid_constant__ TmaPages tm_v, const int32_t* __restrict__ work,
                const int32_t* __restrict__ col_pages, const uint64_t* __restrict__ col_masks,
                __nv_bfloat16* __restrict__ out_o, float* __restrict__ out_lse, int64_t q_slots, float sl2,
                int heads, int kv_group, const float* __restrict__ q_descale, const float* __restrict__ k_descale,
-               int* err, const ScoreArgs sc, int64_t kv_slots, float scale) {
+               int* err, const ScoreArgs sc, int64_t kv_slots) {
   using C = FwdCfg<D, F8>;
   constexpr int KS = C::kKStages, VS = C::kVStages, NP = kFwdStepPages;
   extern __shared__ uint8_t smem_raw[];
@@ -99,6 +106,17 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(o_last + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   const Abort ab{abort_flag, err};
+  constexpr int R = C::kColRing;
+  uint8_t* score_smem = reinterpret_cast<uint8_t*>(bars) + 512;
+  auto col_pos = [&](int st) { return reinterpret_cast<int*>(score_smem + (st % R) * C::kColBytes); };
+  auto col_doc = [&](int st) { return col_pos(st) + 64; };
+  auto col_posf = [&](int st) { return reinterpret_cast<float*>(col_pos(st) + 128); };
+  int4* col_rng = reinterpret_cast<int4*>(score_smem + R * C::kColBytes);
+  uint64_t* c_full = reinterpret_cast<uint64_t*>(col_rng + R);  // [R]
+  float* xrow = reinterpret_cast<float*>(c_full + R);            // [4][128] sums of the row pairs (fixed form)
+  uint64_t* pair_bar = reinterpret_cast<uint64_t*>(xrow + 4 * 128);  // [4]
+  const bool use_cols = SC != kScoreNone && SC != kScoreFixed ? (sc.q_last || sc.q_doc || sc.slopes)
+                                                              : SC == kScoreFixed && (sc.q_last || sc.q_doc);
 
   const Work wk = load_work(work, blockIdx.x);
   // K/V head of this item's query head (grouped-query attention)
@@ -122,11 +140,15 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], 128);
+      mbar_init(&p_full[b], kFwdThreads<SC> - 64);
     }
     mbar_init(o_done, 1);
     mbar_init(drain, 1);
     mbar_init(o_last, 1);
+    if constexpr (SC != kScoreNone) {
+      for (int s = 0; s < R; ++s) mbar_init(&c_full[s], 1);
+      for (int s = 0; s < 4; ++s) mbar_init(&pair_bar[s], 64);
+    }
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(tslot, 256);
@@ -151,15 +173,55 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     __syncwarp();
     load_page_runs<C::kQKNch>(sQ, kChunkBytes, tm_q, lane < wk.n_own ? wk.own_page(lane) : 0, wk.n_own, wk.bh,
                               q_full);
-    int pid_next = (n_steps > 0 && lane < min(NP, n_cols)) ? __ldg(col_pages + wk.e0 + lane) : 0;
+    auto page_of = [&](int st) {
+      return (st < n_steps && lane < min(NP, n_cols - st * NP)) ? __ldg(col_pages + wk.e0 + st * NP + lane) : 0;
+    };
+    int pid_next = page_of(0);
+    // scored forms: lane l also holds columns l and l + 32 of a step, loaded a step
+    // ahead from page ids that are fetched two ahead
+    int pid_next2 = 0;
+    int cpos[2] = {0, 0}, cdoc[2] = {-1, -1};
+    bool clive[2] = {false, false};
+    auto load_cols = [&](int st, int pid_lane) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int pg = (lane >> 4) + 2 * h;
+        const int64_t slot = pref_slot(__shfl_sync(0xffffffffu, pid_lane, pg), lane & 15);
+        clive[h] = st < n_steps && st * NP + pg < n_cols && slot < kv_slots;
+        const int64_t off = (wk.bh / heads) * sc.k_batch + (clive[h] ? slot : 0);
+        cpos[h] = sc.k_pos ? __ldg(sc.k_pos + off) : 0;
+        cdoc[h] = sc.k_doc ? __ldg(sc.k_doc + off) : -1;
+      }
+    };
+    if (use_cols) {
+      pid_next2 = page_of(1);
+      load_cols(0, pid_next);
+    }
     int k_issued = 0, v_issued = 0;
     for (int st = 0; st < n_steps; ++st) {
       const int n = min(NP, n_cols - st * NP);
       const int pid = pid_next;
-      if (st + 1 < n_steps)
-        pid_next = lane < min(NP, n_cols - (st + 1) * NP) ? __ldg(col_pages + wk.e0 + (st + 1) * NP + lane) : 0;
       const int ks = st % KS, vs = st % VS;
+      if (use_cols) {
+        pid_next = pid_next2;
+        pid_next2 = page_of(st + 2);
+      } else {
+        pid_next = page_of(st + 1);
+      }
       if (st >= KS && !__all_sync(0xffffffffu, mbar_wait(&k_empty[ks], ((st / KS) - 1) & 1, ab))) break;
+      if (use_cols) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          col_pos(st)[lane + 32 * h] = cpos[h];
+          col_doc(st)[lane + 32 * h] = cdoc[h];
+          col_posf(st)[lane + 32 * h] = static_cast<float>(cpos[h]);
+        }
+        const int4 rg = range_join(column_range(clive[0], cpos[0], cdoc[0]), column_range(clive[1], cpos[1], cdoc[1]));
+        if (lane == 0) col_rng[st % R] = rg;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c_full[st % R]);
+        load_cols(st + 1, pid_next);
+      }
       if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], n * C::kQKNch * 2048);
       __syncwarp();
       load_page_runs<C::kQKNch>(sK + ks * C::kKStage, kFwdStageChunk, tm_k, pid, n, kv_bh, &k_full[ks]);
@@ -205,7 +267,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
         for (int j = 0; j < NP; ++j)
           if (j < n)
-            umma_ts_w(tO, tmem + 64 * b + 8 * j, sdesc_add(dv, j * 2048), idesc_pv, (st > 0 || j > 0) ? 1u : 0u);
+            umma_ts_w(tO, tmem + 64 * b + 8 * j + (SC == kScoreFixed && j >= 2 ? 16 : 0), sdesc_add(dv, j * 2048), idesc_pv,
+                      (st > 0 || j > 0) ? 1u : 0u);
       }
       umma_commit_w(&v_empty[vs]);
       umma_commit_w(o_done);
@@ -267,6 +330,104 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     if (ok && n_steps > 0 && issue_pv(n_steps - 1)) umma_commit_w(o_last);
     umma_commit_w(drain);
     mbar_wait_drain(drain, 0);
+  } else if constexpr (SC == kScoreFixed) {
+    // ---------------- softmax of the fixed form + epilogue (two threads per row, 32 columns each) ----------------
+    const int grp = (warp - 2) >> 2;
+    const int q4 = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+    // tile row of this thread's TMEM lane, as in the other forms below; in the
+    // 64-row route group 0 has the row's 32 columns and group 1 none
+    const int hh = (lane >> 4) & 1;
+    const int row = halves ? 64 * hh + (lane & 15) + 16 * q4 : q4 * 32 + lane;
+    const int pg0 = halves ? 2 * hh : 2 * grp;  // first of this thread's two pages of a step
+    const uint32_t code = wk.row_code(row);
+    const int seg = code < 8 ? static_cast<int>(code) : -1;
+    float* xr = xrow + row;
+    // this row's side of the masks
+    int row_last = 0, row_doc = -1;
+    {
+      const int bi = wk.bh / heads;
+      const int64_t slot = row < 16 * wk.n_own ? pref_slot(wk.own_page(row >> 4), row & 15) : q_slots;
+      if (slot < q_slots) {
+        const int64_t off = bi * sc.q_batch + slot;
+        if (sc.q_last) row_last = __ldg(sc.q_last + off);
+        if (sc.q_doc) row_doc = __ldg(sc.q_doc + off);
+      }
+    }
+    // this row's masks of its two pages, fetched a step ahead
+    const uint16_t* mask = reinterpret_cast<const uint16_t*>(col_masks + 2 * static_cast<int64_t>(wk.e0)) + (seg < 0 ? 0 : seg);
+    uint32_t m_lo = 0u, m_hi = 0u;
+    auto fetch_masks = [&](int st) {
+      const int e = st * NP + pg0;
+      m_lo = seg >= 0 && e < n_cols ? __ldg(mask + 8 * e) : 0u;
+      m_hi = seg >= 0 && e + 1 < n_cols ? __ldg(mask + 8 * (e + 1)) : 0u;
+    };
+    if (n_steps > 0) fetch_masks(0);
+    SoftRow r;
+    bool ok = true;
+    for (int st = 0; st < n_steps; ++st) {
+      const int b = st & 1;
+      const bool active = halves ? grp == 0 : 2 * grp < n_cols - st * NP;
+      uint32_t bits = m_lo | (m_hi << 16);
+      if (st + 1 < n_steps) fetch_masks(st + 1);
+      if (use_cols) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&c_full[st % R], (st / R) & 1, ab))) {
+          ok = false;
+          break;
+        }
+        if (active && (sc.q_last || sc.q_doc)) {
+          const int4 rg = col_rng[st % R];
+          const bool none = seg < 0 || query_none(sc, rg, row_last, row_doc);
+          if (none) bits = 0u;
+          if (__builtin_expect(__any_sync(0xffffffffu, !none && !query_all(sc, rg, row_last)), 0))
+            bits &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + 16 * pg0, col_doc(st) + 16 * pg0, row_last, row_doc);
+        }
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (st >> 1) & 1, ab));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t x[32];
+      const uint32_t s_addr = tmem + 64 * b + lane_off + 32 * grp;
+      if (active) {
+        tmem_ld32(s_addr, x);
+        tmem_wait_ld();
+        cap_scores<false>(x, x, sc.c);
+        if (__builtin_expect(bits != 0xFFFFFFFFu, 0)) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!((bits >> i) & 1u)) x[i] = 0xFF800000u;  // -inf
+        }
+        soft_weights(x, r, s_addr);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[b]);
+    }
+    if (ok && n_steps > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(o_last, 0, ab));
+      tc_fence_after();
+    }
+    float l = 0.f, l_true = 0.f;
+    ok = ok && soft_total(r, xr, grp, &pair_bar[q4], ab, l, l_true);
+    if (ok) {
+      const bool owned = code != 15u && row < 16 * wk.n_own;
+      const int64_t slot = owned ? pref_slot(wk.own_page(row >> 4), row & 15) : 0;
+      const bool write = owned && slot < q_slots;
+      const bool empty = !(l > 0.f);
+      const float inv = empty ? 0.f : 1.0f / l;
+      __nv_bfloat16* dst = out_o + (static_cast<int64_t>(wk.bh) * q_slots + slot) * D + grp * (D / 2);
+#pragma unroll
+      for (int pc = 0; pc < D / 64; ++pc) {
+        uint32_t v[32] = {};
+        if (n_steps > 0) {
+          tmem_ld32(tO + lane_off + grp * (D / 2) + pc * 32, v);
+          tmem_wait_ld();
+        }
+        if (write) store_row32(dst + pc * 32, v, inv, empty || n_steps == 0);
+      }
+      if (write && grp == 0)
+        out_lse[static_cast<int64_t>(wk.bh) * q_slots + slot] = empty ? -INFINITY : lg2(l_true) * kLn2;
+    }
   } else {
     // ---------------- softmax + epilogue (one row per thread) ----------------
     const int q4 = warp & 3;
@@ -282,41 +443,22 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     bool ok = true;
     StepMasks<NP> raw;
     if (n_steps > 0) raw.fetch(col_masks, wk.e0, min(NP, n_cols), seg);
-    // scored form: lane l holds columns l and l + 32 of the step, loaded a step
-    // ahead (their page references two ahead)
-    float* col_pos = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 512) + 64 * q4;
-    KeyCol kc[2];
-    int32_t ref[2];
-    int64_t kb = 0;
-    RowRule rule{0, 0};
-    float row_pos = 0.f, slope2 = 0.f;
-    auto col_ref = [&](int st, int h) {
-      const int e = st * NP + (lane >> 4) + 2 * h;
-      return e < n_cols ? __ldg(col_pages + wk.e0 + e) : 0;
-    };
-    auto col_load = [&](int st, int h) {
-      return load_key_col(sc, kb, st * NP + (lane >> 4) + 2 * h < n_cols, ref[h], lane & 15, kv_slots);
-    };
-    if constexpr (SC) {
+    // scored forms: this row's side of the masks and the bias
+    int row_last = 0, row_doc = -1;
+    float row_pos = 0.f, slope = 0.f;
+    constexpr bool kCap = SC == kScoreCap;
+    const float mul = kCap ? 1.0f : sl2;  // after the cap the scores are in log2 units
+    if constexpr (SC != kScoreNone) {
       const int bi = wk.bh / heads;
-      kb = bi * sc.k_batch;
       const int64_t slot = row < 16 * wk.n_own ? pref_slot(wk.own_page(row >> 4), row & 15) : q_slots;
       if (slot < q_slots) {
         const int64_t off = bi * sc.q_batch + slot;
-        if (sc.q_last) rule.last = __ldg(sc.q_last + off);
-        if (sc.q_doc) rule.doc = __ldg(sc.q_doc + off);
+        if (sc.q_last) row_last = __ldg(sc.q_last + off);
+        if (sc.q_doc) row_doc = __ldg(sc.q_doc + off);
         if (sc.slopes) row_pos = static_cast<float>(__ldg(sc.q_pos + off));
       }
-      if (sc.slopes) slope2 = __ldg(sc.slopes + wk.bh % heads) * kLog2e;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ref[h] = col_ref(0, h);
-        kc[h] = col_load(0, h);
-        ref[h] = col_ref(1, h);
-      }
+      if (sc.slopes) slope = __ldg(sc.slopes + wk.bh % heads) * kLog2e / mul;
     }
-    // after the cap or the bias the scores are in log2 units already
-    const float mul = SC && (sc.cap > 0.f || sc.slopes) ? 1.0f : sl2;
     const uint64_t mul2 = f2_pack(mul, mul);
     for (int st = 0; st < n_steps; ++st) {
       const int b = st & 1;
@@ -327,35 +469,20 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       if (halves && hh) mw[0] = mw[1];
       // mask words of the next step load while this one computes
       if (st + 1 < n_steps) raw.fetch(col_masks, wk.e0 + (st + 1) * NP, min(NP, n_cols - (st + 1) * NP), seg);
-      if constexpr (SC) {
+      if (SC != kScoreNone && use_cols) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&c_full[st % R], (st / R) & 1, ab))) {
+          ok = false;
+          break;
+        }
         if (sc.q_last || sc.q_doc) {
-          ColRange rg;
-          rg.reset();
-          rg.add(kc[0]);
-          rg.add(kc[1]);
-          rg.reduce();
-          const bool none = seg < 0 || (sc.q_last && rg.pos_min > rule.last) ||
-                            (sc.q_doc && (rule.doc < 0 || rule.doc < rg.doc_min || rule.doc > rg.doc_max));
-          const bool all = (!sc.q_last || rg.pos_max <= rule.last) && (!sc.q_doc || rg.doc_min == rg.doc_max);
+          const int4 rg = col_rng[st % R];
+          const bool none = seg < 0 || query_none(sc, rg, row_last, row_doc);
           if (none) mw[0] = mw[1] = 0u;
-          if (__any_sync(0xffffffffu, !none && !all)) {
-            const uint32_t b0 = key_bits(kc[0], sc.q_last, rule.last, sc.q_doc, rule.doc);
-            const uint32_t b1 = key_bits(kc[1], sc.q_last, rule.last, sc.q_doc, rule.doc);
-            mw[0] &= halves && hh ? b1 : b0;
-            mw[1] &= b1;
-          }
-        }
-        if (sc.slopes) {
-          __syncwarp();
-          col_pos[lane] = static_cast<float>(kc[0].pos);
-          col_pos[lane + 32] = static_cast<float>(kc[1].pos);
-          __syncwarp();
-        }
-        if (st + 1 < n_steps) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            kc[h] = col_load(st + 1, h);
-            ref[h] = col_ref(st + 2, h);
+          if (__builtin_expect(__any_sync(0xffffffffu, !none && !query_all(sc, rg, row_last)), 0)) {
+            const int c0 = halves ? 32 * hh : 0;
+            mw[0] &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + c0, col_doc(st) + c0, row_last, row_doc);
+            if (!halves)
+              mw[1] &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + 32, col_doc(st) + 32, row_last, row_doc);
           }
         }
       }
@@ -367,14 +494,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       for (int pc = 0; pc < 2; ++pc)
         if (pc * 32 < N) tmem_ld32(tmem + 64 * b + lane_off + pc * 32, sr[pc]);
       tmem_wait_ld();
-      if constexpr (SC) {
+      if constexpr (SC != kScoreNone) {
 #pragma unroll
         for (int pc = 0; pc < 2; ++pc) {
           if (pc * 32 < N) {
-            if (sc.cap > 0.f) cap_scores<false>(sr[pc], sr[pc], scale / sc.cap, sc.cap * kLog2e);
-            if (sc.slopes)
-              bias_scores(sr[pc], col_pos + (halves ? 32 * hh : 32 * pc), row_pos, sc.cap > 0.f ? 1.0f : sl2, slope2,
-                          slope2);
+            if constexpr (kCap) cap_scores<false>(sr[pc], sr[pc], sc.c);
+            if (sc.slopes) bias_scores(sr[pc], col_posf(st) + (halves ? 32 * hh : 32 * pc), row_pos, slope);
           }
         }
       }
@@ -512,48 +637,53 @@ __global__ void fill_kernel(const int32_t* __restrict__ fill, int64_t n_bh, int6
   }
 }
 
-template <int D, bool F8, bool ROUTE, bool SC>
+template <int D, bool F8, bool ROUTE, int SC>
 cudaError_t launch_fwd_r(const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
                          const ScoreArgs& sc, __nv_bfloat16* o, float* lse, const float* q_descale,
                          const float* k_descale, cudaStream_t st) {
   using C = FwdCfg<D, F8>;
-  constexpr int kSmem = C::kSmem + (SC ? C::kScoreBytes : 0);
+  constexpr int kSmem = C::kSmem + (SC != kScoreNone ? C::kScoreBytes : 0);
   cudaError_t e =
       cudaFuncSetAttribute(fwd_kernel<D, F8, ROUTE, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   if (a.n_work == 0) return cudaSuccess;
-  fwd_kernel<D, F8, ROUTE, SC><<<static_cast<unsigned>(a.n_work), kFwdThreads, kSmem, st>>>(
+  fwd_kernel<D, F8, ROUTE, SC><<<static_cast<unsigned>(a.n_work), kFwdThreads<SC>, kSmem, st>>>(
       tq, tk, tv, a.work, a.pages, a.masks, o, lse, a.own_slots, a.scale * kLog2e, a.heads, a.kv_group, q_descale,
-      k_descale, a.err, sc, a.col_slots, a.scale);
+      k_descale, a.err, sc, a.col_slots);
   return cudaGetLastError();
 }
 
-template <int D, bool F8>
+template <int D, bool F8, int SC>
+cudaError_t launch_fwd_sc(const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
+                          const ScoreArgs& sc, __nv_bfloat16* o, float* lse, const float* q_descale,
+                          const float* k_descale, cudaStream_t st) {
+  return a.route64 ? launch_fwd_r<D, F8, true, SC>(tq, tk, tv, a, sc, o, lse, q_descale, k_descale, st)
+                   : launch_fwd_r<D, F8, false, SC>(tq, tk, tv, a, sc, o, lse, q_descale, k_descale, st);
+}
+
+template <int D>
 cudaError_t launch_fwd_t(const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
-                         const ScoreArgs* sc, __nv_bfloat16* o, float* lse, const float* q_descale,
-                         const float* k_descale, cudaStream_t st) {
-  if constexpr (!F8) {
-    if (sc)
-      return a.route64 ? launch_fwd_r<D, F8, true, true>(tq, tk, tv, a, *sc, o, lse, q_descale, k_descale, st)
-                       : launch_fwd_r<D, F8, false, true>(tq, tk, tv, a, *sc, o, lse, q_descale, k_descale, st);
-  }
-  const ScoreArgs none;
-  return a.route64 ? launch_fwd_r<D, F8, true, false>(tq, tk, tv, a, none, o, lse, q_descale, k_descale, st)
-                   : launch_fwd_r<D, F8, false, false>(tq, tk, tv, a, none, o, lse, q_descale, k_descale, st);
+                         const ScoreArgs* sc, __nv_bfloat16* o, float* lse, cudaStream_t st) {
+  if (!sc) return launch_fwd_sc<D, false, kScoreNone>(tq, tk, tv, a, ScoreArgs(), o, lse, nullptr, nullptr, st);
+  if (!(sc->cap > 0.f)) return launch_fwd_sc<D, false, kScoreMask>(tq, tk, tv, a, *sc, o, lse, nullptr, nullptr, st);
+  // a bounded cap without a bias needs no running maximum (kCapFixedMax)
+  if (!sc->slopes && sc->c.cap2 <= kCapFixedMax)
+    return launch_fwd_sc<D, false, kScoreFixed>(tq, tk, tv, a, *sc, o, lse, nullptr, nullptr, st);
+  return launch_fwd_sc<D, false, kScoreCap>(tq, tk, tv, a, *sc, o, lse, nullptr, nullptr, st);
 }
 
 }  // namespace
 
 cudaError_t launch_fwd(int head_dim, const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
                        const ScoreArgs* sc, __nv_bfloat16* o, float* lse, cudaStream_t st) {
-  return head_dim == 128 ? launch_fwd_t<128, false>(tq, tk, tv, a, sc, o, lse, nullptr, nullptr, st)
-                         : launch_fwd_t<64, false>(tq, tk, tv, a, sc, o, lse, nullptr, nullptr, st);
+  return head_dim == 128 ? launch_fwd_t<128>(tq, tk, tv, a, sc, o, lse, st)
+                         : launch_fwd_t<64>(tq, tk, tv, a, sc, o, lse, st);
 }
 
 cudaError_t launch_fwd_e4m3(const TmaPages& tq8, const TmaPages& tk8, const TmaPages& tv, const TileArgs& a,
                             const float* q_descale, const float* k_descale, __nv_bfloat16* o, float* lse,
                             cudaStream_t st) {
-  return launch_fwd_t<128, true>(tq8, tk8, tv, a, nullptr, o, lse, q_descale, k_descale, st);
+  return launch_fwd_sc<128, true, kScoreNone>(tq8, tk8, tv, a, ScoreArgs(), o, lse, q_descale, k_descale, st);
 }
 
 cudaError_t launch_fill(int head_dim, const int32_t* fill, int64_t n, int64_t bh, int64_t slots,

@@ -50,9 +50,23 @@ struct TileArgs {
   bool route64 = false;
 };
 
+// tanh cap c of scores x = scale * s, in the forms the kernels use (cap_args).
+struct CapArgs {
+  float a[5];   // c log2(e) tanh(scale s / c) = s (a0 + a1 w + ... + a4 w^4), w = s^2 ...
+  float w_max;  // ... for w up to this (|scale s / c| <= 1/2)
+  float k2;     // 2 log2(e) scale / c
+  float cap2;   // c log2(e)
+  float ng;     // -1 / cap2^2
+};
+CapArgs cap_args(float cap, float scale);
+// Caps up to this (in log2 units) keep 2^z and its sums inside fp32 without a
+// running maximum: z within +-80 leaves 2^47 for values and sums.
+constexpr float kCapFixedMax = 80.0f;
+
 // Score modification (spattn_score): device arrays, null where unused.
 struct ScoreArgs {
   float cap = 0.f;                  // 0: no cap
+  CapArgs c = {};
   const float* slopes = nullptr;    // [heads]
   const int32_t* q_pos = nullptr;
   const int32_t* k_pos = nullptr;

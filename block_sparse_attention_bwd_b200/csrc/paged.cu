@@ -70,6 +70,7 @@ struct PagedArgs {
   int heads, kv_heads, group, page16;  // page16: 16-slot pages per page
   int max_q, max_kv, q_tiles, tile_rows, splits, chunk;
   float scale, cap;
+  CapArgs c;
   int* err;
 };
 
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
 #pragma unroll
       for (int pc = 0; pc < 2; ++pc) {
         if (pc * 32 < N) {
-          if (capped) cap_scores<false>(sr[pc], sr[pc], a.scale / a.cap, a.cap * kLog2e);
+          if (capped) cap_scores<false>(sr[pc], sr[pc], a.c);
           if (a.slopes) {
             // distance of column i: (last - base - 32 pc) - i, exact in fp32
             const float d0 = static_cast<float>(last - base - 32 * pc);
@@ -667,6 +668,7 @@ int spattn_paged_fwd(spattn_paged_t p, const spattn_paged_call* c, void* stream)
   a.chunk = sp.chunk;
   a.scale = L.scale;
   a.cap = L.softcap;
+  a.c = cap_args(L.softcap, L.scale);
   a.err = p->d_err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int n = static_cast<int>(c->n_seqs);

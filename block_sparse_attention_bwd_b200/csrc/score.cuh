@@ -4,12 +4,11 @@
 //   z = c tanh(x / c) - slope |pos_q - pos_k|,   x = scale q.k   (no cap: z = x - ...)
 //   allowed iff the plan's masks say so, k_pos <= q_last and q_doc == k_doc >= 0.
 //
-// A lane holds the position and document of one or two columns of the step
-// (loaded a step ahead); a row's thread reads them by shuffle when it has to
-// compare, and as fp32 from a warp's own shared-memory line for the bias, which
-// touches every pair.  Comparison per pair happens only in steps where some row of the
-// warp is neither fully allowed nor fully masked by the range of the
-// step's positions and documents.
+// The column side of a step (positions, documents, and their range over the
+// step) is written into shared memory by the warp that loads the step's tiles,
+// so that a row thread pays two compares per step while its row is fully
+// allowed or fully masked by the range, and compares pair by pair only in
+// steps where some row of its warp is neither.
 #pragma once
 
 #include "tile.cuh"
@@ -17,17 +16,12 @@
 namespace spattn {
 namespace dev {
 
-// tanh for |u| <= 1/2: u + u v Q(v), v = u^2, Q the minimax cubic of
-// (tanh(u) / u - 1) / v on [0, 1/4] (relative error 1.5e-8), all on the FMA
-// pipe.  Outside, 1 - 2 / (1 + e^2u) with two special-function operations.
-// A warp takes the first form when all of its scores of the step allow it:
-// scores well inside the cap are the ordinary case, and the softmax already
-// spends a special-function operation per pair.
-constexpr float kTanhPolyMax = 0.5f;
-constexpr float kTq0 = -0.33333149552345276f, kTq1 = 0.1332598626613617f, kTq2 = -0.05305291339755058f,
-                kTq3 = 0.017256902530789375f;
-// e^2u is held at 2^100 so that 1 - tanh^2 = 4 e r^2 (r = 1 / (1 + e)) stays finite
-constexpr float kTanhExpMax = 100.0f;
+// Forms of a scored kernel.
+//   kScoreNone   the plain kernel
+//   kScoreMask   masks and bias
+//   kScoreCap    the same with a cap
+//   kScoreFixed  (forward) a cap small enough for a fixed softmax reference, no bias
+enum : int { kScoreNone = 0, kScoreMask = 1, kScoreCap = 2, kScoreFixed = 3 };
 
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
@@ -41,67 +35,89 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return y;
 }
 
-// s (raw products) -> cap2 * tanh(s * k1), in place; k1 = scale / cap, cap2 =
-// cap * log2(e).  With GRAD also d *= 1 - tanh^2.
-template <bool GRAD>
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[32], uint32_t (&d)[32], float k1, float cap2) {
+// s (raw products) -> z = c log2(e) tanh(s scale / c) in place; with GRAD also
+// d *= 1 - tanh^2.
+//
+// While every score of the warp's step is at most half the cap, tanh is its
+// polynomial: z = s (a0 + a1 w + ... + a4 w^4), w = s^2, the coefficients of
+// tanh(u) / u on |u| <= 1/2 (relative error 1.5e-8) with scale, cap and log2(e)
+// folded in by the host: five FMA-pipe operations per pair more than a plain
+// score.  Beyond that it is 1 - 2 / (1 + e^2u) with two special-function
+// operations per pair, of which the softmax already spends one.  Scores well
+// inside the cap are the ordinary case; a warp decides per step.
+constexpr float kTanhExpMax = 100.0f;  // e^2u held at 2^100: 1 - tanh^2 = 4 e r^2, r = 1 / (1 + e), stays finite
+template <bool GRAD, int N>
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], uint32_t (&d)[N], const CapArgs& c) {
+  auto pair = [&](int i) { return f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])); };
   float mx[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    mx[0] = fmax3(mx[0], fabsf(__uint_as_float(s[i])), fabsf(__uint_as_float(s[i + 1])));
-    mx[1] = fmax3(mx[1], fabsf(__uint_as_float(s[i + 2])), fabsf(__uint_as_float(s[i + 3])));
+  for (int i = 0; i < N / 2; ++i) {
+    float a, b;
+    f2_unpack(f2_mul(pair(i), pair(i)), a, b);
+    mx[i & 1] = fmax3(mx[i & 1], a, b);  // a NaN drops out here and keeps its NaN in either form
   }
-  const bool wide = fmaxf(mx[0], mx[1]) * fabsf(k1) > kTanhPolyMax;  // a NaN score keeps its NaN in either form
-  if (!__any_sync(0xffffffffu, wide)) {
-    const uint64_t k = f2_pack(k1, k1), c2 = f2_pack(cap2, cap2);
-    const uint64_t q0 = f2_pack(kTq0, kTq0), q1 = f2_pack(kTq1, kTq1), q2 = f2_pack(kTq2, kTq2), q3 = f2_pack(kTq3, kTq3);
-    const uint64_t one = f2_pack(1.f, 1.f), m1 = f2_pack(-1.f, -1.f);
+  if (__builtin_expect(!__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > c.w_max), 1)) {
+    const uint64_t a0 = f2_pack(c.a[0], c.a[0]), a1 = f2_pack(c.a[1], c.a[1]), a2 = f2_pack(c.a[2], c.a[2]),
+                   a3 = f2_pack(c.a[3], c.a[3]), a4 = f2_pack(c.a[4], c.a[4]);
+    const uint64_t ng = f2_pack(c.ng, c.ng), one = f2_pack(1.f, 1.f);
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const uint64_t u = f2_mul(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), k);
-      const uint64_t v = f2_mul(u, u);
-      const uint64_t q = f2_fma(f2_fma(f2_fma(q3, v, q2), v, q1), v, q0);
-      const uint64_t t = f2_fma(f2_mul(u, v), q, u);
+    for (int i = 0; i < N / 2; ++i) {
+      const uint64_t x = pair(i), w = f2_mul(x, x);
+      const uint64_t z = f2_mul(x, f2_fma(f2_fma(f2_fma(f2_fma(a4, w, a3), w, a2), w, a1), w, a0));
       float a, b;
-      f2_unpack(f2_mul(t, c2), a, b);
-      s[i] = __float_as_uint(a);
-      s[i + 1] = __float_as_uint(b);
+      f2_unpack(z, a, b);
+      s[2 * i] = __float_as_uint(a);
+      s[2 * i + 1] = __float_as_uint(b);
       if constexpr (GRAD) {
-        const uint64_t g = f2_fma(f2_mul(t, m1), t, one);
-        f2_unpack(f2_mul(f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), g), a, b);
-        d[i] = __float_as_uint(a);
-        d[i + 1] = __float_as_uint(b);
+        // 1 - tanh^2 = 1 - (z / (c log2 e))^2
+        const uint64_t g = f2_fma(f2_mul(z, ng), z, one);
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), g), a, b);
+        d[2 * i] = __float_as_uint(a);
+        d[2 * i + 1] = __float_as_uint(b);
       }
     }
   } else {
-    const float k2 = k1 * (2.f * kLog2e);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float e = ex2(min_nan(__uint_as_float(s[i]) * k2, kTanhExpMax));
+    for (int i = 0; i < N; ++i) {
+      const float e = ex2(min_nan(__uint_as_float(s[i]) * c.k2, kTanhExpMax));
       const float r = rcp_approx(1.f + e);
-      s[i] = __float_as_uint(fmaf(-2.f * cap2, r, cap2));
+      s[i] = __float_as_uint(fmaf(-2.f * c.cap2, r, c.cap2));
       if constexpr (GRAD) d[i] = __float_as_uint(__uint_as_float(d[i]) * (4.f * r * (e * r)));
     }
   }
 }
 
-// s * mul - slope2 * |row - col| in place, col[i] the fp32 positions of 32
-// columns in shared memory (16-byte aligned); slope_lo is the slope of
-// columns 0..15, slope_hi that of 16..31 (the two pages may belong to two heads).
-__device__ __forceinline__ void bias_scores(uint32_t (&s)[32], const float* col, float row, float mul, float slope_lo,
-                                            float slope_hi) {
-  const uint64_t m2 = f2_pack(mul, mul), nr = f2_pack(-row, -row);
+// s - slope * |row - col| in place, col[i] the fp32 positions of the N columns
+// in shared memory (16-byte aligned).  Scores that are multiplied later (no cap)
+// come with the slope divided by that factor.
+template <int N>
+__device__ __forceinline__ void bias_scores(uint32_t (&s)[N], const float* col, float row, float slope) {
+  const uint64_t nr = f2_pack(-row, -row);
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const float sl = i < 16 ? -slope_lo : -slope_hi;
-    const uint64_t ns = f2_pack(sl, sl);
+  for (int i = 0; i < N; i += 4) {
     const float4 c = *reinterpret_cast<const float4*>(col + i);
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
-      float d0, d1, a, b;
+      float d0, d1;
       f2_unpack(f2_add(j ? f2_pack(c.z, c.w) : f2_pack(c.x, c.y), nr), d0, d1);
-      f2_unpack(f2_fma(f2_pack(fabsf(d0), fabsf(d1)), ns,
-                       f2_mul(f2_pack(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 1])), m2)),
+      s[i + j] = __float_as_uint(fmaf(-slope, fabsf(d0), __uint_as_float(s[i + j])));
+      s[i + j + 1] = __float_as_uint(fmaf(-slope, fabsf(d1), __uint_as_float(s[i + j + 1])));
+    }
+  }
+}
+
+// s * mul + col[i] in place (col: N fp32 values in shared memory).
+template <int N>
+__device__ __forceinline__ void add_columns(uint32_t (&s)[N], const float* col, float mul) {
+  const uint64_t m2 = f2_pack(mul, mul);
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float4 c = *reinterpret_cast<const float4*>(col + i);
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      float a, b;
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 1])), m2,
+                       j ? f2_pack(c.z, c.w) : f2_pack(c.x, c.y)),
                 a, b);
       s[i + j] = __float_as_uint(a);
       s[i + j + 1] = __float_as_uint(b);
@@ -109,142 +125,155 @@ __device__ __forceinline__ void bias_scores(uint32_t (&s)[32], const float* col,
   }
 }
 
-// s * mul - col[i] in place (col: 32 fp32 values in shared memory).
-__device__ __forceinline__ void sub_columns(uint32_t (&s)[32], const float* col, float mul) {
-  const uint64_t m2 = f2_pack(mul, mul);
+// dS of one row and its weights, N columns: w = 2^x (x = log2 of the weight, in
+// `s`), ds = w d, both packed to bf16.  Columns whose bit is clear get zeros, and
+// dS is dropped where the weight rounds to one (live_weight).
+__device__ __forceinline__ bool live_weight(float p);
+template <int N>
+__device__ __forceinline__ void weights_and_ds(uint32_t (&s)[N], uint32_t (&d)[N], uint32_t bits, uint32_t (&pp)[N / 2],
+                                               uint32_t (&pd)[N / 2]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const float4 c = *reinterpret_cast<const float4*>(col + i);
+  for (int i = 0; i < N; ++i) s[i] = __float_as_uint(ex2(__uint_as_float(s[i])));
+  if (__builtin_expect(bits != (N == 32 ? 0xFFFFFFFFu : (1u << (N & 31)) - 1u), 0)) {
 #pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-      float a, b;
-      f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i + j]), __uint_as_float(s[i + j + 1])), m2,
-                       j ? f2_pack(-c.z, -c.w) : f2_pack(-c.x, -c.y)),
-                a, b);
-      s[i + j] = __float_as_uint(a);
-      s[i + j + 1] = __float_as_uint(b);
+    for (int i = 0; i < N; ++i) {
+      const bool on = (bits >> i) & 1u;
+      if (!on || !live_weight(__uint_as_float(s[i]))) d[i] = 0u;
+      if (!on) s[i] = 0u;
     }
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float p0 = __uint_as_float(s[2 * i]), p1 = __uint_as_float(s[2 * i + 1]);
+    float s0, s1;
+    f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]))), s0, s1);
+    pp[i] = pack_bf16(p0, p1);
+    pd[i] = pack_bf16(s0, s1);
   }
 }
 
 // Whether a pair of weight p has a gradient: not when masked (p = 0), and not
 // when p rounds to one.  With p = 1 - e every other weight of the row is at most
 // e, so |dS| <= 2 e max |dP|, below 2^-15 of dP for e < 2^-16, while Delta (from O
-// rounded to bf16, summed in another order than dP) is off by more; a row with
-// a single key gets the exact 0.  Used where a step's mask has holes, which a
-// row with one key always has.
+// rounded to bf16, summed in another order than dP) is off by more; a query
+// with a single key gets the exact 0.  Used where a step's mask has holes, as
+// the mask of a query with one key always has in the query-owned pass.
 __device__ __forceinline__ bool live_weight(float p) { return p != 0.f && p < 1.0f - 1.52587890625e-5f; }
 
-// Position and document of one key column (lanes hold one each).  A column
-// behind the list or the tensor is left out of the ranges; the plan's masks
-// already exclude it.
-struct KeyCol {
-  int pos, doc;
-  bool live;
-  __device__ __forceinline__ void clear() {
-    pos = 0;
-    doc = -1;
-    live = false;
-  }
-};
-
-__device__ __forceinline__ KeyCol load_key_col(const ScoreArgs& sc, int64_t batch_off, bool listed, int32_t ref, int r,
-                                               int64_t slots) {
-  KeyCol k;
-  k.clear();
-  const int64_t slot = pref_slot(ref, r);
-  k.live = listed && slot < slots;
-  if (k.live) {
-    if (sc.k_pos) k.pos = __ldg(sc.k_pos + batch_off + slot);
-    if (sc.k_doc) k.doc = __ldg(sc.k_doc + batch_off + slot);
-  }
-  return k;
+// Range of the positions (or last positions) and documents of the live columns
+// of a step or half step: {min, max} of each.  No live column leaves the
+// range empty (min above max).
+__device__ __forceinline__ int4 column_range(bool live, int pos, int doc) {
+  constexpr int kLow = static_cast<int>(0x80000000), kHigh = 0x7FFFFFFF;
+  return make_int4(__reduce_min_sync(0xffffffffu, live ? pos : kHigh), __reduce_max_sync(0xffffffffu, live ? pos : kLow),
+                   __reduce_min_sync(0xffffffffu, live ? doc : kHigh), __reduce_max_sync(0xffffffffu, live ? doc : kLow));
+}
+__device__ __forceinline__ int4 range_join(int4 a, int4 b) {
+  return make_int4(min(a.x, b.x), max(a.y, b.y), min(a.z, b.z), max(a.w, b.w));
 }
 
-// What a query row allows.
-struct RowRule {
-  int last, doc;  // doc: -1 attends nothing when documents are in use
-};
+// A query row against the range of its key columns.
+__device__ __forceinline__ bool query_none(const ScoreArgs& sc, int4 r, int last, int doc) {
+  return (sc.q_last && r.x > last) || (sc.q_doc && (doc < 0 || doc < r.z || doc > r.w));
+}
+__device__ __forceinline__ bool query_all(const ScoreArgs& sc, int4 r, int last) {
+  return (!sc.q_last || r.y <= last) && (!sc.q_doc || r.z == r.w);
+}
+// A key row against the range of its query columns.
+__device__ __forceinline__ bool key_none(const ScoreArgs& sc, int4 r, int pos, int doc) {
+  return (sc.q_last && pos > r.y) || (sc.q_doc && (doc < 0 || doc < r.z || doc > r.w));
+}
+__device__ __forceinline__ bool key_all(const ScoreArgs& sc, int4 r, int pos) {
+  return (!sc.q_last || pos <= r.x) && (!sc.q_doc || r.z == r.w);
+}
 
-// Range of positions and documents over the live columns of a warp's lanes.
-struct ColRange {
-  int pos_min, pos_max, doc_min, doc_max;
-  __device__ __forceinline__ void reset() {
-    pos_min = doc_min = 0x7FFFFFFF;
-    pos_max = doc_max = static_cast<int>(0x80000000);
-  }
-  __device__ __forceinline__ void add(const KeyCol& k) {
-    if (!k.live) return;
-    pos_min = min(pos_min, k.pos);
-    pos_max = max(pos_max, k.pos);
-    doc_min = min(doc_min, k.doc);
-    doc_max = max(doc_max, k.doc);
-  }
-  __device__ __forceinline__ void reduce() {
-    pos_min = __reduce_min_sync(0xffffffffu, pos_min);
-    pos_max = __reduce_max_sync(0xffffffffu, pos_max);
-    doc_min = __reduce_min_sync(0xffffffffu, doc_min);
-    doc_max = __reduce_max_sync(0xffffffffu, doc_max);
-  }
-};
-
-// One query column of the key-owned pass: what it allows, and its LSE.
-struct QueryCol {
-  int last, doc;
-  float pos, lse2, slope2;
-  bool live;
-};
-
-// Range of the live columns' rules over a warp's lanes.
-struct QueryRange {
-  int last_min, last_max, doc_min, doc_max;
-  __device__ __forceinline__ void of(const QueryCol& q) {
-    last_min = __reduce_min_sync(0xffffffffu, q.live ? q.last : 0x7FFFFFFF);
-    last_max = __reduce_max_sync(0xffffffffu, q.live ? q.last : static_cast<int>(0x80000000));
-    doc_min = __reduce_min_sync(0xffffffffu, q.live ? q.doc : 0x7FFFFFFF);
-    doc_max = __reduce_max_sync(0xffffffffu, q.live ? q.doc : static_cast<int>(0x80000000));
-  }
-};
-
-// Columns (of 32, one per lane) that may attend this thread's key row.
-__device__ __forceinline__ uint32_t query_bits(const QueryCol& q, bool use_pos, int pos, bool use_doc, int doc) {
+// Bits of N columns for one row.  KEYS: the columns are keys (position <=
+// `mine`), else queries (`mine` <= their last position).
+template <bool KEYS, int N>
+__device__ __forceinline__ uint32_t column_bits(bool use_pos, bool use_doc, const int* pos, const int* doc, int mine,
+                                             int my_doc) {
   uint32_t bits = 0xFFFFFFFFu;
   if (use_pos) {
     uint32_t b = 0u;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (pos <= __shfl_sync(0xffffffffu, q.last, i)) b |= 1u << i;
+    for (int i = 0; i < N; i += 4) {
+      const int4 c = *reinterpret_cast<const int4*>(pos + i);
+      b |= (KEYS ? c.x <= mine : mine <= c.x) ? 1u << i : 0u;
+      b |= (KEYS ? c.y <= mine : mine <= c.y) ? 2u << i : 0u;
+      b |= (KEYS ? c.z <= mine : mine <= c.z) ? 4u << i : 0u;
+      b |= (KEYS ? c.w <= mine : mine <= c.w) ? 8u << i : 0u;
+    }
     bits = b;
   }
   if (use_doc) {
     uint32_t b = 0u;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (__shfl_sync(0xffffffffu, q.doc, i) == doc) b |= 1u << i;
-    bits &= doc >= 0 ? b : 0u;
+    for (int i = 0; i < N; i += 4) {
+      const int4 c = *reinterpret_cast<const int4*>(doc + i);
+      b |= c.x == my_doc ? 1u << i : 0u;
+      b |= c.y == my_doc ? 2u << i : 0u;
+      b |= c.z == my_doc ? 4u << i : 0u;
+      b |= c.w == my_doc ? 8u << i : 0u;
+    }
+    bits &= my_doc >= 0 ? b : 0u;
   }
   return bits;
 }
 
-// Columns (of 32, one per lane) that the row of this thread may attend: bit i
-// set iff column i's position is at most `last` and its document is `doc`.
-__device__ __forceinline__ uint32_t key_bits(const KeyCol& k, bool use_pos, int last, bool use_doc, int doc) {
-  uint32_t bits = 0xFFFFFFFFu;
-  if (use_pos) {
-    uint32_t b = 0u;
+// ----------------------------------------------------------------------------
+// Softmax of one step in the scored forward forms
+// ----------------------------------------------------------------------------
+// The fixed form has two threads per row: group g (0, 1) has 32 of the step's 64
+// columns, so that four row warps per scheduler (two CTAs) cover each other's
+// latency and a thread's code is half as long.  They meet once, at the end.
+// (With a running maximum they would exchange their halves' maxima every step;
+// that exchange cost more than the second thread gave, so those forms keep one.)
+struct SoftRow {
+  float l = 0.f;   // sum of this thread's weights
+  float lr = 0.f;  // the same of the weights rounded to bf16
+};
+
+// Meeting of the two warps of a row pair (a barrier of 64 arrivals).  A bounded
+// wait, so that a warp that gave up cannot strand its partner; false when the CTA
+// is aborting.
+__device__ __forceinline__ bool pair_sync(uint64_t* bar, const Abort& ab) {
+  mbar_arrive(bar);
+  return __all_sync(0xffffffffu, mbar_wait(bar, 0, ab));
+}
+
+// Weights 2^s of this thread's 32 columns to P (bf16, TMEM) and their sums.
+__device__ __forceinline__ void soft_weights(const uint32_t (&s)[32], SoftRow& r, uint32_t p_addr) {
+  uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)}, sumr[2] = {sum[0], sum[1]};
+  uint32_t pk[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (__shfl_sync(0xffffffffu, k.pos, i) <= last) b |= 1u << i;
-    bits = b;
+  for (int i = 0; i < 16; ++i) {
+    const float p0 = ex2(__uint_as_float(s[2 * i])), p1 = ex2(__uint_as_float(s[2 * i + 1]));
+    sum[i & 1] = f2_add(sum[i & 1], f2_pack(p0, p1));
+    pk[i] = pack_bf16(p0, p1);
+    sumr[i & 1] = f2_add(sumr[i & 1], f2_pack(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xFFFF0000u)));
   }
-  if (use_doc) {
-    uint32_t b = 0u;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (__shfl_sync(0xffffffffu, k.doc, i) == doc) b |= 1u << i;
-    bits &= doc >= 0 ? b : 0u;
-  }
-  return bits;
+  tmem_st16(p_addr, pk);
+  float a0, a1, b0, b1;
+  f2_unpack(sum[0], a0, a1);
+  f2_unpack(sum[1], b0, b1);
+  r.l += (a0 + a1) + (b0 + b1);
+  f2_unpack(sumr[0], a0, a1);
+  f2_unpack(sumr[1], b0, b1);
+  r.lr += (a0 + a1) + (b0 + b1);
+}
+
+// Sums of both threads of the row (xsum: this row's entries of [4][128] floats).
+// `l`, the divisor of O, sums the rounded weights: no weight is 1 in this form, so
+// a row with few keys would keep its weights' rounding otherwise.  l_true is
+// the sum in LSE.
+__device__ __forceinline__ bool soft_total(const SoftRow& r, float* xsum, int grp, uint64_t* bar, const Abort& ab,
+                                           float& l, float& l_true) {
+  xsum[128 * grp] = r.l;
+  xsum[256 + 128 * grp] = r.lr;
+  if (!pair_sync(bar, ab)) return false;
+  l_true = xsum[0] + xsum[128];
+  l = xsum[256] + xsum[256 + 128];
+  return true;
 }
 
 }  // namespace dev

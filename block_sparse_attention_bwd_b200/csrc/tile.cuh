@@ -139,18 +139,22 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-// Store 32 fp32 values (times `mul`) of one row as bf16 to global memory.
-__device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (&r)[32], float mul, bool zero) {
-  uint32_t pk[16];
+// Store N fp32 values (times `mul`) of one row as bf16 to global memory.
+template <int N>
+__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint32_t (&r)[N], float mul, bool zero) {
+  uint32_t pk[N / 2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < N / 2; ++i) {
     const float a = zero ? 0.f : __uint_as_float(r[2 * i]) * mul;
     const float b = zero ? 0.f : __uint_as_float(r[2 * i + 1]) * mul;
     pk[i] = pack_bf16(a, b);
   }
   uint4* d = reinterpret_cast<uint4*>(dst);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) d[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+  for (int i = 0; i < N / 8; ++i) d[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+}
+__device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (&r)[32], float mul, bool zero) {
+  store_row(dst, r, mul, zero);
 }
 
 }  // namespace dev
