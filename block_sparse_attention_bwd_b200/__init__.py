@@ -68,12 +68,13 @@ class _Score(ctypes.Structure):
 
 
 class _RopeLayout(ctypes.Structure):
+    # the stride arrays of spattn_rope_layout, element by element
     _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "batch", "heads", "kv_heads", "head_dim", "rot_dim",
                                               "interleaved", "inverse")] + [
-        ("slots", ctypes.c_int64)] + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "q_out_stride",
-                                                                       "k_out_stride")] + [
-        ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3), ("pos_batch_stride", ctypes.c_int64),
-        ("mscale", ctypes.c_float)]
+        ("slots", ctypes.c_int64)] + [(f"{n}{i}", ctypes.c_int64) for n in ("q_stride", "k_stride", "q_out_stride",
+                                                                           "k_out_stride") for i in range(3)] + [
+        ("n_axes", ctypes.c_int32), ("section0", ctypes.c_int32), ("section1", ctypes.c_int32),
+        ("section2", ctypes.c_int32), ("pos_batch_stride", ctypes.c_int64), ("mscale", ctypes.c_float)]
 
 
 class _PagedLayout(ctypes.Structure):
@@ -397,28 +398,37 @@ class Score:
         self.slopes, self.q_pos, self.k_pos, self.q_last, self.q_doc, self.k_doc = slopes, q_pos, k_pos, q_last, q_doc, k_doc
 
     def _c_struct(self, plan: Plan, device) -> _Score:
-        import torch
-
-        c = _Score(softcap=self.softcap, batches=1)
+        torch = _torch()
+        i32 = torch.int32
+        ptrs, dims = [], 0
         if self.slopes is not None:
-            _need(self.slopes, "slopes", (plan.heads,), torch.float32)
-            _same_device(self.slopes, "slopes", device)
-            c.slopes = self.slopes.data_ptr()
-        dims = set()
-        for name, slots in (("q_pos", plan.q_slots), ("k_pos", plan.kv_slots), ("q_last", plan.q_slots),
-                            ("q_doc", plan.q_slots), ("k_doc", plan.kv_slots)):
-            t = getattr(self, name)
+            _want(self.slopes, "slopes", (plan.heads,), torch.float32, device)
+        for name, t, slots in (("q_pos", self.q_pos, plan.q_slots), ("k_pos", self.k_pos, plan.kv_slots),
+                               ("q_last", self.q_last, plan.q_slots), ("q_doc", self.q_doc, plan.q_slots),
+                               ("k_doc", self.k_doc, plan.kv_slots)):
             if t is None:
+                ptrs.append(None)
                 continue
             batched = isinstance(t, torch.Tensor) and t.dim() == 2
-            _need(t, name, (plan.batch, slots) if batched else (slots,), torch.int32)
-            _same_device(t, name, device)
-            dims.add(batched)
-            setattr(c, name, t.data_ptr())
-        if len(dims) > 1:
+            _want(t, name, (plan.batch, slots) if batched else (slots,), i32, device)
+            dims |= 2 if batched else 1
+            ptrs.append(t.data_ptr())
+        if dims == 3:
             raise ValueError("score arrays: either all or none have a batch dimension")
-        c.batches = plan.batch if dims == {True} else 1
-        return c
+        return _Score(self.softcap, None if self.slopes is None else self.slopes.data_ptr(), *ptrs,
+                      plan.batch if dims == 2 else 1)
+
+
+_TORCH = None
+
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+
+        _TORCH = torch
+    return _TORCH
 
 
 def _same_device(t, name, device):
@@ -426,50 +436,76 @@ def _same_device(t, name, device):
         raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
 
 
+def _want(t, name, shape, dtype, device):
+    """_need, and on the given device."""
+    if not isinstance(t, _torch().Tensor) or t.dtype is not dtype or t.device != device or t.shape != shape \
+            or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _raw_stream(stream, device):
+    """The stream's handle; without one, the current stream of ``device``."""
+    torch = _torch()
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _device_of(t, name):
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return t.device
+
+
 def spattn_fwd_scored(q, k, v, plan: Plan, score: Score, o=None, lse=None, stream=None):
     """O [B,H,Sq,D] bf16 and LSE [B,H,Sq] fp32 for the plan's sparse graph with modified scores."""
-    import torch
-
+    torch = _torch()
+    dev, bf16 = _device_of(q, "q"), torch.bfloat16
     qs = (plan.batch, plan.heads, plan.q_slots, plan.head_dim)
     ks = (plan.batch, plan.kv_heads, plan.kv_slots, plan.head_dim)
-    _need(q, "q", qs, torch.bfloat16)
-    _need(k, "k", ks, torch.bfloat16)
-    _need(v, "v", ks, torch.bfloat16)
-    sc = score._c_struct(plan, q.device)
+    _want(q, "q", qs, bf16, dev)
+    _want(k, "k", ks, bf16, dev)
+    _want(v, "v", ks, bf16, dev)
+    sc = score._c_struct(plan, dev)
     if o is None:
-        o = torch.empty(qs, dtype=torch.bfloat16, device=q.device)
+        o = torch.empty(qs, dtype=bf16, device=dev)
+    else:
+        _want(o, "o", qs, bf16, dev)
     if lse is None:
-        lse = torch.empty(qs[:3], dtype=torch.float32, device=q.device)
-    _need(o, "o", qs, torch.bfloat16)
-    _need(lse, "lse", qs[:3], torch.float32)
-    for t, nm in ((k, "k"), (v, "v"), (o, "o"), (lse, "lse")):
-        _same_device(t, nm, q.device)
-    _check(_lib().spattn_fwd_scored(_ptr(q), _ptr(k), _ptr(v), plan.handle, ctypes.byref(sc), _ptr(o), _ptr(lse),
-                                    _stream_handle(stream)), "spattn_fwd_scored")
+        lse = torch.empty(qs[:3], dtype=torch.float32, device=dev)
+    else:
+        _want(lse, "lse", qs[:3], torch.float32, dev)
+    _check(_lib().spattn_fwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), plan.handle, ctypes.byref(sc),
+                                    o.data_ptr(), lse.data_ptr(), _raw_stream(stream, dev)), "spattn_fwd_scored")
     return o, lse
 
 
 def spattn_bwd_scored(q, k, v, o, lse, do, plan: Plan, score: Score, dq=None, dk=None, dv=None, stream=None):
     """dQ, dK, dV (bf16) of :func:`spattn_fwd_scored` with the same score, given its O and LSE and the loss gradient dO."""
-    import torch
-
+    torch = _torch()
+    dev, bf16 = _device_of(q, "q"), torch.bfloat16
     qs = (plan.batch, plan.heads, plan.q_slots, plan.head_dim)
     ks = (plan.batch, plan.kv_heads, plan.kv_slots, plan.head_dim)
-    for t, nm, sh in ((q, "q", qs), (k, "k", ks), (v, "v", ks), (o, "o", qs), (do, "do", qs)):
-        _need(t, nm, sh, torch.bfloat16)
-    _need(lse, "lse", qs[:3], torch.float32)
-    sc = score._c_struct(plan, q.device)
-    dq = torch.empty(qs, dtype=torch.bfloat16, device=q.device) if dq is None else dq
-    dk = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dk is None else dk
-    dv = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dv is None else dv
-    _need(dq, "dq", qs, torch.bfloat16)
-    _need(dk, "dk", ks, torch.bfloat16)
-    _need(dv, "dv", ks, torch.bfloat16)
-    for t, nm in ((k, "k"), (v, "v"), (o, "o"), (lse, "lse"), (do, "do"), (dq, "dq"), (dk, "dk"), (dv, "dv")):
-        _same_device(t, nm, q.device)
-    _check(_lib().spattn_bwd_scored(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), plan.handle,
-                                    ctypes.byref(sc), _ptr(dq), _ptr(dk), _ptr(dv), _stream_handle(stream)),
-           "spattn_bwd_scored")
+    _want(q, "q", qs, bf16, dev)
+    _want(k, "k", ks, bf16, dev)
+    _want(v, "v", ks, bf16, dev)
+    _want(o, "o", qs, bf16, dev)
+    _want(do, "do", qs, bf16, dev)
+    _want(lse, "lse", qs[:3], torch.float32, dev)
+    sc = score._c_struct(plan, dev)
+    if dq is None:
+        dq = torch.empty(qs, dtype=bf16, device=dev)
+    else:
+        _want(dq, "dq", qs, bf16, dev)
+    if dk is None:
+        dk = torch.empty(ks, dtype=bf16, device=dev)
+    else:
+        _want(dk, "dk", ks, bf16, dev)
+    if dv is None:
+        dv = torch.empty(ks, dtype=bf16, device=dev)
+    else:
+        _want(dv, "dv", ks, bf16, dev)
+    _check(_lib().spattn_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                    do.data_ptr(), plan.handle, ctypes.byref(sc), dq.data_ptr(), dk.data_ptr(),
+                                    dv.data_ptr(), _raw_stream(stream, dev)), "spattn_bwd_scored")
     return dq, dk, dv
 
 
@@ -519,82 +555,90 @@ def _span(t):
     return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
 
 
+def _rope_rows(t, what, name, dtype, device, shape=None):
+    """Checks a [B, H, S, D] tensor of a rope call."""
+    if not isinstance(t, _torch().Tensor) or t.dim() != 4 or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name}: {what} must be a {dtype} tensor [B, H, S, D] on {device}, as q is")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: {what} must have shape {tuple(shape)}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: {what} must be contiguous in its last dimension")
+
+
+def _rope_overlaps(name, ins, outs):
+    """Refuses outputs that overlap an input without being in place of it."""
+    own = [y.data_ptr() == x.data_ptr() and all(a == b or n == 1 for a, b, n in zip(x.stride(), y.stride(), x.shape))
+           for x, y in zip(ins, outs)]
+    for i, y in enumerate(outs):
+        if any(n > 1 and st == 0 for n, st in zip(y.shape, y.stride())):
+            raise ValueError(f"{name}: an output has elements that share an address")
+        for j, x in enumerate(ins):
+            (a0, a1), (b0, b1) = _span(y), _span(x)
+            # views of one packed buffer interleave; both in place is the case that is allowed
+            if a0 < b1 and b0 < a1 and not (own[i] and (i == j or own[j])):
+                raise ValueError(f"{name}: an output overlaps an input without being in place of it")
+    if len(outs) == 2 and outs[0].data_ptr() == outs[1].data_ptr():
+        raise ValueError(f"{name}: the two outputs share an address")
+
+
 def _rope(name, inverse, q, k, pos, freqs, rot_dim, interleaved, sections, mscale, q_out, k_out, stream):
-    import torch
-
-    types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-
-    def rows(t, what, shape=None):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4 or t.dtype not in types:
-            raise ValueError(f"{name}: {what} must be a CUDA bf16, fp16 or fp32 tensor [B, H, S, D]")
-        if t.shape[3] > 1 and t.stride(3) != 1:
-            raise ValueError(f"{name}: {what} must be contiguous in its last dimension")
-        if shape is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name}: {what} must have shape {tuple(shape)}")
-        if t.dtype != q.dtype or t.device != q.device:
-            raise ValueError(f"{name}: {what} must have the type and device of q")
-
-    rows(q, "q")
+    torch = _torch()
+    dev, dt = _device_of(q, f"{name}: q"), q.dtype
+    code = 0 if dt is torch.bfloat16 else 1 if dt is torch.float16 else 2 if dt is torch.float32 else None
+    if code is None:
+        raise ValueError(f"{name}: q must be bf16, fp16 or fp32")
+    _rope_rows(q, "q", name, dt, dev)
     B, H, S, D = q.shape
-    if H < 1 or D < 1:
-        raise ValueError(f"{name}: q must have at least one head and one element per row")
+    Hk = 0
     if k is not None:
-        rows(k, "k", (B, k.shape[1], S, D) if isinstance(k, torch.Tensor) and k.dim() == 4 else None)
-        if k.shape[1] < 1:
-            raise ValueError(f"{name}: k must have at least one head")
+        _rope_rows(k, "k", name, dt, dev)
+        Hk = k.shape[1]
+        if k.shape != (B, Hk, S, D) or Hk < 1:
+            raise ValueError(f"{name}: k must have shape {(B, 'heads', S, D)}")
     elif k_out is not None:
         raise ValueError(f"{name}: an output for k without k")
+    if H < 1 or D < 1:
+        raise ValueError(f"{name}: q must have at least one head and one element per row")
     rot = D if rot_dim is None else int(rot_dim)
     if rot < 0 or rot > D or rot % 2:
         raise ValueError(f"{name}: rot_dim must be even and between 0 and {D}")
-    sec = [rot // 2] if sections is None else [int(n) for n in sections]
-    if not 1 <= len(sec) <= 3 or any(n < 0 for n in sec) or sum(sec) != rot // 2:
-        raise ValueError(f"{name}: sections must be one to three counts that sum to rot_dim / 2 = {rot // 2}")
-    if not isinstance(pos, torch.Tensor) or pos.dtype != torch.int32 or pos.device != q.device or not pos.is_contiguous():
-        raise ValueError(f"{name}: pos must be a contiguous int32 tensor on {q.device}")
-    want = ((S,), (len(sec), S), (B, len(sec), S))
-    if tuple(pos.shape) not in (want if len(sec) == 1 else want[1:]):
-        raise ValueError(f"{name}: pos must have shape {want[1]} or {want[2]}" + (f" or {want[0]}" if len(sec) == 1 else ""))
-    if not isinstance(freqs, torch.Tensor) or freqs.dtype != torch.float64 or freqs.device != q.device \
-            or not freqs.is_contiguous() or tuple(freqs.shape) != (rot // 2,):
-        raise ValueError(f"{name}: freqs must be a contiguous fp64 tensor [{rot // 2}] on {q.device}")
-    ins, outs = [q] + ([k] if k is not None else []), []
-    with torch.cuda.device(q.device):
-        for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
-            if x is None:
-                continue
-            if y is None:
-                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            rows(y, f"the output for {what}", x.shape)
-            if any(n > 1 and st == 0 for n, st in zip(y.shape, y.stride())):
-                raise ValueError(f"{name}: the output for {what} has elements that share an address")
-            outs.append(y)
-        own = [y.data_ptr() == x.data_ptr() and all(a == b or n == 1 for a, b, n in zip(x.stride(), y.stride(), x.shape))
-               for x, y in zip(ins, outs)]
-        if q.numel():
-            for i, y in enumerate(outs):
-                for j, x in enumerate(ins):
-                    (a0, a1), (b0, b1) = _span(y), _span(x)
-                    # views of one packed buffer interleave; both in place is the case that is allowed
-                    if a0 < b1 and b0 < a1 and not (own[i] and (i == j or own[j])):
-                        raise ValueError(f"{name}: an output overlaps an input without being in place of it")
-            if len(outs) == 2 and outs[0].data_ptr() == outs[1].data_ptr():
-                raise ValueError(f"{name}: the two outputs share an address")
-        lay = _RopeLayout(dtype=types[q.dtype], batch=B, heads=H, kv_heads=0 if k is None else k.shape[1], head_dim=D,
-                          rot_dim=rot, interleaved=int(bool(interleaved)), inverse=int(inverse), slots=S,
-                          n_axes=len(sec), pos_batch_stride=len(sec) * S if pos.dim() == 3 else 0,
-                          mscale=float(mscale))
-        for i, n in enumerate(sec):
-            lay.sections[i] = n
-        for field, t in (("q_stride", q), ("k_stride", k), ("q_out_stride", outs[0]),
-                         ("k_out_stride", outs[1] if len(outs) > 1 else None)):
-            for i in range(3):
-                getattr(lay, field)[i] = 0 if t is None else t.stride(i)
-        null = ctypes.c_void_p()
-        _check(_lib().spattn_rope(ctypes.byref(lay), _ptr(q), null if k is None else _ptr(k), _ptr(pos), _ptr(freqs),
-                                  _ptr(outs[0]), null if k is None else _ptr(outs[1]), _stream_handle(stream)),
-               "spattn_rope")
-    return outs[0], outs[1] if len(outs) > 1 else None
+    pairs = rot // 2
+    sec = (pairs,) if sections is None else tuple(int(n) for n in sections)
+    axes = len(sec)
+    if not 1 <= axes <= 3 or min(sec) < 0 or sum(sec) != pairs:
+        raise ValueError(f"{name}: sections must be one to three counts that sum to rot_dim / 2 = {pairs}")
+    if not isinstance(pos, torch.Tensor) or pos.dtype is not torch.int32 or pos.device != dev \
+            or not pos.is_contiguous() or not (pos.shape == (axes, S) or pos.shape == (B, axes, S)
+                                               or (axes == 1 and pos.shape == (S,))):
+        raise ValueError(f"{name}: pos must be a contiguous int32 tensor {(axes, S)} or {(B, axes, S)}"
+                         + (f" or {(S,)}" if axes == 1 else "") + f" on {dev}")
+    _want(freqs, f"{name}: freqs", (pairs,), torch.float64, dev)
+    given = q_out is not None or k_out is not None
+    if q_out is None:
+        q_out = torch.empty((B, H, S, D), dtype=dt, device=dev)
+    else:
+        _rope_rows(q_out, "the output for q", name, dt, dev, (B, H, S, D))
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty((B, Hk, S, D), dtype=dt, device=dev)
+        else:
+            _rope_rows(k_out, "the output for k", name, dt, dev, (B, Hk, S, D))
+    if given and q.numel():
+        _rope_overlaps(name, [q] if k is None else [q, k], [q_out] if k is None else [q_out, k_out])
+    sec3 = sec + (0,) * (3 - axes)
+    zero = (0, 0, 0)
+    lay = _RopeLayout(code, B, H, Hk, D, rot, 1 if interleaved else 0, 1 if inverse else 0, S, *q.stride()[:3],
+                      *(k.stride()[:3] if Hk else zero), *q_out.stride()[:3], *(k_out.stride()[:3] if Hk else zero),
+                      axes, *sec3, axes * S if pos.dim() == 3 else 0, mscale)
+    args = (ctypes.byref(lay), q.data_ptr(), k.data_ptr() if Hk else None, pos.data_ptr(), freqs.data_ptr(),
+            q_out.data_ptr(), k_out.data_ptr() if Hk else None, _raw_stream(stream, dev))
+    if torch.cuda.current_device() == dev.index:
+        status = _lib().spattn_rope(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = _lib().spattn_rope(*args)
+    _check(status, "spattn_rope")
+    return q_out, k_out
 
 
 def rope(q, k, pos, freqs, *, rot_dim=None, interleaved=False, sections=None, mscale=1.0, q_out=None, k_out=None,
@@ -672,56 +716,58 @@ def spattn_paged_fwd(q, k_cache, v_cache, page_table, q_start, kv_len, paged: Pa
     (undefined in the tensors that the call makes itself).  ``workspace``: a uint8
     CUDA tensor of ``paged.workspace_bytes(n)`` bytes; by default the call allocates one.
     """
-    import torch
-
+    torch = _torch()
     H, Hk, D, ps = paged.heads, paged.kv_heads, paged.head_dim, paged.page_slots
-    dev = q.device
-    if not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[1] != H or q.shape[2] != D \
-            or q.stride(2) != 1:
+    dev, bf16, i32 = _device_of(q, "q"), torch.bfloat16, torch.int32
+    if q.dtype is not bf16 or q.dim() != 3 or q.shape[1:] != (H, D) or q.stride(2) != 1:
         raise ValueError(f"q: expected a CUDA bf16 tensor [tokens, {H}, {D}], contiguous in its last dimension")
     T = q.shape[0]
+    pages = k_cache.shape[0] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else -1
     strides = []
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.device != dev or t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape[1:] != (ps, Hk, D) \
-                or t.stride(3) != 1 or t.shape[0] != k_cache.shape[0]:
+        if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype is not bf16 or t.shape != (pages, ps, Hk, D) \
+                or t.stride(3) != 1:
             raise ValueError(f"{name}: expected a bf16 tensor [pages, {ps}, {Hk}, {D}] on {dev}, contiguous in its "
                              "last dimension")
-        if t.shape[0] > 1 and t.stride(0) != ps * t.stride(1):
+        st = t.stride()
+        if pages > 1 and st[0] != ps * st[1]:
             raise ValueError(f"{name}: pages must follow each other (page stride = {ps} slot strides)")
-        strides += [t.stride(1), t.stride(2) if Hk > 1 else 0]
-    n = kv_len.shape[0] if kv_len.dim() == 1 else -1
-    if page_table.dim() != 2 or page_table.shape[0] != n:
-        raise ValueError(f"page_table: expected an int32 tensor [{max(n, 0)}, pages]")
-    for t, name, shape in ((page_table, "page_table", tuple(page_table.shape)), (q_start, "q_start", (n + 1,)),
-                           (kv_len, "kv_len", (n,))):
-        _need(t, name, shape, torch.int32)
-        _same_device(t, name, dev)
-    if paged.slopes is not None:
-        _same_device(paged.slopes, "slopes", dev)
+        strides += [st[1], st[2] if Hk > 1 else 0]
+    if not isinstance(kv_len, torch.Tensor) or kv_len.dim() != 1:
+        raise ValueError("kv_len: expected an int32 tensor [sequences]")
+    n = kv_len.shape[0]
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError(f"page_table: expected an int32 tensor [{n}, pages]")
+    width = page_table.shape[1]
+    _want(page_table, "page_table", (n, width), i32, dev)
+    _want(q_start, "q_start", (n + 1,), i32, dev)
+    _want(kv_len, "kv_len", (n,), i32, dev)
+    slopes = paged.slopes
+    if slopes is not None:
+        _want(slopes, "slopes", (H,), torch.float32, dev)
     if o is None:
-        o = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+        o = torch.empty((T, H, D), dtype=bf16, device=dev)
     else:
-        _need(o, "o", (T, H, D), torch.bfloat16)
-        _same_device(o, "o", dev)
+        _want(o, "o", (T, H, D), bf16, dev)
     if lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=dev)
     else:
-        _need(lse, "lse", (T, H), torch.float32)
-        _same_device(lse, "lse", dev)
+        _want(lse, "lse", (T, H), torch.float32, dev)
     need = paged.workspace_bytes(n)
     if workspace is None:
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             if stream is not None:
                 workspace.record_stream(stream)
-    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or workspace.dtype is not torch.uint8 \
+            or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous uint8 tensor on {dev}")
     c = _PagedCall(q.data_ptr(), q.stride(0), q.stride(1), T, k_cache.data_ptr(), v_cache.data_ptr(), *strides,
-                   k_cache.shape[0], page_table.data_ptr(), page_table.shape[1], n, q_start.data_ptr(),
-                   kv_len.data_ptr(), None if paged.slopes is None else paged.slopes.data_ptr(), o.data_ptr(),
-                   lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+                   pages, page_table.data_ptr(), width, n, q_start.data_ptr(), kv_len.data_ptr(),
+                   None if slopes is None else slopes.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                   None if workspace is None else workspace.data_ptr(),
                    0 if workspace is None else workspace.numel())
-    _check(_lib().spattn_paged_fwd(paged.handle, ctypes.byref(c), _stream_handle(stream)), "spattn_paged_fwd")
+    _check(_lib().spattn_paged_fwd(paged.handle, ctypes.byref(c), _raw_stream(stream, dev)), "spattn_paged_fwd")
     return o, lse
 
 

@@ -23,6 +23,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -41,17 +42,31 @@ using namespace dev;
 constexpr int kStepKeys = 64;
 constexpr int kStep16 = kStepKeys / 16;
 constexpr int kStageChunk = kStepKeys * 128;
-constexpr int kPagedThreads = 192;
 constexpr float kRescale = 8.0f;  // rescale O when the running maximum grows by more than 2^8, as in the plan's forward
 
-template <int D>
+// FORM: kScoreMask (no cap) and kScoreCap run with a running maximum, one thread
+// per row; kScoreFixed (a cap within kCapFixedMax) has a fixed reference and two
+// threads per row (score.cuh).
+// SMALL: tiles of at most 32 rows (decoding).  Q then takes 4 KB per chunk, not 16,
+// and the K and V rings are a stage deeper: with one warp of rows memory sets the
+// pace, and it needs the bytes in flight.  The tensor core still reads 128 rows,
+// the other 96 from the stages behind Q; their products land in lanes nothing reads.
+template <int D, int FORM, bool SMALL>
 struct PagedCfg {
   static constexpr int kNch = D / 64;
-  static constexpr int kTile = kNch * kChunkBytes;
+  static constexpr int kQChunk = SMALL ? 32 * 128 : kChunkBytes;
+  static constexpr int kTile = kNch * kQChunk;
   static constexpr int kStage = kNch * kStageChunk;
-  static constexpr int kKStages = D == 128 ? 2 : 4;
-  static constexpr int kVStages = D == 128 ? 2 : 4;
-  static constexpr int kSmem = kTile + (kKStages + kVStages) * kStage + 1024 + 512;
+  static constexpr int kKStages = D == 128 ? (SMALL ? 3 : 2) : (SMALL ? 6 : 4);
+  static constexpr int kVStages = kKStages;
+  static constexpr int kRowThreads = FORM == kScoreFixed ? 256 : 128;
+  static constexpr int kThreads = 64 + kRowThreads;
+  static constexpr int kRamp = 384;   // barriers, TMEM slot and abort flag, then the ramp of a step's columns
+  static constexpr int kBars = kRamp + kStepKeys * 4;
+  static constexpr int kPairs = FORM == kScoreFixed ? 4 * 128 * 4 + 4 * 8 : 0;  // sums and barriers of the row pairs
+  static constexpr int kSmem = kTile + (kKStages + kVStages) * kStage + 1024 + kBars + kPairs;
+  static_assert((7 + 2 * (kKStages + kVStages) + 1) * 8 + 8 <= kRamp, "barriers end before the ramp");
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
 struct PagedArgs {
@@ -65,7 +80,7 @@ struct PagedArgs {
   __nv_bfloat16* o;
   float* lse;
   const float* slopes;
-  float* part;  // [tile][split][tile_rows][D], then (maximum, sum) pairs in the same order
+  float* part;  // [tile][split][tile_rows][D], then (reference, sum, divisor, 0) in the same order
   int64_t n_pages;
   int heads, kv_heads, group, page16;  // page16: 16-slot pages per page
   int max_q, max_kv, q_tiles, tile_rows, splits, chunk;
@@ -96,10 +111,11 @@ __device__ __forceinline__ int tile_keys(const PagedArgs& a, const Seq& s, int q
   return s.kv - s.nq + last + 1;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kPagedThreads, 2)
+template <int D, int FORM, bool SMALL>
+__global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
     paged_kernel(const __grid_constant__ TmaPages tm_k, const __grid_constant__ TmaPages tm_v, const PagedArgs a) {
-  using C = PagedCfg<D>;
+  using C = PagedCfg<D, FORM, SMALL>;
+  constexpr bool kFixed = FORM == kScoreFixed, kCap = kFixed || FORM == kScoreCap;
   constexpr int KS = C::kKStages, VS = C::kVStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -120,6 +136,9 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(o_last + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   const Abort ab{abort_flag, a.err};
+  float* ramp = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + C::kRamp);  // 0, 1, .. 63
+  float* xrow = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + C::kBars);
+  uint64_t* pair_bar = reinterpret_cast<uint64_t*>(xrow + 4 * 128);  // [4]
 
   const int qt = blockIdx.x / a.splits, split = blockIdx.x - qt * a.splits;
   const int hk = blockIdx.y, sq = blockIdx.z;
@@ -138,7 +157,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    mbar_init(q_full, 32 * row_warps);
+    mbar_init(q_full, 32 * row_warps);  // group 0 of the row threads loads Q
     for (int s = 0; s < KS; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
@@ -149,13 +168,16 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], 32 * row_warps);
+      mbar_init(&p_full[b], (kFixed ? 64 : 32) * row_warps);
     }
     mbar_init(o_done, 1);
     mbar_init(drain, 1);
     mbar_init(o_last, 1);
+    if constexpr (kFixed)
+      for (int i = 0; i < 4; ++i) mbar_init(&pair_bar[i], 64);
     fence_barrier_init();
   }
+  if (threadIdx.x < kStepKeys) ramp[threadIdx.x] = static_cast<float>(threadIdx.x);
   if (warp == 1) tmem_alloc(tslot, 256);
   tc_fence_before();
   __syncthreads();
@@ -237,7 +259,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
 #pragma unroll
       for (int j = 0; j < kStep16; ++j)
         if (j < n)
-          umma_ts_w(tO, tmem + 64 * b + 8 * j, sdesc_add(dv, j * 2048), idesc_pv, (st > 0 || j > 0) ? 1u : 0u);
+          umma_ts_w(tO, tmem + 64 * b + 8 * j + (kFixed && j >= 2 ? 16 : 0), sdesc_add(dv, j * 2048), idesc_pv,
+                    (st > 0 || j > 0) ? 1u : 0u);
       umma_commit_w(&v_empty[vs]);
       umma_commit_w(o_done);
       return true;
@@ -256,7 +279,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
       const uint32_t idesc_s = idesc_bf16(128, 16 * n, false, false);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        umma_ss_w(tmem + 64 * b, sdesc_add(dq0, (kk >> 2) * kChunkBytes + (kk & 3) * 32),
+        umma_ss_w(tmem + 64 * b, sdesc_add(dq0, (kk >> 2) * C::kQChunk + (kk & 3) * 32),
                   sdesc_add(dk, (kk >> 2) * kStageChunk + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
       umma_commit_w(&s_full[b]);
       umma_commit_w(&k_empty[ks]);
@@ -266,7 +289,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     umma_commit_w(drain);
     mbar_wait_drain(drain, 0);
   } else if ((warp & 3) < row_warps) {
-    // ---------------- softmax + epilogue (one row per thread; row warps without rows stay out) ----------------
+    // ---------------- softmax + epilogue (row warps without rows stay out) ----------------
+    const int grp = kFixed ? (warp - 2) >> 2 : 0;  // fixed form: column half of a step, and of O
     const int q4 = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const int row = q4 * 32 + lane;
@@ -275,7 +299,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     const int head = hk * a.group + rr % a.group;
     const bool live = row < rows;
     const int last = seq.kv - seq.nq + tok;  // this row's position
-    {
+    if (grp == 0) {
       // the row's 16-byte pieces go to their places in the 128-byte swizzle
       const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(seq.t0 + tok) * a.q_token +
                                                         static_cast<int64_t>(head) * a.q_head);
@@ -284,119 +308,177 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
       for (int i = 0; i < D / 8; ++i) v[i] = __ldg(src + i);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<uint4*>(sQ + (i >> 3) * kChunkBytes + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = v[i];
+        *reinterpret_cast<uint4*>(sQ + (i >> 3) * C::kQChunk + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = v[i];
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     }
     const float sl2 = a.scale * kLog2e;
-    const bool capped = a.cap > 0.f;
     const float slope2 = a.slopes ? __ldg(a.slopes + head) * kLog2e : 0.f;
-    const float mul = capped || a.slopes ? 1.0f : sl2;
-    const uint64_t mul2 = f2_pack(mul, mul);
-    float m_used = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int st = 0; st < n_steps; ++st) {
-      const int b = st & 1;
-      const int N = 16 * min(kStep16, n16 - st * kStep16);
-      const int base = k0 + st * kStepKeys;  // position of column 0
-      const int vis = last - base + 1;       // columns 0 .. vis - 1 are allowed
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (st >> 1) & 1, ab));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sr[2][32];
-#pragma unroll
-      for (int pc = 0; pc < 2; ++pc)
-        if (pc * 32 < N) tmem_ld32(tmem + 64 * b + lane_off + pc * 32, sr[pc]);
-      tmem_wait_ld();
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int pc = 0; pc < 2; ++pc) {
-        if (pc * 32 < N) {
-          if (capped) cap_scores<false>(sr[pc], sr[pc], a.c);
-          if (a.slopes) {
-            // distance of column i: (last - base - 32 pc) - i, exact in fp32
-            const float d0 = static_cast<float>(last - base - 32 * pc);
-            const uint64_t m2 = f2_pack(capped ? 1.0f : sl2, capped ? 1.0f : sl2);
-            const uint64_t ns = f2_pack(-slope2, -slope2);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(d0 - i, d0 - (i + 1)), ns,
-                               f2_mul(f2_pack(__uint_as_float(sr[pc][i]), __uint_as_float(sr[pc][i + 1])), m2)),
-                        x0, x1);
-              sr[pc][i] = __float_as_uint(x0);
-              sr[pc][i + 1] = __float_as_uint(x1);
-            }
-          }
-          // a step whose N is not a multiple of 32 ends the range, so vis <= N there
-          if (vis < pc * 32 + 32) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (pc * 32 + i >= vis) sr[pc][i] = 0xFF800000u;  // -inf
-          }
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            mx[0] = fmax3(mx[0], __uint_as_float(sr[pc][i]), __uint_as_float(sr[pc][i + 1]));
-            mx[1] = fmax3(mx[1], __uint_as_float(sr[pc][i + 2]), __uint_as_float(sr[pc][i + 3]));
-            mx[2] = fmax3(mx[2], __uint_as_float(sr[pc][i + 4]), __uint_as_float(sr[pc][i + 5]));
-            mx[3] = fmax3(mx[3], __uint_as_float(sr[pc][i + 6]), __uint_as_float(sr[pc][i + 7]));
-          }
-        }
-      }
-      const float mx2 = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * mul;
-      const bool resc = mx2 > m_used + kRescale;
-      const float m_new = resc ? mx2 : m_used;
-      const float alpha = resc ? ex2(m_used - m_new) : 1.0f;
-      l *= alpha;
-      m_used = m_new;
-      const float neg_mu = (m_used == -INFINITY) ? 0.f : -m_used;
-      const uint64_t nmu2 = f2_pack(neg_mu, neg_mu);
-      uint64_t ls2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
-      for (int pc = 0; pc < 2; ++pc) {
-        if (pc * 32 < N) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[pc][2 * i]), __uint_as_float(sr[pc][2 * i + 1])), mul2, nmu2),
-                      x0, x1);
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            ls2[i & 1] = f2_add(ls2[i & 1], f2_pack(p0, p1));
-            pk[i] = pack_bf16(p0, p1);
-          }
-          tmem_st16(tmem + 64 * b + lane_off + pc * 16, pk);
-        }
-      }
-      {
-        float a0, a1, b0, b1;
-        f2_unpack(ls2[0], a0, a1);
-        f2_unpack(ls2[1], b0, b1);
-        l += (a0 + a1) + (b0 + b1);
-      }
-      if (st > 0 && __any_sync(0xffffffffu, resc)) {
-        // O must hold the steps before this one; o_done has completed st - 1 or st
-        // phases here (S(st) was issued after PV(st-2), PV(st) waits for this arrival)
-        ok = __all_sync(0xffffffffu, mbar_wait(o_done, (st - 1) & 1, ab));
+    // results of the loops below: reference of the weights (log2), their sum, divisor of O
+    float ref = -INFINITY, l_true = 0.f, l = 0.f;
+    if constexpr (kFixed) {
+      // The cap bounds the capped scores, and the bias is largest at the range's
+      // nearest key (farthest for a negative slope), a distance known here: with it
+      // as reference no weight passes 2^cap2, and that key's is at least 2^-cap2.
+      const int d_ref = slope2 >= 0.f ? max(0, last - (k1 - 1)) : last - k0;
+      ref = a.slopes ? -slope2 * static_cast<float>(d_ref) : 0.f;
+      SoftRow r;
+      for (int st = 0; st < n_steps; ++st) {
+        const int b = st & 1;
+        const bool active = 2 * grp < n16 - st * kStep16;
+        const int base = k0 + st * kStepKeys + 32 * grp;  // position of this thread's first column
+        const int vis = last - base + 1;                   // its columns 0 .. vis - 1 are allowed
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (st >> 1) & 1, ab));
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
-        for (int pc = 0; pc < D / 32; ++pc) {
-          uint32_t r[32];
-          tmem_ld32(tO + lane_off + pc * 32, r);
+        const uint32_t s_addr = tmem + 64 * b + lane_off + 32 * grp;
+        if (active) {
+          uint32_t x[32];
+          tmem_ld32(s_addr, x);
           tmem_wait_ld();
+          cap_scores<false>(x, x, a.c);
+          if (a.slopes) {
+            // - slope (distance - d_ref) = slope (column - (last - base - d_ref))
+            const float b0 = -slope2 * static_cast<float>(last - base - d_ref);
+            const uint64_t b2 = f2_pack(b0, b0), s2 = f2_pack(slope2, slope2);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-          tmem_st32(tO + lane_off + pc * 32, r);
+            for (int i = 0; i < 32; i += 4) {
+              const float4 c = *reinterpret_cast<const float4*>(ramp + i);
+#pragma unroll
+              for (int j = 0; j < 4; j += 2) {
+                float x0, x1;
+                f2_unpack(f2_add(f2_pack(__uint_as_float(x[i + j]), __uint_as_float(x[i + j + 1])),
+                                 f2_fma(j ? f2_pack(c.z, c.w) : f2_pack(c.x, c.y), s2, b2)),
+                          x0, x1);
+                x[i + j] = __float_as_uint(x0);
+                x[i + j + 1] = __float_as_uint(x1);
+              }
+            }
+          }
+          // a step with fewer than 64 keys ends the range, so vis stays below them there
+          if (__builtin_expect(vis < 32, 0)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i >= vis) x[i] = 0xFF800000u;  // -inf
+          }
+          soft_weights(x, r, s_addr);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[b]);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&p_full[b]);
-    }
-    if (ok) {
-      ok = __all_sync(0xffffffffu, mbar_wait(o_last, 0, ab));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(o_last, 0, ab));
       tc_fence_after();
+      ok = ok && soft_total(r, xrow + row, grp, &pair_bar[q4], ab, l, l_true);
+    } else {
+      const float mul = kCap ? 1.0f : sl2;  // after the cap the scores are in log2 units
+      const uint64_t mul2 = f2_pack(mul, mul);
+      const float slope = slope2 / mul;
+      for (int st = 0; st < n_steps; ++st) {
+        const int b = st & 1;
+        const int N = 16 * min(kStep16, n16 - st * kStep16);
+        const int base = k0 + st * kStepKeys;  // position of column 0
+        const int vis = last - base + 1;       // columns 0 .. vis - 1 are allowed
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (st >> 1) & 1, ab));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[2][32];
+#pragma unroll
+        for (int pc = 0; pc < 2; ++pc)
+          if (pc * 32 < N) tmem_ld32(tmem + 64 * b + lane_off + pc * 32, sr[pc]);
+        tmem_wait_ld();
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int pc = 0; pc < 2; ++pc) {
+          if (pc * 32 < N) {
+            if constexpr (kCap) cap_scores<false>(sr[pc], sr[pc], a.c);
+            if (a.slopes) {
+              const float b0 = -slope * static_cast<float>(last - base);
+              const uint64_t b2 = f2_pack(b0, b0), s2 = f2_pack(slope, slope);
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 c = *reinterpret_cast<const float4*>(ramp + 32 * pc + i);
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                  float x0, x1;
+                  f2_unpack(f2_add(f2_pack(__uint_as_float(sr[pc][i + j]), __uint_as_float(sr[pc][i + j + 1])),
+                                   f2_fma(j ? f2_pack(c.z, c.w) : f2_pack(c.x, c.y), s2, b2)),
+                            x0, x1);
+                  sr[pc][i + j] = __float_as_uint(x0);
+                  sr[pc][i + j + 1] = __float_as_uint(x1);
+                }
+              }
+            }
+            // a step whose N is not a multiple of 32 ends the range, so vis <= N there
+            if (vis < pc * 32 + 32) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (pc * 32 + i >= vis) sr[pc][i] = 0xFF800000u;  // -inf
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              mx[0] = fmax3(mx[0], __uint_as_float(sr[pc][i]), __uint_as_float(sr[pc][i + 1]));
+              mx[1] = fmax3(mx[1], __uint_as_float(sr[pc][i + 2]), __uint_as_float(sr[pc][i + 3]));
+              mx[2] = fmax3(mx[2], __uint_as_float(sr[pc][i + 4]), __uint_as_float(sr[pc][i + 5]));
+              mx[3] = fmax3(mx[3], __uint_as_float(sr[pc][i + 6]), __uint_as_float(sr[pc][i + 7]));
+            }
+          }
+        }
+        const float mx2 = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * mul;
+        const bool resc = mx2 > ref + kRescale;
+        const float m_new = resc ? mx2 : ref;
+        const float alpha = resc ? ex2(ref - m_new) : 1.0f;
+        l *= alpha;
+        ref = m_new;
+        const float neg_mu = (ref == -INFINITY) ? 0.f : -ref;
+        const uint64_t nmu2 = f2_pack(neg_mu, neg_mu);
+        uint64_t ls2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int pc = 0; pc < 2; ++pc) {
+          if (pc * 32 < N) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[pc][2 * i]), __uint_as_float(sr[pc][2 * i + 1])), mul2, nmu2),
+                        x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              ls2[i & 1] = f2_add(ls2[i & 1], f2_pack(p0, p1));
+              pk[i] = pack_bf16(p0, p1);
+            }
+            tmem_st16(tmem + 64 * b + lane_off + pc * 16, pk);
+          }
+        }
+        {
+          float a0, a1, b0, b1;
+          f2_unpack(ls2[0], a0, a1);
+          f2_unpack(ls2[1], b0, b1);
+          l += (a0 + a1) + (b0 + b1);
+        }
+        if (st > 0 && __any_sync(0xffffffffu, resc)) {
+          // O must hold the steps before this one; o_done has completed st - 1 or st
+          // phases here (S(st) was issued after PV(st-2), PV(st) waits for this arrival)
+          ok = __all_sync(0xffffffffu, mbar_wait(o_done, (st - 1) & 1, ab));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int pc = 0; pc < D / 32; ++pc) {
+            uint32_t r[32];
+            tmem_ld32(tO + lane_off + pc * 32, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+            tmem_st32(tO + lane_off + pc * 32, r);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[b]);
+      }
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(o_last, 0, ab));
+      tc_fence_after();
+      l_true = l;
     }
     if (ok) {
       const int64_t out = static_cast<int64_t>(seq.t0 + tok) * a.heads + head;
@@ -405,24 +487,26 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
       const int64_t part = (tile * a.splits + split) * a.tile_rows + row;
       const bool empty = !(l > 0.f);
       const float inv = empty ? 0.f : 1.0f / l;
+      constexpr int kOut = kFixed ? D / 2 : D;  // columns of O that this thread writes
+      const int col = grp * kOut;
 #pragma unroll
-      for (int pc = 0; pc < D / 32; ++pc) {
+      for (int pc = 0; pc < kOut / 32; ++pc) {
         uint32_t r[32];
-        tmem_ld32(tO + lane_off + pc * 32, r);
+        tmem_ld32(tO + lane_off + col + pc * 32, r);
         tmem_wait_ld();
         if (live && whole) {
-          store_row32(a.o + out * D + pc * 32, r, inv, empty);
+          store_row32(a.o + out * D + col + pc * 32, r, inv, empty);
         } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(a.part + part * D + pc * 32);
+          uint4* dst = reinterpret_cast<uint4*>(a.part + part * D + col + pc * 32);
 #pragma unroll
           for (int i = 0; i < 8; ++i) dst[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
         }
       }
-      if (live) {
+      if (live && grp == 0) {
         if (whole) {
-          if (a.lse) a.lse[out] = empty ? -INFINITY : (m_used + lg2(l)) * kLn2;
+          if (a.lse) a.lse[out] = empty ? -INFINITY : (ref + lg2(l_true)) * kLn2;
         } else {
-          *reinterpret_cast<float2*>(a.part + n_part * D + 2 * part) = make_float2(m_used, l);
+          *reinterpret_cast<float4*>(a.part + n_part * D + 4 * part) = make_float4(empty ? -INFINITY : ref, l_true, l, 0.f);
         }
       }
     }
@@ -437,7 +521,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
 }
 
 // Join of split rows, one warp per (token, head): with M the largest maximum,
-// O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
+// O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s (m_s, l_s: a split's reference
+// and divisor; LSE has the sum of its unrounded weights).
 constexpr int kJoinWarps = 4;
 
 template <int D>
@@ -455,19 +540,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
   const int64_t tile = (static_cast<int64_t>(sq) * a.kv_heads + hk) * a.q_tiles + qt;
   const int64_t n_part = static_cast<int64_t>(gridDim.y) * a.kv_heads * a.q_tiles * a.splits * a.tile_rows;
   const int64_t part0 = tile * a.splits * a.tile_rows + row;
-  const float2* ml = reinterpret_cast<const float2*>(a.part + n_part * D);
+  const float4* ml = reinterpret_cast<const float4*>(a.part + n_part * D);
   float m = -INFINITY;
   for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[part0 + static_cast<int64_t>(s) * a.tile_rows].x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   constexpr int E = D / 32;  // elements per lane
-  float acc[E] = {}, l = 0.f;
+  float acc[E] = {}, l = 0.f, l_true = 0.f;
 #pragma unroll 4
   for (int s = 0; s < n; ++s) {
     const int64_t p = part0 + static_cast<int64_t>(s) * a.tile_rows;
-    const float2 x = ml[p];
+    const float4 x = ml[p];
     const float w = x.x == -INFINITY ? 0.f : ex2(x.x - m);
-    l = fmaf(w, x.y, l);
+    l_true = fmaf(w, x.y, l_true);
+    l = fmaf(w, x.z, l);
     const float* src = a.part + p * D + lane * E;
     if constexpr (E == 4) {
       const float4 v = *reinterpret_cast<const float4*>(src);
@@ -486,23 +572,37 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D + lane * E);
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) dst[i] = pack_bf16(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-  if (a.lse && lane == 0) a.lse[out] = l > 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
+  if (a.lse && lane == 0) a.lse[out] = l > 0.f ? (m + lg2(l_true)) * kLn2 : -INFINITY;
 }
 
-template <int D>
+template <int D, int FORM, bool SMALL>
 cudaError_t launch_paged_t(const TmaPages& tk, const TmaPages& tv, const PagedArgs& a, int n_seqs, cudaStream_t st) {
-  using C = PagedCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  using C = PagedCfg<D, FORM, SMALL>;
+  cudaError_t e =
+      cudaFuncSetAttribute(paged_kernel<D, FORM, SMALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(a.q_tiles * a.splits), static_cast<unsigned>(a.kv_heads),
                   static_cast<unsigned>(n_seqs));
-  paged_kernel<D><<<grid, kPagedThreads, C::kSmem, st>>>(tk, tv, a);
+  paged_kernel<D, FORM, SMALL><<<grid, C::kThreads, C::kSmem, st>>>(tk, tv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
   const int64_t items = static_cast<int64_t>(a.max_q) * a.heads;
   const dim3 jgrid(static_cast<unsigned>((items + kJoinWarps - 1) / kJoinWarps), static_cast<unsigned>(n_seqs));
   paged_join_kernel<D><<<jgrid, 32 * kJoinWarps, 0, st>>>(a);
   return cudaGetLastError();
+}
+
+template <int D, int FORM>
+cudaError_t launch_paged_f(const TmaPages& tk, const TmaPages& tv, const PagedArgs& a, int n_seqs, cudaStream_t st) {
+  return a.tile_rows <= 32 ? launch_paged_t<D, FORM, true>(tk, tv, a, n_seqs, st)
+                           : launch_paged_t<D, FORM, false>(tk, tv, a, n_seqs, st);
+}
+
+template <int D>
+cudaError_t launch_paged(const TmaPages& tk, const TmaPages& tv, const PagedArgs& a, int n_seqs, cudaStream_t st) {
+  if (!(a.cap > 0.f)) return launch_paged_f<D, kScoreMask>(tk, tv, a, n_seqs, st);
+  return a.c.cap2 <= kCapFixedMax ? launch_paged_f<D, kScoreFixed>(tk, tv, a, n_seqs, st)
+                                  : launch_paged_f<D, kScoreCap>(tk, tv, a, n_seqs, st);
 }
 
 }  // namespace
@@ -520,9 +620,13 @@ struct spattn_paged_s {
 namespace {
 
 // Split of a call over n sequences: q tiles per (sequence, K/V head), splits and
-// their length in keys.  Two CTAs run on an SM; a CTA costs its keys plus
-// about 320 keys' time for its start and end and, where split, its share of the
-// join.  The split count with the fewest rounds x cost wins.
+// their length in keys.  Two CTAs run on an SM.  A CTA costs its keys, about 320
+// keys' time for its start and end and, with a full tile, about 550 for writing
+// its rows in fp32 and reading them back.  One sequence fills whole rounds of CTAs, so
+// the split count with the fewest rounds x cost wins.  Of several, the host knows
+// only the bounds: with half of them as the mean length, ranges of
+// sqrt(work x overhead / slots) keys balance that overhead against the last
+// CTA's tail.
 struct Split {
   int q_tiles, tile_rows, splits, chunk;
 };
@@ -534,25 +638,31 @@ Split choose_split(const spattn_paged_s* p, int64_t n_seqs) {
   s.q_tiles = static_cast<int>((rows + 127) / 128);
   s.tile_rows = static_cast<int>(rows < 128 ? rows : 128);
   const int64_t tiles = n_seqs * L.kv_heads * s.q_tiles, slots = 2 * p->sms;
-  int64_t best = -1;
-  s.splits = 1;
-  s.chunk = (L.max_kv + 63) / 64 * 64;
-  const int64_t most = (L.max_kv + 127) / 128;
-  for (int64_t n = 1; n <= most && n <= 1024 && (n == 1 || tiles * n <= 16 * slots); ++n) {
-    const int64_t chunk = ((L.max_kv + n - 1) / n + 63) / 64 * 64;
-    const int64_t cost = (tiles * n + slots - 1) / slots * (chunk + 320);
-    if (best < 0 || cost < best) {
-      best = cost;
-      s.chunk = static_cast<int>(chunk);
-      s.splits = static_cast<int>((L.max_kv + chunk - 1) / chunk);
+  const double overhead = 320 + 550.0 * s.tile_rows / 128;
+  const int64_t most = std::min<int64_t>((L.max_kv + 127) / 128, 1024);
+  int64_t n = 1;
+  if (n_seqs == 1) {
+    double best = -1;
+    for (int64_t k = 1; k <= most && (k == 1 || tiles * k <= 16 * slots); ++k) {
+      const int64_t chunk = ((L.max_kv + k - 1) / k + 63) / 64 * 64;
+      const double cost = static_cast<double>((tiles * k + slots - 1) / slots) * (chunk + (k > 1 ? overhead : 320));
+      if (best < 0 || cost < best) {
+        best = cost;
+        n = k;
+      }
     }
+  } else {
+    const double chunk = std::sqrt(0.5 * tiles * L.max_kv * overhead / slots);
+    n = std::min<int64_t>(most, std::max<int64_t>(1, static_cast<int64_t>(L.max_kv / chunk + 0.5)));
   }
+  s.chunk = static_cast<int>(((L.max_kv + n - 1) / n + 63) / 64 * 64);
+  s.splits = (L.max_kv + s.chunk - 1) / s.chunk;
   return s;
 }
 
 int64_t split_bytes(const spattn_paged_s* p, const Split& s, int64_t n_seqs) {
   if (s.splits == 1) return 0;
-  return n_seqs * p->lay.kv_heads * s.q_tiles * s.splits * s.tile_rows * (p->lay.head_dim + 2) * 4;
+  return n_seqs * p->lay.kv_heads * s.q_tiles * s.splits * s.tile_rows * (p->lay.head_dim + 4) * 4;
 }
 
 bool aligned(const void* p, uintptr_t al) { return p && reinterpret_cast<uintptr_t>(p) % al == 0; }
@@ -565,7 +675,7 @@ int spattn_paged_create(const spattn_paged_layout* L, spattn_paged_t* out) {
   if (!out) return SPATTN_ERR_INVALID_ARG;
   *out = nullptr;
   if (!L || L->heads < 1 || L->kv_heads < 1 || L->heads % L->kv_heads || L->page_slots < 16 || L->page_slots % 16 ||
-      L->max_seqs < 1 || L->max_q < 1 || L->max_kv < L->max_q || !std::isfinite(L->scale) || L->scale < 0.f ||
+      L->max_seqs < 1 || L->max_q < 1 || L->max_kv < 1 || !std::isfinite(L->scale) || L->scale < 0.f ||
       !std::isfinite(L->softcap) || L->softcap < 0.f)
     return SPATTN_ERR_INVALID_ARG;
   if ((L->head_dim != 64 && L->head_dim != 128) || L->heads > 32768 || L->max_seqs > 65535 || L->max_kv > (1 << 30) ||
@@ -672,7 +782,7 @@ int spattn_paged_fwd(spattn_paged_t p, const spattn_paged_call* c, void* stream)
   a.err = p->d_err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int n = static_cast<int>(c->n_seqs);
-  const cudaError_t e = L.head_dim == 128 ? launch_paged_t<128>(tk, tv, a, n, s) : launch_paged_t<64>(tk, tv, a, n, s);
+  const cudaError_t e = L.head_dim == 128 ? launch_paged<128>(tk, tv, a, n, s) : launch_paged<64>(tk, tv, a, n, s);
   return e == cudaSuccess ? SPATTN_OK : SPATTN_ERR_CUDA;
 }
 

@@ -328,7 +328,7 @@ typedef struct {
   int32_t page_slots;      /* multiple of 16 */
   int32_t max_seqs;        /* bounds of any call: sequences, */
   int32_t max_q;           /* new tokens of one sequence (1: decoding), */
-  int32_t max_kv;          /* cache slots of one sequence (>= max_q) */
+  int32_t max_kv;          /* cache slots of one sequence */
   float scale;             /* softmax scale > 0; 0 selects 1/sqrt(head_dim) */
   float softcap;           /* > 0, or 0 for none */
 } spattn_paged_layout;
