@@ -639,11 +639,12 @@ Split choose_split(const spattn_paged_s* p, int64_t n_seqs) {
   s.tile_rows = static_cast<int>(rows < 128 ? rows : 128);
   const int64_t tiles = n_seqs * L.kv_heads * s.q_tiles, slots = 2 * p->sms;
   const double overhead = 320 + 550.0 * s.tile_rows / 128;
-  const int64_t most = std::min<int64_t>((L.max_kv + 127) / 128, 1024);
+  // at most sixteen rounds of CTAs, which bounds the workspace (320 MB of full tiles)
+  const int64_t most = std::max<int64_t>(1, std::min({(L.max_kv + 127) / int64_t{128}, int64_t{1024}, 16 * slots / tiles}));
   int64_t n = 1;
   if (n_seqs == 1) {
     double best = -1;
-    for (int64_t k = 1; k <= most && (k == 1 || tiles * k <= 16 * slots); ++k) {
+    for (int64_t k = 1; k <= most; ++k) {
       const int64_t chunk = ((L.max_kv + k - 1) / k + 63) / 64 * 64;
       const double cost = static_cast<double>((tiles * k + slots - 1) / slots) * (chunk + (k > 1 ? overhead : 320));
       if (best < 0 || cost < best) {

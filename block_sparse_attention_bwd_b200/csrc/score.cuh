@@ -45,7 +45,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // score.  Beyond that it is 1 - 2 / (1 + e^2u) with two special-function
 // operations per pair, of which the softmax already spends one.  Scores well
 // inside the cap are the ordinary case; a warp decides per step.
-constexpr float kTanhExpMax = 100.0f;  // e^2u held at 2^100: 1 - tanh^2 = 4 e r^2, r = 1 / (1 + e), stays finite
+constexpr float kTanhExpMax = 126.0f;  // e^2u held at 2^126: 1 - tanh^2 = 4 r (e r), r = 1 / (1 + e), stays finite
 template <bool GRAD, int N>
 __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], uint32_t (&d)[N], const CapArgs& c) {
   auto pair = [&](int i) { return f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])); };

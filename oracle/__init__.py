@@ -16,7 +16,10 @@ other than itself (dense attention from ``torch`` on a full graph, closed
 forms for single-key rows and zero queries, central finite differences,
 brute-force counts).  ``oracle.fp8`` (the E4M3 codec and per-slice quantiser
 of the FP8 forward) is pinned by ``tests/test_oracle_fp8.py`` against
-hand-computed codes of the format and a brute-force nearest-value search.
+hand-computed codes of the format and a brute-force nearest-value search;
+``oracle.operators`` (scored and paged attention, rotary positions) by
+``tests/test_oracle_operators.py`` against torch autograd, complex
+multiplication and central differences.
 """
 
 from .attention import (  # noqa: F401
@@ -37,3 +40,4 @@ from .plan import (  # noqa: F401
     bsa_physical_pairs,
 )
 from . import fp8  # noqa: F401,E402
+from . import operators  # noqa: F401,E402
