@@ -237,6 +237,19 @@ int score_args(const spattn_plan_s* P, const spattn_score* s, ScoreArgs* a, bool
   return SPATTN_OK;
 }
 
+FillArgs fill_args(const int32_t* list, const std::vector<int32_t>& host, int64_t bh, int64_t slots, __nv_bfloat16* t0,
+                   __nv_bfloat16* t1, float* lse) {
+  FillArgs f;
+  f.list = list;
+  f.n = static_cast<int64_t>(host.size() / 2);
+  f.bh = bh;
+  f.slots = slots;
+  f.t0 = t0;
+  f.t1 = t1;
+  f.lse = lse;
+  return f;
+}
+
 int run_fwd(const void* q, const void* k, const void* v, spattn_plan_s* plan, const ScoreArgs* sc, void* o, float* lse,
             void* stream) {
   if (!plan) return SPATTN_ERR_INVALID_ARG;
@@ -252,10 +265,12 @@ int run_fwd(const void* q, const void* k, const void* v, spattn_plan_s* plan, co
     return SPATTN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto* O = static_cast<__nv_bfloat16*>(o);
+  FillArgs fill;  // a scored forward does it in the same launch
+  if (sc) fill = fill_args(plan->d_q_fill, plan->q_fill, bh, plan->q.slots, O, nullptr, lse);
   cudaError_t e = timed(plan, SPATTN_K_FWD, s, [&] {
-    return launch_fwd(D, tq, tk, tv, tile_args(plan, plan->wq, plan->q.slots, plan->k.slots), sc, O, lse, s);
+    return launch_fwd(D, tq, tk, tv, tile_args(plan, plan->wq, plan->q.slots, plan->k.slots), sc, fill, O, lse, s);
   });
-  if (e == cudaSuccess && !plan->q_fill.empty())
+  if (!sc && e == cudaSuccess && !plan->q_fill.empty())
     e = timed(plan, SPATTN_K_FILL, s, [&] {
       return launch_fill(D, plan->d_q_fill, static_cast<int64_t>(plan->q_fill.size() / 2), bh, plan->q.slots, O,
                          nullptr, lse, s);
@@ -283,6 +298,11 @@ int run_bwd(const void* q, const void* k, const void* v, const void* o, const fl
   auto* dK = static_cast<__nv_bfloat16*>(dk);
   auto* dV = static_cast<__nv_bfloat16*>(dv);
   cudaError_t e = timed(plan, SPATTN_K_DELTA, s, [&] {
+    if (sc)  // with the counter and the fills, in one launch
+      return launch_prep(D, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), plan->d_delta,
+                         bh * plan->q.slots, plan->d_sched,
+                         fill_args(plan->d_q_fill, plan->q_fill, bh, plan->q.slots, dQ, nullptr, nullptr),
+                         fill_args(plan->d_k_fill, plan->k_fill, bh_kv, plan->k.slots, dK, dV, nullptr), s);
     return launch_delta(D, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), plan->d_delta,
                         bh * plan->q.slots, s);
   });
@@ -296,12 +316,12 @@ int run_bwd(const void* q, const void* k, const void* v, const void* o, const fl
       return launch_dq(D, static_cast<const __nv_bfloat16*>(q), tdo, tk, tv, tile_args(plan, plan->wq, plan->q.slots, plan->k.slots), sc,
                        lse, plan->d_delta, dQ, s);
     });
-  if (e == cudaSuccess && !plan->k_fill.empty())
+  if (!sc && e == cudaSuccess && !plan->k_fill.empty())
     e = timed(plan, SPATTN_K_FILL, s, [&] {
       return launch_fill(D, plan->d_k_fill, static_cast<int64_t>(plan->k_fill.size() / 2), bh_kv, plan->k.slots, dK,
                          dV, nullptr, s);
     });
-  if (e == cudaSuccess && !plan->q_fill.empty())
+  if (!sc && e == cudaSuccess && !plan->q_fill.empty())
     e = timed(plan, SPATTN_K_FILL, s, [&] {
       return launch_fill(D, plan->d_q_fill, static_cast<int64_t>(plan->q_fill.size() / 2), bh, plan->q.slots, dQ,
                          nullptr, nullptr, s);

@@ -64,6 +64,52 @@ __global__ void delta_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfl
   }
 }
 
+// Start of a scored backward in one launch: Delta, the work-item counter of the
+// dK / dV kernel, and the zero rows that no work item writes.  Blocks 0 ..
+// n_delta - 1 form Delta, one warp-row group per pass as above; the others take
+// (fill entry, batch*head) pairs.
+struct PrepArgs {
+  const __nv_bfloat16* o;
+  const __nv_bfloat16* d_o;
+  float* delta;
+  int64_t rows;
+  int n_delta;
+  int* sched;
+  FillArgs q, k;  // dQ; dK and dV
+};
+template <int D>
+__global__ void __launch_bounds__(256) prep_kernel(const PrepArgs a) {
+  if (static_cast<int>(blockIdx.x) >= a.n_delta) {
+    const int64_t first = blockIdx.x - a.n_delta, step = gridDim.x - a.n_delta;
+    for (int64_t i = first; i < a.q.n * a.q.bh; i += step) fill_rows<D>(a.q, i % a.q.n, i / a.q.n);
+    for (int64_t i = first; i < a.k.n * a.k.bh; i += step) fill_rows<D>(a.k, i % a.k.n, i / a.k.n);
+    return;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.sched = 0;
+  constexpr int TPR = D / 8;
+  const int64_t total = a.rows * TPR, stride = static_cast<int64_t>(a.n_delta) * blockDim.x;
+  const int lane = threadIdx.x & 31;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + (threadIdx.x & ~31); t0 < total; t0 += stride) {
+    const int64_t t = t0 + lane;
+    float acc = 0.f;
+    if (t < total) {
+      const uint4 x = *reinterpret_cast<const uint4*>(a.o + t * 8);
+      const uint4 y = *reinterpret_cast<const uint4*>(a.d_o + t * 8);
+      const __nv_bfloat162* px = reinterpret_cast<const __nv_bfloat162*>(&x);
+      const __nv_bfloat162* py = reinterpret_cast<const __nv_bfloat162*>(&y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 fx = __bfloat1622float2(px[i]), fy = __bfloat1622float2(py[i]);
+        acc = fmaf(fx.x, fy.x, acc);
+        acc = fmaf(fx.y, fy.y, acc);
+      }
+    }
+#pragma unroll
+    for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off, TPR);
+    if (t < total && t % TPR == 0) a.delta[t / TPR] = acc;
+  }
+}
+
 // ----------------------------------------------------------------------------
 // K3: dK, dV (key-owned tiles, query pages as columns, 64 columns per step)
 // ----------------------------------------------------------------------------
@@ -119,8 +165,9 @@ struct DkvCfg {
   static constexpr int kSmem = 2 * kTile + (kQStages + kDStages) * (kStageTile + kAugStage) + kOnesBytes + 1024 + 512;
   // scored forms, per stage: -LSE, last position, document and fp32 position of
   // its 64 query columns, the slopes of its pages, and the ranges of its halves.
-  // A stage's lines are rewritten when its tiles are, after the dV / dK products
-  // of its step, which wait for every row thread.
+  // The producers write them (the dO producer the positions); they are rewritten
+  // when the tiles are, after the dV / dK products of the step, which wait for
+  // every row thread.
   static constexpr int kColBytes = 4 * 64 * 4 + 16 + 32;
   static constexpr int kScoreBytes = kQStages * kColBytes;
   static_assert(kQStages == kDStages, "both producers fill the same line");
@@ -240,7 +287,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       mbar_init(&do_full[s], 1);
       mbar_init(&do_empty[s], 1);
     }
-    mbar_init(st_full, 1);
+    mbar_init(st_full, kScored ? 2 : 1);  // the products' commit; scored forms: and their issuer
     mbar_init(st_free, W::kRowThreads);
     for (int b = 0; b < 2; ++b) mbar_init(&pt_full[b], W::kRowThreads);
     mbar_init(acc_done, 1);
@@ -386,26 +433,32 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       float xc[NH];
       uint32_t livec;
       fetch_terms(0, pid, cbh, xc, livec);
-      // scored forms: the dO producer also holds the positions, last positions and
-      // documents of columns lane + 32h, the Q producer the slopes of the pages
+      // scored forms: the Q producer, which has no slice to write there, also holds
+      // the last positions and documents of columns lane + 32h and the slopes of
+      // the pages, the dO producer the positions
       int xpos[NH], xlast[NH], xdoc[NH];
       float xslope = 0.f;
       const bool masked = kScored && (sc.q_last || sc.q_doc);
+      const bool fetches = kScored && (is_q ? masked || sc.slopes : sc.slopes != nullptr);
+      const int64_t q_off = (wk.bh / kv_heads) * sc.q_batch;
+      const int head0 = (wk.bh / kv_heads) * heads;
       auto fetch_cols = [&](int t, int pg_lane, int bh_lane) {
-        if (!is_q) {
-          if (!masked && !sc.slopes) return;
+        if constexpr (kScored) {
+          if (!fetches) return;
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
             const int idx2 = lane + 32 * h;
             const int64_t slot = pref_slot(__shfl_sync(0xffffffffu, pg_lane, idx2 >> 4), idx2 & 15);
             const bool okc = t < n_stages && (idx2 >> 4) < min(SP, n_cols - t * SP) && slot < q_slots;
-            const int64_t off = (wk.bh / kv_heads) * sc.q_batch + (okc ? slot : 0);
-            xpos[h] = sc.slopes ? __ldg(sc.q_pos + off) : 0;
-            xlast[h] = sc.q_last ? __ldg(sc.q_last + off) : 0;
-            xdoc[h] = sc.q_doc ? __ldg(sc.q_doc + off) : -1;
+            const int64_t off = q_off + (okc ? slot : 0);
+            if (!is_q) {
+              xpos[h] = __ldg(sc.q_pos + off);
+            } else {
+              xlast[h] = sc.q_last ? __ldg(sc.q_last + off) : 0;
+              xdoc[h] = sc.q_doc ? __ldg(sc.q_doc + off) : -1;
+            }
           }
-        } else if (sc.slopes) {
-          xslope = __ldg(sc.slopes + bh_lane % heads);
+          if (is_q && sc.slopes) xslope = __ldg(sc.slopes + bh_lane - head0);
         }
       };
       if constexpr (kScored) fetch_cols(0, pid, cbh);
@@ -428,28 +481,27 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
                 term_row(xc[h], (livec >> h) & 1u);
           fence_proxy_async_smem();
         }
-        if constexpr (kScored) {
-          if (is_q) {
+        if (kScored && is_q) {
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const bool okc = (livec >> h) & 1u;
             // -LSE; -inf for a column behind the list and for a query that attends
             // nothing: its weights are 2^-inf = 0 whatever its scores
-#pragma unroll
-            for (int h = 0; h < NH; ++h)
-              col_lse(s)[lane + 32 * h] = ((livec >> h) & 1u) && xc[h] != -INFINITY ? -xc[h] * kLog2e : -INFINITY;
-            if (lane < SP) col_slope(s)[lane] = SC == kScoreCap ? xslope * kLog2e : xslope * kLog2e / sl2;
-          } else {
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-              if (sc.slopes) col_posf(s)[lane + 32 * h] = static_cast<float>(xpos[h]);
-              if (masked) {
-                col_last(s)[lane + 32 * h] = xlast[h];
-                col_doc(s)[lane + 32 * h] = xdoc[h];
-                const int4 rg = column_range((livec >> h) & 1u, xlast[h], xdoc[h]);
-                if (lane == 0) col_rng(s)[h] = rg;
-              }
+            col_lse(s)[lane + 32 * h] = okc && xc[h] != -INFINITY ? -xc[h] * kLog2e : -INFINITY;
+            if (masked) {
+              col_last(s)[lane + 32 * h] = xlast[h];
+              col_doc(s)[lane + 32 * h] = xdoc[h];
+              const int4 rg = column_range(okc, xlast[h], xdoc[h]);
+              if (lane == 0) col_rng(s)[h] = rg;
             }
           }
-          fetch_cols(t + 1, pid_next, cbh_next);
+          // (before a score is multiplied by sl2, where there is no cap)
+          if (sc.slopes && lane < SP) col_slope(s)[lane] = xslope * (SC == kScoreCap ? kLog2e : inv_scale);
+        } else if (kScored && sc.slopes) {
+#pragma unroll
+          for (int h = 0; h < NH; ++h) col_posf(s)[lane + 32 * h] = static_cast<float>(xpos[h]);
         }
+        if constexpr (kScored) fetch_cols(t + 1, pid_next, cbh_next);
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&full[s], n * C::kNch * 2048);
         __syncwarp();
@@ -510,6 +562,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
                     sdesc_add(bd, (kk >> 2) * kStageChunk + (kk & 3) * 32), idesc_s, kk > 0);
         umma_ss_w(tmem + 64, d_ones, sdesc_add(d_da, ds * kAugStage), idesc_s, 1u);
         umma_commit_w(st_full);
+        if (kScored && lane == 0) mbar_arrive(st_full);
       }
       // the owned K / V buffers are free once these products have read them
       umma_commit_w(own_free);
@@ -580,6 +633,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
           if (sc.k_doc) key_doc = __ldg(sc.k_doc + off);
         }
       }
+      const int4 rows = row_range(seg >= 0, key_pos, key_doc), mine = make_int4(key_pos, key_pos, key_doc, key_doc);
       // this row's mask of the group's page, fetched a step ahead
       const uint16_t* mask = reinterpret_cast<const uint16_t*>(col_masks + 2 * static_cast<int64_t>(wk.e0)) + (seg < 0 ? 0 : seg);
       auto mask_of = [&](int st) -> uint32_t {
@@ -602,19 +656,13 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(st_free);
-        // The stage's lines: both producers' writes are ordered by the barriers that
-        // announce its tiles (long complete: S^T and dP^T were made from them).
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(&q_full[qs], (G / QS) & 1, ab) && mbar_wait(&do_full[qs], (G / QS) & 1, ab))) {
-          ok = false;
-          break;
-        }
         if (active) {
           if (sc.q_last || sc.q_doc) {
             const int4 rg = col_rng(qs)[grp >> 1];
-            const bool none = seg < 0 || key_none(sc, rg, key_pos, key_doc);
-            if (none) m = 0u;
-            if (__builtin_expect(__any_sync(0xffffffffu, !none && !key_all(sc, rg, key_pos)), 0))
+            if (key_none(sc, rg, rows))
+              m = 0u;
+            else if (__builtin_expect(!key_all(sc, rg, rows), 0) &&
+                     __any_sync(0xffffffffu, mixed_row(m, key_none(sc, rg, mine), key_all(sc, rg, mine))))
               m &= column_bits<false, CW>(sc.q_last, sc.q_doc, col_last(qs) + CW * grp, col_doc(qs) + CW * grp, key_pos, key_doc);
           }
           // d = dP^T - Delta (from the augmented product); a = S^T -> log2 P^T
@@ -889,7 +937,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       mbar_init(&v_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&sd_full[b], 1);
+      mbar_init(&sd_full[b], kScored ? 2 : 1);  // the products' commit; scored forms: and their issuer
       mbar_init(&s_free[b], W::kRowThreads);
       mbar_init(&ds_full[b], W::kRowThreads);
       mbar_init(&dq_done[b], 1);
@@ -1021,6 +1069,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
                   sdesc_add(bv, (kk >> 2) * kStageChunk + (kk & 3) * 32), idesc_s, kk > 0);
       if (stage_end) umma_commit_w(&v_empty[vs]);
       umma_commit_w(&sd_full[b]);
+      if (kScored && lane == 0) mbar_arrive(&sd_full[b]);
     }
     umma_commit_w(&drain[0]);
     mbar_wait_drain(&drain[0], 0);
@@ -1097,6 +1146,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     const float mul = kCap ? 1.0f : sl2;  // after the cap the scores are in log2 units
     if (sc.slopes) slope = __ldg(sc.slopes + wk.bh % heads) * kLog2e / mul;
     const uint64_t m2 = f2_pack(mul, mul);
+    const int4 rows = row_range(seg >= 0, row_last, row_doc), mine = make_int4(row_last, row_last, row_doc, row_doc);
     // Bits of this group's 16 columns of a step, compared pair by pair: lanes load
     // one column each (the stage's lines hold fp32 positions only).
     auto step_bits = [&](int st) -> uint32_t {
@@ -1133,20 +1183,16 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       const bool active = st * NP + grp < n_cols;
       uint32_t m = m_next;
       m_next = st + 1 < n_steps ? mask_of(st + 1) : 0u;
-      if (use_cols) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&k_full[ks], (t / KS) & 1, ab))) {
-          ok = false;
-          break;
-        }
-        if (active && (sc.q_last || sc.q_doc)) {
-          const int4 rg = col_rng(ks)[2 * (st % SPS) + (grp >> 1)];
-          const bool none = seg < 0 || query_none(sc, rg, row_last, row_doc);
-          if (none) m = 0u;
-          if (__builtin_expect(__any_sync(0xffffffffu, !none && !query_all(sc, rg, row_last)), 0)) m &= step_bits(st);
-        }
-      }
       ok = __all_sync(0xffffffffu, mbar_wait(&sd_full[b], (st >> 1) & 1, ab));
       if (!ok) break;
+      if (active && (sc.q_last || sc.q_doc)) {
+        const int4 rg = col_rng(ks)[2 * (st % SPS) + (grp >> 1)];
+        if (query_none(sc, rg, rows))
+          m = 0u;
+        else if (__builtin_expect(!query_all(sc, rg, rows), 0) &&
+                 __any_sync(0xffffffffu, mixed_row(m, query_none(sc, rg, mine), query_all(sc, rg, mine))))
+          m &= step_bits(st);
+      }
       tc_fence_after();
       uint32_t a[CW], d[CW], pp[CW / 2], pd[CW / 2];
       if (active) {
@@ -1362,6 +1408,20 @@ cudaError_t launch_delta(int head_dim, const __nv_bfloat16* o, const __nv_bfloat
   return cudaGetLastError();
 }
 
+cudaError_t launch_prep(int head_dim, const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* delta, int64_t rows,
+                        int* sched, const FillArgs& q, const FillArgs& k, cudaStream_t st) {
+  PrepArgs a{o, d_o, delta, rows, 0, sched, q, k};
+  const int64_t blocks = std::min<int64_t>((rows * (head_dim / 8) + 255) / 256, 148 * 16);
+  a.n_delta = static_cast<int>(std::max<int64_t>(blocks, 1));
+  const int64_t fills = std::min<int64_t>(std::max(q.n * q.bh, k.n * k.bh), 148 * 16);
+  const unsigned grid = static_cast<unsigned>(a.n_delta + fills);
+  if (head_dim == 128)
+    prep_kernel<128><<<grid, 256, 0, st>>>(a);
+  else
+    prep_kernel<64><<<grid, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <int D, int SC>
 static cudaError_t launch_dkdv_t(const TmaPages& tk, const TmaPages& tv, const TmaPages& tq,
                                  const TmaPages& tdo, const TileArgs& a, const ScoreArgs& sc, const float* lse,
@@ -1374,7 +1434,7 @@ static cudaError_t launch_dkdv_t(const TmaPages& tk, const TmaPages& tv, const T
   int dev = 0, sms = 0;
   e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaMemsetAsync(a.sched, 0, sizeof(int), st);
+  if (e == cudaSuccess && SC == kScoreNone) e = cudaMemsetAsync(a.sched, 0, sizeof(int), st);  // else launch_prep's
   if (e != cudaSuccess) return e;
   const int64_t grid = std::min<int64_t>(a.n_work, std::max(sms, 1));
   dkdv_kernel<D, SC><<<static_cast<unsigned>(grid), BwdWarps<SC != kScoreNone>::kThreads, kSmem, st>>>(

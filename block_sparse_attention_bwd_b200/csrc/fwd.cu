@@ -54,12 +54,12 @@ struct FwdCfg {
   static constexpr int kVStages = (D == 128) ? 2 : 4;         // V ring depth
   static constexpr int kSmem = kTile + kKStages * kKStage + kVStages * kVStage + 1024 + 512;
   // scored forms: ring of column lines (positions, documents, fp32 positions of
-  // a step's 64 columns), the range of each, and their barriers.  The producer
+  // a step's 64 columns) and the range of each.  The producer
   // is at most kKStages steps ahead of S, and S(st) is issued after the rows have
   // left step st - 2, so kKStages + 2 lines are never overwritten while read.
   static constexpr int kColRing = 8;
   static constexpr int kColBytes = 3 * 64 * 4;
-  static constexpr int kScoreBytes = kColRing * (kColBytes + 16 + 8) + 4 * 128 * 4 + 4 * 8;  // + the row pairs' exchange and barriers
+  static constexpr int kScoreBytes = kColRing * (kColBytes + 16) + 4 * 128 * 4 + 4 * 8;  // + the row pairs' exchange and barriers
   static_assert(kColRing >= kKStages + 2, "column lines outlive their readers");
   static_assert(!F8 || D == 128, "the E4M3 forward has D = 128 (one 128-byte row per chunk)");
 };
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
                const int32_t* __restrict__ col_pages, const uint64_t* __restrict__ col_masks,
                __nv_bfloat16* __restrict__ out_o, float* __restrict__ out_lse, int64_t q_slots, float sl2,
                int heads, int kv_group, const float* __restrict__ q_descale, const float* __restrict__ k_descale,
-               int* err, const ScoreArgs sc, int64_t kv_slots) {
+               int* err, const ScoreArgs sc, int64_t kv_slots, int64_t n_work, const FillArgs fill) {
   using C = FwdCfg<D, F8>;
   constexpr int KS = C::kKStages, VS = C::kVStages, NP = kFwdStepPages;
   extern __shared__ uint8_t smem_raw[];
@@ -112,12 +112,18 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
   auto col_doc = [&](int st) { return col_pos(st) + 64; };
   auto col_posf = [&](int st) { return reinterpret_cast<float*>(col_pos(st) + 128); };
   int4* col_rng = reinterpret_cast<int4*>(score_smem + R * C::kColBytes);
-  uint64_t* c_full = reinterpret_cast<uint64_t*>(col_rng + R);  // [R]
-  float* xrow = reinterpret_cast<float*>(c_full + R);            // [4][128] sums of the row pairs (fixed form)
+  float* xrow = reinterpret_cast<float*>(col_rng + R);            // [4][128] sums of the row pairs (fixed form)
   uint64_t* pair_bar = reinterpret_cast<uint64_t*>(xrow + 4 * 128);  // [4]
   const bool use_cols = SC != kScoreNone && SC != kScoreFixed ? (sc.q_last || sc.q_doc || sc.slopes)
                                                               : SC == kScoreFixed && (sc.q_last || sc.q_doc);
 
+  if constexpr (SC != kScoreNone) {
+    // blocks behind the work items: rows that none of them writes (a launch less)
+    if (blockIdx.x >= n_work) {
+      for (int64_t bh = 0; bh < fill.bh; ++bh) fill_rows<D>(fill, blockIdx.x - n_work, bh);
+      return;
+    }
+  }
   const Work wk = load_work(work, blockIdx.x);
   // K/V head of this item's query head (grouped-query attention)
   const int kv_bh = (wk.bh / heads) * (heads / kv_group) + (wk.bh % heads) / kv_group;
@@ -139,14 +145,13 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
       mbar_init(&v_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&s_full[b], 1);
+      mbar_init(&s_full[b], SC == kScoreNone ? 1 : 2);  // the products' commit; scored forms: and their issuer
       mbar_init(&p_full[b], kFwdThreads<SC> - 64);
     }
     mbar_init(o_done, 1);
     mbar_init(drain, 1);
     mbar_init(o_last, 1);
     if constexpr (SC != kScoreNone) {
-      for (int s = 0; s < R; ++s) mbar_init(&c_full[s], 1);
       for (int s = 0; s < 4; ++s) mbar_init(&pair_bar[s], 64);
     }
     fence_barrier_init();
@@ -218,9 +223,8 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
         }
         const int4 rg = range_join(column_range(clive[0], cpos[0], cdoc[0]), column_range(clive[1], cpos[1], cdoc[1]));
         if (lane == 0) col_rng[st % R] = rg;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c_full[st % R]);
         load_cols(st + 1, pid_next);
+        __syncwarp();
       }
       if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], n * C::kQKNch * 2048);
       __syncwarp();
@@ -324,6 +328,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
                     sdesc_add(dk, (kk >> 2) * kFwdStageChunk + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
       }
       umma_commit_w(&s_full[b]);
+      if (SC != kScoreNone && lane == 0) mbar_arrive(&s_full[b]);
       umma_commit_w(&k_empty[ks]);
       if (st >= 1 && !issue_pv(st - 1)) ok = false;
     }
@@ -354,6 +359,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
         if (sc.q_doc) row_doc = __ldg(sc.q_doc + off);
       }
     }
+    const int4 rows = row_range(seg >= 0, row_last, row_doc), mine = make_int4(row_last, row_last, row_doc, row_doc);
     // this row's masks of its two pages, fetched a step ahead
     const uint16_t* mask = reinterpret_cast<const uint16_t*>(col_masks + 2 * static_cast<int64_t>(wk.e0)) + (seg < 0 ? 0 : seg);
     uint32_t m_lo = 0u, m_hi = 0u;
@@ -370,21 +376,16 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
       const bool active = halves ? grp == 0 : 2 * grp < n_cols - st * NP;
       uint32_t bits = m_lo | (m_hi << 16);
       if (st + 1 < n_steps) fetch_masks(st + 1);
-      if (use_cols) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&c_full[st % R], (st / R) & 1, ab))) {
-          ok = false;
-          break;
-        }
-        if (active && (sc.q_last || sc.q_doc)) {
-          const int4 rg = col_rng[st % R];
-          const bool none = seg < 0 || query_none(sc, rg, row_last, row_doc);
-          if (none) bits = 0u;
-          if (__builtin_expect(__any_sync(0xffffffffu, !none && !query_all(sc, rg, row_last)), 0))
-            bits &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + 16 * pg0, col_doc(st) + 16 * pg0, row_last, row_doc);
-        }
-      }
       ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (st >> 1) & 1, ab));
       if (!ok) break;
+      if (use_cols && active) {
+        const int4 rg = col_rng[st % R];
+        if (query_none(sc, rg, rows))
+          bits = 0u;
+        else if (__builtin_expect(!query_all(sc, rg, rows), 0) &&
+                 __any_sync(0xffffffffu, mixed_row(bits, query_none(sc, rg, mine), query_all(sc, rg, mine))))
+          bits &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + 16 * pg0, col_doc(st) + 16 * pg0, row_last, row_doc);
+      }
       tc_fence_after();
       uint32_t x[32];
       const uint32_t s_addr = tmem + 64 * b + lane_off + 32 * grp;
@@ -459,6 +460,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
       }
       if (sc.slopes) slope = __ldg(sc.slopes + wk.bh % heads) * kLog2e / mul;
     }
+    const int4 rows = SC != kScoreNone ? row_range(seg >= 0, row_last, row_doc) : make_int4(0, 0, 0, 0);
     const uint64_t mul2 = f2_pack(mul, mul);
     for (int st = 0; st < n_steps; ++st) {
       const int b = st & 1;
@@ -469,25 +471,25 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
       if (halves && hh) mw[0] = mw[1];
       // mask words of the next step load while this one computes
       if (st + 1 < n_steps) raw.fetch(col_masks, wk.e0 + (st + 1) * NP, min(NP, n_cols - (st + 1) * NP), seg);
-      if (SC != kScoreNone && use_cols) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&c_full[st % R], (st / R) & 1, ab))) {
-          ok = false;
-          break;
-        }
-        if (sc.q_last || sc.q_doc) {
-          const int4 rg = col_rng[st % R];
-          const bool none = seg < 0 || query_none(sc, rg, row_last, row_doc);
-          if (none) mw[0] = mw[1] = 0u;
-          if (__builtin_expect(__any_sync(0xffffffffu, !none && !query_all(sc, rg, row_last)), 0)) {
-            const int c0 = halves ? 32 * hh : 0;
-            mw[0] &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + c0, col_doc(st) + c0, row_last, row_doc);
-            if (!halves)
-              mw[1] &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + 32, col_doc(st) + 32, row_last, row_doc);
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (st >> 1) & 1, ab));
+      if (!ok) break;
+      if (SC != kScoreNone && (sc.q_last || sc.q_doc)) {
+        const int4 rg = col_rng[st % R];
+        if (query_none(sc, rg, rows)) {
+          mw[0] = mw[1] = 0u;
+        } else if (__builtin_expect(!query_all(sc, rg, rows), 0)) {
+          const int4 mine = make_int4(row_last, row_last, row_doc, row_doc);
+          const int c0 = halves ? 32 * hh : 0;
+          uint32_t some = mw[0] | mw[1];
+          const bool mixed = mixed_row(some, query_none(sc, rg, mine), query_all(sc, rg, mine));
+          if (some == 0u) mw[0] = mw[1] = 0u;
+          if (__any_sync(0xffffffffu, mixed)) {
+          mw[0] &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + c0, col_doc(st) + c0, row_last, row_doc);
+          if (!halves)
+            mw[1] &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + 32, col_doc(st) + 32, row_last, row_doc);
           }
         }
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (st >> 1) & 1, ab));
-      if (!ok) break;
       tc_fence_after();
       uint32_t sr[2][32];
 #pragma unroll
@@ -639,51 +641,52 @@ __global__ void fill_kernel(const int32_t* __restrict__ fill, int64_t n_bh, int6
 
 template <int D, bool F8, bool ROUTE, int SC>
 cudaError_t launch_fwd_r(const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
-                         const ScoreArgs& sc, __nv_bfloat16* o, float* lse, const float* q_descale,
-                         const float* k_descale, cudaStream_t st) {
+                         const ScoreArgs& sc, const FillArgs& fill, __nv_bfloat16* o, float* lse,
+                         const float* q_descale, const float* k_descale, cudaStream_t st) {
   using C = FwdCfg<D, F8>;
   constexpr int kSmem = C::kSmem + (SC != kScoreNone ? C::kScoreBytes : 0);
   cudaError_t e =
       cudaFuncSetAttribute(fwd_kernel<D, F8, ROUTE, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  if (a.n_work == 0) return cudaSuccess;
-  fwd_kernel<D, F8, ROUTE, SC><<<static_cast<unsigned>(a.n_work), kFwdThreads<SC>, kSmem, st>>>(
+  const int64_t blocks = a.n_work + (SC != kScoreNone ? fill.n : 0);
+  if (blocks == 0) return cudaSuccess;
+  fwd_kernel<D, F8, ROUTE, SC><<<static_cast<unsigned>(blocks), kFwdThreads<SC>, kSmem, st>>>(
       tq, tk, tv, a.work, a.pages, a.masks, o, lse, a.own_slots, a.scale * kLog2e, a.heads, a.kv_group, q_descale,
-      k_descale, a.err, sc, a.col_slots);
+      k_descale, a.err, sc, a.col_slots, a.n_work, fill);
   return cudaGetLastError();
 }
 
 template <int D, bool F8, int SC>
 cudaError_t launch_fwd_sc(const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
-                          const ScoreArgs& sc, __nv_bfloat16* o, float* lse, const float* q_descale,
-                          const float* k_descale, cudaStream_t st) {
-  return a.route64 ? launch_fwd_r<D, F8, true, SC>(tq, tk, tv, a, sc, o, lse, q_descale, k_descale, st)
-                   : launch_fwd_r<D, F8, false, SC>(tq, tk, tv, a, sc, o, lse, q_descale, k_descale, st);
+                          const ScoreArgs& sc, const FillArgs& fill, __nv_bfloat16* o, float* lse,
+                          const float* q_descale, const float* k_descale, cudaStream_t st) {
+  return a.route64 ? launch_fwd_r<D, F8, true, SC>(tq, tk, tv, a, sc, fill, o, lse, q_descale, k_descale, st)
+                   : launch_fwd_r<D, F8, false, SC>(tq, tk, tv, a, sc, fill, o, lse, q_descale, k_descale, st);
 }
 
 template <int D>
 cudaError_t launch_fwd_t(const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
-                         const ScoreArgs* sc, __nv_bfloat16* o, float* lse, cudaStream_t st) {
-  if (!sc) return launch_fwd_sc<D, false, kScoreNone>(tq, tk, tv, a, ScoreArgs(), o, lse, nullptr, nullptr, st);
-  if (!(sc->cap > 0.f)) return launch_fwd_sc<D, false, kScoreMask>(tq, tk, tv, a, *sc, o, lse, nullptr, nullptr, st);
+                         const ScoreArgs* sc, const FillArgs& fill, __nv_bfloat16* o, float* lse, cudaStream_t st) {
+  if (!sc) return launch_fwd_sc<D, false, kScoreNone>(tq, tk, tv, a, ScoreArgs(), FillArgs(), o, lse, nullptr, nullptr, st);
+  if (!(sc->cap > 0.f)) return launch_fwd_sc<D, false, kScoreMask>(tq, tk, tv, a, *sc, fill, o, lse, nullptr, nullptr, st);
   // a bounded cap without a bias needs no running maximum (kCapFixedMax)
   if (!sc->slopes && sc->c.cap2 <= kCapFixedMax)
-    return launch_fwd_sc<D, false, kScoreFixed>(tq, tk, tv, a, *sc, o, lse, nullptr, nullptr, st);
-  return launch_fwd_sc<D, false, kScoreCap>(tq, tk, tv, a, *sc, o, lse, nullptr, nullptr, st);
+    return launch_fwd_sc<D, false, kScoreFixed>(tq, tk, tv, a, *sc, fill, o, lse, nullptr, nullptr, st);
+  return launch_fwd_sc<D, false, kScoreCap>(tq, tk, tv, a, *sc, fill, o, lse, nullptr, nullptr, st);
 }
 
 }  // namespace
 
 cudaError_t launch_fwd(int head_dim, const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
-                       const ScoreArgs* sc, __nv_bfloat16* o, float* lse, cudaStream_t st) {
-  return head_dim == 128 ? launch_fwd_t<128>(tq, tk, tv, a, sc, o, lse, st)
-                         : launch_fwd_t<64>(tq, tk, tv, a, sc, o, lse, st);
+                       const ScoreArgs* sc, const FillArgs& fill, __nv_bfloat16* o, float* lse, cudaStream_t st) {
+  return head_dim == 128 ? launch_fwd_t<128>(tq, tk, tv, a, sc, fill, o, lse, st)
+                         : launch_fwd_t<64>(tq, tk, tv, a, sc, fill, o, lse, st);
 }
 
 cudaError_t launch_fwd_e4m3(const TmaPages& tq8, const TmaPages& tk8, const TmaPages& tv, const TileArgs& a,
                             const float* q_descale, const float* k_descale, __nv_bfloat16* o, float* lse,
                             cudaStream_t st) {
-  return launch_fwd_sc<128, true, kScoreNone>(tq8, tk8, tv, a, ScoreArgs(), o, lse, q_descale, k_descale, st);
+  return launch_fwd_sc<128, true, kScoreNone>(tq8, tk8, tv, a, ScoreArgs(), FillArgs(), o, lse, q_descale, k_descale, st);
 }
 
 cudaError_t launch_fill(int head_dim, const int32_t* fill, int64_t n, int64_t bh, int64_t slots,

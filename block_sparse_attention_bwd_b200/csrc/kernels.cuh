@@ -76,9 +76,25 @@ struct ScoreArgs {
   int64_t q_batch = 0, k_batch = 0;  // elements between batch entries (0: shared)
 };
 
-// K1: O, LSE for every query-owned work item; `sc` (may be null) modifies the scores.
+// Rows that no work item writes, as (page, 16-bit row mask) pairs: zeroed in t0
+// and t1 (if given), with LSE = -inf (if given), for every (batch, head).
+struct FillArgs {
+  const int32_t* list = nullptr;
+  int64_t n = 0, bh = 0, slots = 0;
+  __nv_bfloat16* t0 = nullptr;
+  __nv_bfloat16* t1 = nullptr;
+  float* lse = nullptr;
+};
+
+// Delta, the zeroed work-item counter of launch_dkdv and the fills of a scored
+// backward, in one launch.
+cudaError_t launch_prep(int head_dim, const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* delta, int64_t rows,
+                        int* sched, const FillArgs& q, const FillArgs& k, cudaStream_t st);
+
+// K1: O, LSE for every query-owned work item; `sc` (may be null) modifies the scores,
+// and with it the launch also does `fill`.
 cudaError_t launch_fwd(int head_dim, const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
-                       const ScoreArgs* sc, __nv_bfloat16* o, float* lse, cudaStream_t st);
+                       const ScoreArgs* sc, const FillArgs& fill, __nv_bfloat16* o, float* lse, cudaStream_t st);
 
 // K1 with E4M3 Q and K (head_dim 128): tq8 / tk8 map the one-byte codes (128
 // per 128-byte row), S is scaled by q_descale[bh] * k_descale[kv_bh].

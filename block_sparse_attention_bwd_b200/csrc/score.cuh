@@ -5,10 +5,13 @@
 //   allowed iff the plan's masks say so, k_pos <= q_last and q_doc == k_doc >= 0.
 //
 // The column side of a step (positions, documents, and their range over the
-// step) is written into shared memory by the warp that loads the step's tiles,
-// so that a row thread pays two compares per step while its row is fully
-// allowed or fully masked by the range, and compares pair by pair only in
-// steps where some row of its warp is neither.
+// step) is written into shared memory by the warp that loads the step's tiles.
+// A row warp holds the range of its own rows, so a step that the two ranges show
+// to be fully allowed or fully masked costs it a few compares; pairs are compared
+// only in the others.  The lines become visible to the rows with the barrier
+// that announces the step's scores: the issuer of the products has waited
+// for the tiles, whose announcement follows the lines, and adds an arrival of its
+// own to that of the products.
 #pragma once
 
 #include "tile.cuh"
@@ -49,11 +52,15 @@ constexpr float kTanhExpMax = 126.0f;  // e^2u held at 2^126: 1 - tanh^2 = 4 r (
 template <bool GRAD, int N>
 __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], uint32_t (&d)[N], const CapArgs& c) {
   auto pair = [&](int i) { return f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])); };
+  constexpr bool kKeep = N <= 16;  // wider rows form the squares twice rather than hold them
+  uint64_t sq[kKeep ? N / 2 : 1];
   float mx[2] = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) {
     float a, b;
-    f2_unpack(f2_mul(pair(i), pair(i)), a, b);
+    const uint64_t w = f2_mul(pair(i), pair(i));
+    if constexpr (kKeep) sq[i] = w;
+    f2_unpack(w, a, b);
     mx[i & 1] = fmax3(mx[i & 1], a, b);  // a NaN drops out here and keeps its NaN in either form
   }
   if (__builtin_expect(!__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > c.w_max), 1)) {
@@ -62,7 +69,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], uint32_t (&d)[N], c
     const uint64_t ng = f2_pack(c.ng, c.ng), one = f2_pack(1.f, 1.f);
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-      const uint64_t x = pair(i), w = f2_mul(x, x);
+      const uint64_t x = pair(i), w = kKeep ? sq[kKeep ? i : 0] : f2_mul(x, x);
       const uint64_t z = f2_mul(x, f2_fma(f2_fma(f2_fma(f2_fma(a4, w, a3), w, a2), w, a1), w, a0));
       float a, b;
       f2_unpack(z, a, b);
@@ -172,19 +179,30 @@ __device__ __forceinline__ int4 range_join(int4 a, int4 b) {
   return make_int4(min(a.x, b.x), max(a.y, b.y), min(a.z, b.z), max(a.w, b.w));
 }
 
-// A query row against the range of its key columns.
-__device__ __forceinline__ bool query_none(const ScoreArgs& sc, int4 r, int last, int doc) {
-  return (sc.q_last && r.x > last) || (sc.q_doc && (doc < 0 || doc < r.z || doc > r.w));
+// Range of a warp's rows: of last positions (query rows) or positions (key rows),
+// and of documents.  Rows without a segment are left out.
+__device__ __forceinline__ int4 row_range(bool real, int pos, int doc) { return column_range(real, pos, doc); }
+
+// Query rows `w` against key columns `c`: none allowed / every pair allowed.
+__device__ __forceinline__ bool query_none(const ScoreArgs& sc, int4 c, int4 w) {
+  return (sc.q_last && c.x > w.y) || (sc.q_doc && (w.w < 0 || w.w < c.z || w.z > c.w));
 }
-__device__ __forceinline__ bool query_all(const ScoreArgs& sc, int4 r, int last) {
-  return (!sc.q_last || r.y <= last) && (!sc.q_doc || r.z == r.w);
+__device__ __forceinline__ bool query_all(const ScoreArgs& sc, int4 c, int4 w) {
+  return (!sc.q_last || c.y <= w.x) && (!sc.q_doc || (c.z == c.w && w.z == w.w && c.z == w.z && w.z >= 0));
 }
-// A key row against the range of its query columns.
-__device__ __forceinline__ bool key_none(const ScoreArgs& sc, int4 r, int pos, int doc) {
-  return (sc.q_last && pos > r.y) || (sc.q_doc && (doc < 0 || doc < r.z || doc > r.w));
+// Key rows `w` against query columns `c`.
+__device__ __forceinline__ bool key_none(const ScoreArgs& sc, int4 c, int4 w) {
+  return (sc.q_last && w.x > c.y) || (sc.q_doc && (w.w < 0 || w.w < c.z || w.z > c.w));
 }
-__device__ __forceinline__ bool key_all(const ScoreArgs& sc, int4 r, int pos) {
-  return (!sc.q_last || pos <= r.x) && (!sc.q_doc || r.z == r.w);
+__device__ __forceinline__ bool key_all(const ScoreArgs& sc, int4 c, int4 w) {
+  return (!sc.q_last || w.y <= c.x) && (!sc.q_doc || (c.z == c.w && w.z == w.w && c.z == w.z && w.z >= 0));
+}
+
+// A warp whose rows differ asks each of them (its own range being a point): a row
+// with nothing loses its bits, and true comes back if it has to be compared.
+__device__ __forceinline__ bool mixed_row(uint32_t& bits, bool none, bool all) {
+  if (none) bits = 0u;
+  return !none && !all && bits != 0u;
 }
 
 // Bits of N columns for one row.  KEYS: the columns are keys (position <=

@@ -157,5 +157,21 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (
   store_row(dst, r, mul, zero);
 }
 
+// One entry of a fill list for one (batch, head), by a whole block.
+template <int D>
+__device__ __forceinline__ void fill_rows(const FillArgs& f, int64_t entry, int64_t bh) {
+  const int64_t page = __ldg(f.list + 2 * entry);
+  const uint32_t rows = static_cast<uint32_t>(__ldg(f.list + 2 * entry + 1));
+  for (int i = threadIdx.x; i < 16 * (D / 8); i += blockDim.x) {
+    const int r = i / (D / 8);
+    const int64_t slot = page * 16 + r;
+    if (slot >= f.slots || !((rows >> r) & 1u)) continue;
+    const int64_t off = (bh * f.slots + slot) * D + (i % (D / 8)) * 8;
+    if (f.t0) *reinterpret_cast<uint4*>(f.t0 + off) = make_uint4(0, 0, 0, 0);
+    if (f.t1) *reinterpret_cast<uint4*>(f.t1 + off) = make_uint4(0, 0, 0, 0);
+    if (f.lse && i % (D / 8) == 0) f.lse[bh * f.slots + slot] = -INFINITY;
+  }
+}
+
 }  // namespace dev
 }  // namespace spattn
