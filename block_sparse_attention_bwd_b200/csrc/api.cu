@@ -183,6 +183,7 @@ TileArgs tile_args(const spattn_plan_s* P, const WorkList& w, int64_t own_slots,
   // entry head offsets exist only under grouped-query attention (else all 0)
   a.col_heads = P->kv_heads == P->heads ? nullptr : w.d_heads;
   a.route64 = w.route64;
+  a.order = w.ordered ? w.d_order : nullptr;
   return a;
 }
 
@@ -196,16 +197,22 @@ CapArgs cap_args(float cap, float scale) {
   constexpr double kLog2E = 1.4426950408889634, t[5] = {1.0, -0.33333149552345276, 0.1332598626613617,
                                                         -0.05305291339755058, 0.017256902530789375};
   const double k = static_cast<double>(scale) / cap, cap2 = cap * kLog2E;
+  const auto twice = [](double x) {
+    const float f = static_cast<float>(x);
+    uint32_t u;
+    std::memcpy(&u, &f, 4);
+    return static_cast<uint64_t>(u) << 32 | u;
+  };
   double p = cap2 * k;
   bool fits = true;
   for (int i = 0; i < 5; ++i, p *= k * k) {
-    r.a[i] = static_cast<float>(t[i] * p);
+    r.a[i] = twice(t[i] * p);
     fits = fits && std::fabs(t[i] * p) < 1e30;
   }
   r.w_max = fits ? static_cast<float>(0.25 / (k * k)) : -1.f;  // never the polynomial where a coefficient overflows
   r.k2 = static_cast<float>(2 * kLog2E * k);
   r.cap2 = static_cast<float>(cap2);
-  r.ng = static_cast<float>(-1.0 / (cap2 * cap2));
+  r.ng = twice(-1.0 / (cap2 * cap2));
   return r;
 }
 

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
                 const float* __restrict__ lse, const float* __restrict__ delta, __nv_bfloat16* __restrict__ out_dk,
                 __nv_bfloat16* __restrict__ out_dv, int64_t kv_slots, int64_t q_slots, float sl2, float scale,
                 int heads, int kv_heads, int kv_group, const uint16_t* __restrict__ col_heads, int* err,
-                const ScoreArgs sc) {
+                const ScoreArgs sc, const int32_t* __restrict__ order) {
   using C = DkvCfg<D>;
   constexpr bool kScored = SC != kScoreNone;
   using W = BwdWarps<kScored>;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
         int v = 0;
         if (lane == 0) {
           v = atomicAdd(sched, 1);
-          v = v < n_work ? v : -1;
+          v = v < n_work ? (kScored && order ? __ldg(order + v) : v) : -1;
           items[s] = v;
           mbar_arrive(&item_full[s]);
         }
@@ -544,7 +544,14 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
         const int n = min(NP, n_cols - st * NP);
         const uint32_t idesc_s = idesc_bf16(128, 16 * n, false, false);
         // the staging set is free once the row threads have loaded step G-1
-        bool w = (G < 1 || mbar_wait(st_free, (G - 1) & 1, ab)) && mbar_wait(&q_full[qs], (G / QS) & 1, ab);
+        // (scored forms wait for the tiles first: what follows st_free is the time
+        // that the row threads wait for)
+        bool w;
+        if constexpr (kScored)
+          w = mbar_wait_warp(&q_full[qs], (G / QS) & 1, ab) && mbar_wait_warp(&do_full[ds], (G / DS) & 1, ab) &&
+              (G < 1 || mbar_wait_warp(st_free, (G - 1) & 1, ab));
+        else
+          w = (G < 1 || mbar_wait(st_free, (G - 1) & 1, ab)) && mbar_wait(&q_full[qs], (G / QS) & 1, ab);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         tc_fence_after();
         const uint64_t bq = sdesc_add(dqk, qs * C::kStageTile);
@@ -554,8 +561,10 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
           umma_ss_w(tmem, sdesc_add(dk0, (kk >> 2) * kChunkBytes + (kk & 3) * 32),
                     sdesc_add(bq, (kk >> 2) * kStageChunk + (kk & 3) * 32), idesc_s, kk > 0);
         if constexpr (!kScored) umma_ss_w(tmem, d_ones, sdesc_add(d_qa, qs * kAugStage), idesc_s, 1u);
-        if (!__all_sync(0xffffffffu, mbar_wait(&do_full[ds], (G / DS) & 1, ab))) { ok = false; break; }
-        tc_fence_after();
+        if constexpr (!kScored) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&do_full[ds], (G / DS) & 1, ab))) { ok = false; break; }
+          tc_fence_after();
+        }
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           umma_ss_w(tmem + 64, sdesc_add(dv0, (kk >> 2) * kChunkBytes + (kk & 3) * 32),
@@ -574,6 +583,9 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     const uint64_t dqm = sdesc_sw128(smem_u32(sQ), kStageChunk, 1024);    // Q stages, MN-major
     const uint64_t ddm = sdesc_sw128(smem_u32(sDO), kStageChunk, 1024);   // dO stages, MN-major
     const uint32_t idesc_acc = idesc_bf16(128, D, false, true);
+    // P^T of page j of packed set b at 128 + 64b + 8j and dS^T 32 columns on; scored
+    // forms: side by side, one store of a row thread
+    constexpr uint32_t kPk = kScored ? 16 : 8;
     int G = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -587,19 +599,22 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       tc_fence_after();
       for (int st = 0; st < n_steps; ++st, ++G) {
         const int b = G & 1, qs = G % QS, ds = G % DS;
-        if (!__all_sync(0xffffffffu, mbar_wait(&pt_full[b], (G >> 1) & 1, ab))) { ok = false; break; }
+        if (!(kScored ? mbar_wait_warp(&pt_full[b], (G >> 1) & 1, ab)
+                      : __all_sync(0xffffffffu, mbar_wait(&pt_full[b], (G >> 1) & 1, ab)))) { ok = false; break; }
         tc_fence_after();
         const int n = min(NP, n_cols - st * NP);
         const uint64_t bq = sdesc_add(dqm, qs * C::kStageTile);
         const uint64_t bd = sdesc_add(ddm, ds * C::kStageTile);
 #pragma unroll
         for (int j = 0; j < NP; ++j)
-          if (j < n) umma_ts_w(tDV, tmem + 128 + 64 * b + 8 * j, sdesc_add(bd, j * 2048), idesc_acc, (st > 0 || j > 0) ? 1u : 0u);
+          if (j < n)
+            umma_ts_w(tDV, tmem + 128 + 64 * b + kPk * j, sdesc_add(bd, j * 2048), idesc_acc, (st > 0 || j > 0) ? 1u : 0u);
         umma_commit_w(&do_empty[ds]);
 #pragma unroll
         for (int j = 0; j < NP; ++j)
           if (j < n)
-            umma_ts_w(tDK, tmem + 160 + 64 * b + 8 * j, sdesc_add(bq, j * 2048), idesc_acc, (st > 0 || j > 0) ? 1u : 0u);
+            umma_ts_w(tDK, tmem + 128 + 64 * b + (kScored ? 8 : 32) + kPk * j, sdesc_add(bq, j * 2048), idesc_acc,
+                      (st > 0 || j > 0) ? 1u : 0u);
         umma_commit_w(&q_empty[qs]);
         umma_commit_w(&acc_b[b]);
       }
@@ -634,21 +649,22 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
         }
       }
       const int4 rows = row_range(seg >= 0, key_pos, key_doc), mine = make_int4(key_pos, key_pos, key_doc, key_doc);
-      // this row's mask of the group's page, fetched a step ahead
-      const uint16_t* mask = reinterpret_cast<const uint16_t*>(col_masks + 2 * static_cast<int64_t>(wk.e0)) + (seg < 0 ? 0 : seg);
-      auto mask_of = [&](int st) -> uint32_t {
-        return seg >= 0 && st * NP + grp < n_cols ? __ldg(mask + 8 * (st * NP + grp)) : 0u;
-      };
-      uint32_t m_next = mask_of(0);
+      // this row's mask of the group's page, fetched a step ahead; `left`: entries
+      // from the group's page of this step on (a row without a segment has none to read)
+      const uint16_t* mask = reinterpret_cast<const uint16_t*>(col_masks + 2 * (static_cast<int64_t>(wk.e0) + grp)) + max(seg, 0);
+      int left = n_cols - grp;
+      uint32_t m_next = seg >= 0 && left > 0 ? __ldg(mask) : 0u;
       for (int st = 0; st < n_steps; ++st, ++G) {
         const int b = G & 1, qs = G % QS;
-        const bool active = st * NP + grp < n_cols;
+        const bool active = left > 0;
         uint32_t m = m_next;
-        m_next = st + 1 < n_steps ? mask_of(st + 1) : 0u;
-        ok = __all_sync(0xffffffffu, mbar_wait(st_full, G & 1, ab));
+        left -= NP;
+        mask += 8 * NP;
+        if (seg >= 0 && left > 0) m_next = __ldg(mask);
+        ok = mbar_wait_warp(st_full, G & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        uint32_t a[CW], d[CW], pp[CW / 2], pd[CW / 2];
+        uint32_t a[CW], d[CW], pk[CW];  // pk: P^T, then dS^T, in bf16
         if (active) {
           tmem_ld16(tmem + lane_off + grp * CW, a);
           tmem_ld16(tmem + 64 + lane_off + grp * CW, d);
@@ -670,18 +686,17 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
           constexpr bool kCap = SC == kScoreCap;
           if (sc.slopes) bias_scores(a, col_posf(qs) + CW * grp, static_cast<float>(key_pos), col_slope(qs)[grp]);
           add_columns(a, col_lse(qs) + CW * grp, kCap ? 1.0f : sl2);
-          weights_and_ds(a, d, m, pp, pd);
+          weights_and_ds(a, d, m, pk);
         }
         // Packed set b still feeds dV(G-2) / dK(G-2).  Every row thread waits, active
         // or not, so that no arrival for step G can land in the pt_full phase of G-2.
-        if (G >= 2 && !__all_sync(0xffffffffu, mbar_wait(&acc_b[b], ((G - 2) >> 1) & 1, ab))) {
+        if (G >= 2 && !mbar_wait_warp(&acc_b[b], ((G - 2) >> 1) & 1, ab)) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (active) {
-          tmem_st8(tmem + 128 + 64 * b + lane_off + grp * (CW / 2), pp);
-          tmem_st8(tmem + 160 + 64 * b + lane_off + grp * (CW / 2), pd);
+          tmem_st16(tmem + 128 + 64 * b + lane_off + grp * CW, pk);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -879,7 +894,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
               const int32_t* __restrict__ work, const int32_t* __restrict__ col_pages,
               const uint64_t* __restrict__ col_masks, const float* __restrict__ lse, const float* __restrict__ delta,
               __nv_bfloat16* __restrict__ out_dq, int64_t q_slots, float sl2, float scale, int heads, int kv_group,
-              int* err, const ScoreArgs sc, int64_t kv_slots) {
+              int* err, const ScoreArgs sc, int64_t kv_slots, const int32_t* __restrict__ order) {
   using C = DqCfg<D>;
   constexpr bool kScored = SC != kScoreNone, kCap = SC == kScoreCap;
   using W = BwdWarps<kScored>;
@@ -917,7 +932,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
   };
   const bool use_cols = kScored && (sc.q_last || sc.q_doc || sc.slopes);
 
-  const Work wk = load_work(work, blockIdx.x);
+  const Work wk = load_work(work, kScored && order ? __ldg(order + blockIdx.x) : blockIdx.x);
   // K/V head of this item's query head (grouped-query attention)
   const int kv_bh = (wk.bh / heads) * (heads / kv_group) + (wk.bh % heads) / kv_group;
   const int n_cols = wk.e1 - wk.e0;
@@ -1053,7 +1068,12 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       const int n = min(NP, n_cols - st * NP);
       const uint32_t idesc_s = idesc_bf16(128, 16 * n, false, false);
       // staging set b is free once the row threads have loaded step st-2
-      bool w = (st < 2 || mbar_wait(&s_free[b], ((st - 2) >> 1) & 1, ab)) && mbar_wait(&k_full[ks], (t / KS) & 1, ab);
+      bool w;
+      if constexpr (kScored)
+        w = mbar_wait_warp(&k_full[ks], (t / KS) & 1, ab) && mbar_wait_warp(&v_full[vs], (t / VS) & 1, ab) &&
+            (st < 2 || mbar_wait_warp(&s_free[b], ((st - 2) >> 1) & 1, ab));
+      else
+        w = (st < 2 || mbar_wait(&s_free[b], ((st - 2) >> 1) & 1, ab)) && mbar_wait(&k_full[ks], (t / KS) & 1, ab);
       if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
       tc_fence_after();
       const uint64_t bk = sdesc_add(dkk, ks * C::kStageTile + half * kHalfStage);
@@ -1061,8 +1081,10 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         umma_ts_w(tS(b), tQ + 8 * kk, sdesc_add(bk, (kk >> 2) * kStageChunk + (kk & 3) * 32), idesc_s, kk > 0);
-      if (!__all_sync(0xffffffffu, mbar_wait(&v_full[vs], (t / VS) & 1, ab))) { ok = false; break; }
-      tc_fence_after();
+      if constexpr (!kScored) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&v_full[vs], (t / VS) & 1, ab))) { ok = false; break; }
+        tc_fence_after();
+      }
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         umma_ss_w(tDP(b), sdesc_add(ddo0, (kk >> 2) * kChunkBytes + (kk & 3) * 32),
@@ -1081,7 +1103,8 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     for (int st = 0; ok && st < n_steps; ++st) {
       const int p = st & 1, t = st / SPS, half = st % SPS, ks = t % KS;
       const bool stage_end = half == SPS - 1 || st + 1 == n_steps;
-      if (!__all_sync(0xffffffffu, mbar_wait(&ds_full[p], (st >> 1) & 1, ab))) { ok = false; break; }
+      if (!(kScored ? mbar_wait_warp(&ds_full[p], (st >> 1) & 1, ab)
+                    : __all_sync(0xffffffffu, mbar_wait(&ds_full[p], (st >> 1) & 1, ab)))) { ok = false; break; }
       tc_fence_after();
       const int n = min(NP, n_cols - st * NP);
       const uint64_t bk = sdesc_add(dkm, ks * C::kStageTile + half * kHalfStage);
@@ -1170,20 +1193,21 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       }
       return bits;
     };
-    // this row's mask of the group's page, fetched a step ahead
-    const uint16_t* mask = reinterpret_cast<const uint16_t*>(col_masks + 2 * static_cast<int64_t>(wk.e0)) + (seg < 0 ? 0 : seg);
-    auto mask_of = [&](int st) -> uint32_t {
-      return seg >= 0 && st * NP + grp < n_cols ? __ldg(mask + 8 * (st * NP + grp)) : 0u;
-    };
+    // this row's mask of the group's page, fetched a step ahead; `left`: entries
+    // from the group's page of this step on (a row without a segment has none to read)
+    const uint16_t* mask = reinterpret_cast<const uint16_t*>(col_masks + 2 * (static_cast<int64_t>(wk.e0) + grp)) + max(seg, 0);
+    int left = n_cols - grp;
+    uint32_t m_next = seg >= 0 && left > 0 ? __ldg(mask) : 0u;
     const uint64_t ndl = f2_pack(-dl, -dl), nl2 = f2_pack(nlse2, nlse2);
     bool ok = true;
-    uint32_t m_next = n_steps > 0 ? mask_of(0) : 0u;
     for (int st = 0; st < n_steps; ++st) {
       const int b = st & 1, t = st / SPS, ks = t % KS;
-      const bool active = st * NP + grp < n_cols;
+      const bool active = left > 0;
       uint32_t m = m_next;
-      m_next = st + 1 < n_steps ? mask_of(st + 1) : 0u;
-      ok = __all_sync(0xffffffffu, mbar_wait(&sd_full[b], (st >> 1) & 1, ab));
+      left -= NP;
+      mask += 8 * NP;
+      if (seg >= 0 && left > 0) m_next = __ldg(mask);
+      ok = mbar_wait_warp(&sd_full[b], (st >> 1) & 1, ab);
       if (!ok) break;
       if (active && (sc.q_last || sc.q_doc)) {
         const int4 rg = col_rng(ks)[2 * (st % SPS) + (grp >> 1)];
@@ -1194,7 +1218,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
           m &= step_bits(st);
       }
       tc_fence_after();
-      uint32_t a[CW], d[CW], pp[CW / 2], pd[CW / 2];
+      uint32_t a[CW], d[CW], pd[CW / 2];
       if (active) {
         tmem_ld16(tS(b) + lane_off + grp * CW, a);
         tmem_ld16(tDP(b) + lane_off + grp * CW, d);
@@ -1219,11 +1243,11 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
           a[i] = __float_as_uint(x0);
           a[i + 1] = __float_as_uint(x1);
         }
-        weights_and_ds(a, d, m, pp, pd);
+        weights_and_ds(a, d, m, pd);
       }
       // Packed set b still feeds dQ(st-2).  Every row thread waits, active or not:
       // dq_done(st-2) implies that ds_full finished the phase of step st-2.
-      if (st >= 2 && !__all_sync(0xffffffffu, mbar_wait(&dq_done[b], ((st - 2) >> 1) & 1, ab))) {
+      if (st >= 2 && !mbar_wait_warp(&dq_done[b], ((st - 2) >> 1) & 1, ab)) {
         ok = false;
         break;
       }
@@ -1439,7 +1463,7 @@ static cudaError_t launch_dkdv_t(const TmaPages& tk, const TmaPages& tv, const T
   const int64_t grid = std::min<int64_t>(a.n_work, std::max(sms, 1));
   dkdv_kernel<D, SC><<<static_cast<unsigned>(grid), BwdWarps<SC != kScoreNone>::kThreads, kSmem, st>>>(
       tk, tv, tq, tdo, a.work, a.n_work, a.sched, a.pages, a.masks, lse, delta, dk, dv, a.own_slots, a.col_slots,
-      a.scale * kLog2e, a.scale, a.heads, a.kv_heads, a.kv_group, a.col_heads, a.err, sc);
+      a.scale * kLog2e, a.scale, a.heads, a.kv_heads, a.kv_group, a.col_heads, a.err, sc, a.order);
   return cudaGetLastError();
 }
 
@@ -1453,7 +1477,7 @@ static cudaError_t launch_dq_t(const __nv_bfloat16* q, const TmaPages& tdo, cons
   if (e != cudaSuccess || a.n_work == 0) return e;
   dq_kernel<D, SC><<<static_cast<unsigned>(a.n_work), BwdWarps<SC != kScoreNone>::kThreads, kSmem, st>>>(
       q, tdo, tk, tv, a.work, a.pages, a.masks, lse, delta, dq, a.own_slots, a.scale * kLog2e, a.scale, a.heads,
-      a.kv_group, a.err, sc, a.col_slots);
+      a.kv_group, a.err, sc, a.col_slots, a.order);
   return cudaGetLastError();
 }
 

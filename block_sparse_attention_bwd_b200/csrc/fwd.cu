@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
                const int32_t* __restrict__ col_pages, const uint64_t* __restrict__ col_masks,
                __nv_bfloat16* __restrict__ out_o, float* __restrict__ out_lse, int64_t q_slots, float sl2,
                int heads, int kv_group, const float* __restrict__ q_descale, const float* __restrict__ k_descale,
-               int* err, const ScoreArgs sc, int64_t kv_slots, int64_t n_work, const FillArgs fill) {
+               int* err, const ScoreArgs sc, int64_t kv_slots, int64_t n_work, const FillArgs fill, const int32_t* __restrict__ order) {
   using C = FwdCfg<D, F8>;
   constexpr int KS = C::kKStages, VS = C::kVStages, NP = kFwdStepPages;
   extern __shared__ uint8_t smem_raw[];
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
       return;
     }
   }
-  const Work wk = load_work(work, blockIdx.x);
+  const Work wk = load_work(work, SC != kScoreNone && order ? __ldg(order + blockIdx.x) : blockIdx.x);
   // K/V head of this item's query head (grouped-query attention)
   const int kv_bh = (wk.bh / heads) * (heads / kv_group) + (wk.bh % heads) / kv_group;
   const int n_cols = wk.e1 - wk.e0;
@@ -652,7 +652,7 @@ cudaError_t launch_fwd_r(const TmaPages& tq, const TmaPages& tk, const TmaPages&
   if (blocks == 0) return cudaSuccess;
   fwd_kernel<D, F8, ROUTE, SC><<<static_cast<unsigned>(blocks), kFwdThreads<SC>, kSmem, st>>>(
       tq, tk, tv, a.work, a.pages, a.masks, o, lse, a.own_slots, a.scale * kLog2e, a.heads, a.kv_group, q_descale,
-      k_descale, a.err, sc, a.col_slots, a.n_work, fill);
+      k_descale, a.err, sc, a.col_slots, a.n_work, fill, a.order);
   return cudaGetLastError();
 }
 

@@ -45,6 +45,7 @@ struct TileArgs {
   // pass, entry e's column head is the item's first query head + col_heads[e].
   int heads = 1, kv_heads = 1, kv_group = 1;
   const uint16_t* col_heads = nullptr;
+  const int32_t* order = nullptr;  // the items longest first over all heads (scored forms; null: as listed)
   // some query-owned item takes the 64-row route (the forward then runs the
   // kernel form that reads the route flag of each item)
   bool route64 = false;
@@ -52,11 +53,13 @@ struct TileArgs {
 
 // tanh cap c of scores x = scale * s, in the forms the kernels use (cap_args).
 struct CapArgs {
-  float a[5];   // c log2(e) tanh(scale s / c) = s (a0 + a1 w + ... + a4 w^4), w = s^2 ...
+  // c log2(e) tanh(scale s / c) = s (a0 + a1 w + ... + a4 w^4), w = s^2 (each
+  // coefficient twice, as the packed arithmetic takes it) ...
+  uint64_t a[5];
+  uint64_t ng;  // -1 / cap2^2, twice
   float w_max;  // ... for w up to this (|scale s / c| <= 1/2)
   float k2;     // 2 log2(e) scale / c
   float cap2;   // c log2(e)
-  float ng;     // -1 / cap2^2
 };
 CapArgs cap_args(float cap, float scale);
 // Caps up to this (in log2 units) keep 2^z and its sums inside fp32 without a

@@ -1020,6 +1020,8 @@ void free_plan_device(spattn_plan_s* P) {
   free_device_planner(P->dp);
   cudaFree(P->wk.d_heads);
   P->wk.d_heads = nullptr;
+  cudaFree(P->wq.d_order);
+  cudaFree(P->wk.d_order);
   cudaFree(P->wq.d_work);
   cudaFree(P->wq.d_pages);
   cudaFree(P->wq.d_masks);
@@ -1187,6 +1189,14 @@ int build_plan(const spattn_layout* L, const spattn_graph* G, spattn_plan_s* P) 
     if ((st = upload(w->work, &w->d_work, bytes, &w->cap_work))) return st;
     if ((st = upload(w->pages, &w->d_pages, bytes, &w->cap_pages))) return st;
     if ((st = upload(w->masks, &w->d_masks, bytes, &w->cap_masks))) return st;
+    if (w->n_work > 0 && w->n_work <= kOrderMax) {
+      std::vector<int32_t> order(static_cast<size_t>(w->n_work));
+      for (size_t i = 0; i < order.size(); ++i) order[i] = static_cast<int32_t>(i);
+      auto len = [&](int32_t i) { return w->work[i * kWorkWords + 3] - w->work[i * kWorkWords + 2]; };
+      std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return len(a) > len(b); });
+      if ((st = upload(order, &w->d_order, bytes, &w->cap_order))) return st;
+      w->ordered = true;
+    }
   }
   if ((st = upload(P->q_fill, &P->d_q_fill, bytes))) return st;
   if ((st = upload(P->k_fill, &P->d_k_fill, bytes))) return st;

@@ -71,11 +71,24 @@ struct WorkList {
   int32_t* d_work = nullptr;
   int32_t* d_pages = nullptr;
   uint64_t* d_masks = nullptr;
+  // the items by falling list length over all heads, for the scored kernels
+  // (kOrderMax; null where there are more, ordered false after a device re-plan)
+  int32_t* d_order = nullptr;
+  int64_t cap_order = 0;
+  bool ordered = false;
   // capacities of the device arrays (elements) and, after a device re-plan,
   // the number of entries on the device
   int64_t cap_work = 0, cap_pages = 0, cap_masks = 0, cap_heads = 0;
   int64_t n_entries_dev = -1;
 };
+
+// A head's items run longest first, one head after another, which keeps a head's
+// K and V in the L2 cache.  With few items per SM the last head's long items then
+// end late; up to this many items (32 per SM) the scored kernels take the longest
+// of all heads first instead.  List steps of the busiest SM on causal rows of 12289
+// tokens, 16 query heads over 4: forward 630 -> 540, dK / dV 1360 -> 1140; on 16384
+// tokens of short documents, 16 heads: 111 -> 94 and 201 -> 186.
+constexpr int64_t kOrderMax = 32 * 148;
 
 // Work item templates of one pass for the device planner: the slot-order
 // tiles of the layout split into items, without their column lists.

@@ -64,9 +64,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], uint32_t (&d)[N], c
     mx[i & 1] = fmax3(mx[i & 1], a, b);  // a NaN drops out here and keeps its NaN in either form
   }
   if (__builtin_expect(!__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > c.w_max), 1)) {
-    const uint64_t a0 = f2_pack(c.a[0], c.a[0]), a1 = f2_pack(c.a[1], c.a[1]), a2 = f2_pack(c.a[2], c.a[2]),
-                   a3 = f2_pack(c.a[3], c.a[3]), a4 = f2_pack(c.a[4], c.a[4]);
-    const uint64_t ng = f2_pack(c.ng, c.ng), one = f2_pack(1.f, 1.f);
+    const uint64_t a0 = c.a[0], a1 = c.a[1], a2 = c.a[2], a3 = c.a[3], a4 = c.a[4], ng = c.ng, one = f2_pack(1.f, 1.f);
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       const uint64_t x = pair(i), w = kKeep ? sq[kKeep ? i : 0] : f2_mul(x, x);
@@ -132,13 +130,14 @@ __device__ __forceinline__ void add_columns(uint32_t (&s)[N], const float* col, 
   }
 }
 
-// dS of one row and its weights, N columns: w = 2^x (x = log2 of the weight, in
-// `s`), ds = w d, both packed to bf16.  Columns whose bit is clear get zeros, and
-// dS is dropped where the weight rounds to one (live_weight).
+// dS of one row, N columns, and its weights: w = 2^x (x = log2 of the weight, in
+// `s`), ds = w d, both in bf16; `out` holds dS, or with 2 N / 2 words the weights
+// and then dS.  Columns whose bit is clear get zeros, and dS is dropped where the
+// weight rounds to one (live_weight).
 __device__ __forceinline__ bool live_weight(float p);
-template <int N>
-__device__ __forceinline__ void weights_and_ds(uint32_t (&s)[N], uint32_t (&d)[N], uint32_t bits, uint32_t (&pp)[N / 2],
-                                               uint32_t (&pd)[N / 2]) {
+template <int N, int W>
+__device__ __forceinline__ void weights_and_ds(uint32_t (&s)[N], uint32_t (&d)[N], uint32_t bits, uint32_t (&out)[W]) {
+  static_assert(W == N / 2 || W == N, "dS, or weights and dS");
 #pragma unroll
   for (int i = 0; i < N; ++i) s[i] = __float_as_uint(ex2(__uint_as_float(s[i])));
   if (__builtin_expect(bits != (N == 32 ? 0xFFFFFFFFu : (1u << (N & 31)) - 1u), 0)) {
@@ -154,8 +153,8 @@ __device__ __forceinline__ void weights_and_ds(uint32_t (&s)[N], uint32_t (&d)[N
     const float p0 = __uint_as_float(s[2 * i]), p1 = __uint_as_float(s[2 * i + 1]);
     float s0, s1;
     f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]))), s0, s1);
-    pp[i] = pack_bf16(p0, p1);
-    pd[i] = pack_bf16(s0, s1);
+    if constexpr (W == N) out[i] = pack_bf16(p0, p1);
+    out[W - N / 2 + i] = pack_bf16(s0, s1);
   }
 }
 

@@ -108,6 +108,29 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
+// The same for a whole warp in a hot loop: a first run of polls without the
+// bookkeeping (few instructions matter where warps compete for issue slots),
+// then mbar_wait.  Warp-uniform: false for all lanes if any lane gave up.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const Abort& ab) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 64;\n\t"
+      "WAIT:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra WAIT;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (__builtin_expect(__all_sync(0xffffffffu, ok != 0u), 1)) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
+}
+
 // Same, ignoring the abort flag (used during teardown to drain async work),
 // with a short deadline.
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) {
