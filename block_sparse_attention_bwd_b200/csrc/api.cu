@@ -320,8 +320,10 @@ int run_bwd(const void* q, const void* k, const void* v, const void* o, const fl
     });
   if (e == cudaSuccess)
     e = timed(plan, SPATTN_K_DQ, s, [&] {
-      return launch_dq(D, static_cast<const __nv_bfloat16*>(q), tdo, tk, tv, tile_args(plan, plan->wq, plan->q.slots, plan->k.slots), sc,
-                       lse, plan->d_delta, dQ, s);
+      TileArgs t = tile_args(plan, plan->wq, plan->q.slots, plan->k.slots);
+      // (an event between the two, when profiling, keeps them apart)
+      t.beside = sc && plan->wk.n_work > 0 && !plan->profiling;
+      return launch_dq(D, static_cast<const __nv_bfloat16*>(q), tdo, tk, tv, t, sc, lse, plan->d_delta, dQ, s);
     });
   if (!sc && e == cudaSuccess && !plan->k_fill.empty())
     e = timed(plan, SPATTN_K_FILL, s, [&] {

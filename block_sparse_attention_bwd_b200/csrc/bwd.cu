@@ -317,6 +317,9 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tslot;
   const uint32_t tDV = tmem + 256, tDK = tmem + 256 + D;
+  // The scored dQ kernel needs nothing from this one: once every CTA is here (all
+  // are resident), its CTAs may take the SMs that are free or become so.
+  if constexpr (kScored) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Item k of this CTA (k = 0, 1, ...): the readers wait for its queue slot,
   // read it and release the slot; -1 ends the loop (also on abort).
@@ -1416,6 +1419,9 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // launched beside the dK / dV kernel: what follows in the stream waits for this
+  // kernel only, so this one ends after that one
+  if constexpr (kScored) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace
@@ -1475,10 +1481,19 @@ static cudaError_t launch_dq_t(const __nv_bfloat16* q, const TmaPages& tdo, cons
   constexpr int kSmem = C::kSmem + (SC != kScoreNone ? C::kScoreBytes : 0);
   cudaError_t e = cudaFuncSetAttribute(dq_kernel<D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess || a.n_work == 0) return e;
-  dq_kernel<D, SC><<<static_cast<unsigned>(a.n_work), BwdWarps<SC != kScoreNone>::kThreads, kSmem, st>>>(
-      q, tdo, tk, tv, a.work, a.pages, a.masks, lse, delta, dq, a.own_slots, a.scale * kLog2e, a.scale, a.heads,
-      a.kv_group, a.err, sc, a.col_slots, a.order);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_work));
+  cfg.blockDim = dim3(BwdWarps<SC != kScoreNone>::kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute beside = {};
+  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  beside.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &beside;
+  cfg.numAttrs = a.beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, dq_kernel<D, SC>, q, tdo, tk, tv, a.work, a.pages, a.masks, lse, delta, dq,
+                            a.own_slots, a.scale * kLog2e, a.scale, a.heads, a.kv_group, a.err, sc, a.col_slots,
+                            a.order);
 }
 
 // Calls `go` with the head size and the form of the scores as constants.

@@ -45,6 +45,8 @@ struct TileArgs {
   // pass, entry e's column head is the item's first query head + col_heads[e].
   int heads = 1, kv_heads = 1, kv_group = 1;
   const uint16_t* col_heads = nullptr;
+  // launch_dq right behind launch_dkdv, both scored: it may run beside that kernel
+  bool beside = false;
   const int32_t* order = nullptr;  // the items longest first over all heads (scored forms; null: as listed)
   // some query-owned item takes the 64-row route (the forward then runs the
   // kernel form that reads the route flag of each item)
