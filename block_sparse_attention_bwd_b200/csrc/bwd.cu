@@ -79,6 +79,7 @@ struct PrepArgs {
 };
 template <int D>
 __global__ void __launch_bounds__(256) prep_kernel(const PrepArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the exact Delta of short items waits on its own
   if (static_cast<int>(blockIdx.x) >= a.n_delta) {
     const int64_t first = blockIdx.x - a.n_delta, step = gridDim.x - a.n_delta;
     for (int64_t i = first; i < a.q.n * a.q.bh; i += step) fill_rows<D>(a.q, i % a.q.n, i / a.q.n);
@@ -890,14 +891,23 @@ struct DqCfg {
 };
 
 // SC: the scored forms (score.cuh).
-template <int D, int SC>
+//
+// DELTA: no dQ, but Delta_i = sum_j P_ij dP_ij for the rows of an item, from the
+// weights themselves.  Delta = dO.O inherits the rounding of O, 2^-9 of |dO| |O|
+// or so.  In a row of many keys O is small against V and that is lost in the
+// rounding of dS; in a row of two or five keys dP - Delta is a difference of like
+// numbers, and dQ came out 1% off (its own roundings are 0.24%).  Items of up to
+// 256 keys therefore get this pass (their rows are where keys are few, and it costs
+// a few steps each); it overwrites what Delta = dO.O gave.
+template <int D, int SC, bool DELTA>
 __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     dq_kernel(const __nv_bfloat16* __restrict__ q, const __grid_constant__ TmaPages tm_do,
               const __grid_constant__ TmaPages tm_k, const __grid_constant__ TmaPages tm_v,
               const int32_t* __restrict__ work, const int32_t* __restrict__ col_pages,
               const uint64_t* __restrict__ col_masks, const float* __restrict__ lse, const float* __restrict__ delta,
               __nv_bfloat16* __restrict__ out_dq, int64_t q_slots, float sl2, float scale, int heads, int kv_group,
-              int* err, const ScoreArgs sc, int64_t kv_slots, const int32_t* __restrict__ order) {
+              int* err, const ScoreArgs sc, int64_t kv_slots, const int32_t* __restrict__ order, int short_entries,
+              float* __restrict__ out_delta) {
   using C = DqCfg<D>;
   constexpr bool kScored = SC != kScoreNone, kCap = SC == kScoreCap;
   using W = BwdWarps<kScored>;
@@ -941,6 +951,12 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
   const int n_cols = wk.e1 - wk.e0;
   const int n_steps = (n_cols + NP - 1) / NP;
   const int warp = warp_id(), lane = lane_id();
+  if constexpr (DELTA) {
+    if (n_cols > short_entries || n_cols == 0) {  // (a row without keys keeps its 0)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      return;
+    }
+  }
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -1113,7 +1129,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       const uint64_t bk = sdesc_add(dkm, ks * C::kStageTile + half * kHalfStage);
 #pragma unroll
       for (int j = 0; j < NP; ++j)
-        if (j < n) umma_ts_w(tDQ, tPk(p) + 8 * j, sdesc_add(bk, j * 2048), idesc_acc, (st > 0 || j > 0) ? 1u : 0u);
+        if (!DELTA && j < n) umma_ts_w(tDQ, tPk(p) + 8 * j, sdesc_add(bk, j * 2048), idesc_acc, (st > 0 || j > 0) ? 1u : 0u);
       if (stage_end) umma_commit_w(&k_empty[ks]);
       umma_commit_w(&dq_done[p]);
     }
@@ -1159,7 +1175,8 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     }
     const float lse_row = (valid_slot && seg >= 0) ? __ldg(lse + roff) : 0.f;
     const float nlse2 = lse_row == -INFINITY ? -INFINITY : -lse_row * kLog2e;  // -inf: no key, every weight 0
-    const float dl = (valid_slot && seg >= 0) ? __ldg(delta + roff) : 0.f;
+    const float dl = (!DELTA && valid_slot && seg >= 0) ? __ldg(delta + roff) : 0.f;
+    float delta_sum = 0.f;  // DELTA: this group's part of the row's sum
     // this row's side of the masks and the bias
     int row_last = 0, row_doc = -1;
     float row_pos = 0.f, slope = 0.f;
@@ -1230,14 +1247,16 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       tc_fence_before();
       mbar_arrive(&s_free[b]);
       if (active) {
+        if constexpr (!DELTA) {
 #pragma unroll
-        for (int i = 0; i < CW; i += 2) {
-          float x0, x1;
-          f2_unpack(f2_add(f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), ndl), x0, x1);
-          d[i] = __float_as_uint(x0);
-          d[i + 1] = __float_as_uint(x1);
+          for (int i = 0; i < CW; i += 2) {
+            float x0, x1;
+            f2_unpack(f2_add(f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), ndl), x0, x1);
+            d[i] = __float_as_uint(x0);
+            d[i + 1] = __float_as_uint(x1);
+          }
         }
-        if constexpr (kCap) cap_scores<true>(a, d, sc.c);
+        if constexpr (kCap) cap_scores<!DELTA>(a, d, sc.c);
         if (sc.slopes) bias_scores(a, col_posf(ks) + 64 * (st % SPS) + CW * grp, row_pos, slope);
 #pragma unroll
         for (int i = 0; i < CW; i += 2) {
@@ -1246,7 +1265,13 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
           a[i] = __float_as_uint(x0);
           a[i + 1] = __float_as_uint(x1);
         }
-        weights_and_ds(a, d, m, pd);
+        if constexpr (DELTA) {
+#pragma unroll
+          for (int i = 0; i < CW; ++i)
+            if ((m >> i) & 1u) delta_sum = fmaf(ex2(__uint_as_float(a[i])), __uint_as_float(d[i]), delta_sum);
+        } else {
+          weights_and_ds(a, d, m, pd);
+        }
       }
       // Packed set b still feeds dQ(st-2).  Every row thread waits, active or not:
       // dq_done(st-2) implies that ds_full finished the phase of step st-2.
@@ -1255,7 +1280,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
         break;
       }
       tc_fence_after();
-      if (active) {
+      if (!DELTA && active) {
         tmem_st8(tPk(b) + lane_off + grp * (CW / 2), pd);
         tmem_wait_st();
       }
@@ -1266,7 +1291,9 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, ab));
       tc_fence_after();
     }
-    if (ok) {
+    // (the dO tile's last readers, the products of the last step, are done)
+    if constexpr (DELTA) reinterpret_cast<float*>(sDO)[128 * grp + row] = delta_sum;
+    if (!DELTA && ok) {
       // group g writes columns [g*D/4, (g+1)*D/4) of dQ
       constexpr int kOut = D / NG;  // 32 or 16
       const int col = grp * kOut;
@@ -1419,9 +1446,19 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // launched beside the dK / dV kernel: what follows in the stream waits for this
-  // kernel only, so this one ends after that one
+  // launched beside the dK / dV kernel (DELTA: beside the one that writes every
+  // row's Delta first): what follows in the stream waits for this kernel only, so
+  // this one ends after that one
   if constexpr (kScored) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (DELTA) {
+    const int row = threadIdx.x;
+    if (row < 16 * wk.n_own && wk.row_code(row) < 8u && !*abort_flag) {
+      const int64_t slot = pref_slot(wk.own_page(row >> 4), row & 15);
+      const float* part = reinterpret_cast<const float*>(sDO) + row;
+      if (slot < q_slots)
+        out_delta[static_cast<int64_t>(wk.bh) * q_slots + slot] = (part[0] + part[128]) + (part[256] + part[384]);
+    }
+  }
 }
 
 }  // namespace
@@ -1473,16 +1510,17 @@ static cudaError_t launch_dkdv_t(const TmaPages& tk, const TmaPages& tv, const T
   return cudaGetLastError();
 }
 
-template <int D, int SC>
+template <int D, int SC, bool DELTA>
 static cudaError_t launch_dq_t(const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
                                const TmaPages& tv, const TileArgs& a, const ScoreArgs& sc, const float* lse,
-                               const float* delta, __nv_bfloat16* dq, cudaStream_t st) {
+                               const float* delta, __nv_bfloat16* dq, int64_t n_items, int short_entries,
+                               float* out_delta, cudaStream_t st) {
   using C = DqCfg<D>;
   constexpr int kSmem = C::kSmem + (SC != kScoreNone ? C::kScoreBytes : 0);
-  cudaError_t e = cudaFuncSetAttribute(dq_kernel<D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess || a.n_work == 0) return e;
+  cudaError_t e = cudaFuncSetAttribute(dq_kernel<D, SC, DELTA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess || n_items == 0) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.n_work));
+  cfg.gridDim = dim3(static_cast<unsigned>(n_items));
   cfg.blockDim = dim3(BwdWarps<SC != kScoreNone>::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
@@ -1491,9 +1529,11 @@ static cudaError_t launch_dq_t(const __nv_bfloat16* q, const TmaPages& tdo, cons
   beside.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &beside;
   cfg.numAttrs = a.beside ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, dq_kernel<D, SC>, q, tdo, tk, tv, a.work, a.pages, a.masks, lse, delta, dq,
+  // short items are the last ones of the order
+  const int32_t* order = DELTA && a.order ? a.order + (a.n_work - n_items) : a.order;
+  return cudaLaunchKernelEx(&cfg, dq_kernel<D, SC, DELTA>, q, tdo, tk, tv, a.work, a.pages, a.masks, lse, delta, dq,
                             a.own_slots, a.scale * kLog2e, a.scale, a.heads, a.kv_group, a.err, sc, a.col_slots,
-                            a.order);
+                            order, short_entries, out_delta);
 }
 
 // Calls `go` with the head size and the form of the scores as constants.
@@ -1522,8 +1562,19 @@ cudaError_t launch_dq(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo,
                       const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, const float* lse,
                       const float* delta, __nv_bfloat16* dq, cudaStream_t st) {
   const auto go = [&](auto d, auto form) {
-    return launch_dq_t<decltype(d)::value, decltype(form)::value>(q, tdo, tk, tv, a, sc ? *sc : ScoreArgs(), lse, delta,
-                                                                  dq, st);
+    return launch_dq_t<decltype(d)::value, decltype(form)::value, false>(q, tdo, tk, tv, a, sc ? *sc : ScoreArgs(), lse,
+                                                                         delta, dq, a.n_work, 0, nullptr, st);
+  };
+  return by_form(head_dim, sc, go);
+}
+
+cudaError_t launch_delta_exact(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
+                               const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, int64_t n_short,
+                               int short_entries, const float* lse, float* delta, cudaStream_t st) {
+  const auto go = [&](auto d, auto form) {
+    constexpr int kForm = decltype(form)::value == kScoreNone ? kScoreMask : decltype(form)::value;  // always scored
+    return launch_dq_t<decltype(d)::value, kForm, true>(q, tdo, tk, tv, a, *sc, lse, nullptr, nullptr,
+                                                        a.order ? n_short : a.n_work, short_entries, delta, st);
   };
   return by_form(head_dim, sc, go);
 }

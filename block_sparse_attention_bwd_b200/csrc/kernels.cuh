@@ -96,6 +96,13 @@ struct FillArgs {
 cudaError_t launch_prep(int head_dim, const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* delta, int64_t rows,
                         int* sched, const FillArgs& q, const FillArgs& k, cudaStream_t st);
 
+// Exact Delta for the query-owned items of at most `short_entries` entries
+// (`n_short`: how many the end of a.order holds; without an order every item
+// is looked at), right behind launch_prep and beside it.
+cudaError_t launch_delta_exact(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
+                               const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, int64_t n_short,
+                               int short_entries, const float* lse, float* delta, cudaStream_t st);
+
 // K1: O, LSE for every query-owned work item; `sc` (may be null) modifies the scores,
 // and with it the launch also does `fill`.
 cudaError_t launch_fwd(int head_dim, const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
