@@ -441,10 +441,6 @@ def _torch():
     return _TORCH
 
 
-def _same_device(t, name, device):
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
-
 
 def _want(t, name, shape, dtype, device):
     """_need, and on the given device."""
@@ -467,10 +463,18 @@ def _device_of(t, name):
     return t.device
 
 
+def _current_device_of(t, name):
+    """The tensor's device, which a call with a plan needs to be the current one (the plan's is checked there)."""
+    dev = _device_of(t, name)
+    if dev.index != _torch().cuda.current_device():
+        raise ValueError(f"{name}: is on {dev}, but the current device is cuda:{_torch().cuda.current_device()}")
+    return dev
+
+
 def spattn_fwd_scored(q, k, v, plan: Plan, score: Score, o=None, lse=None, stream=None):
     """O [B,H,Sq,D] bf16 and LSE [B,H,Sq] fp32 for the plan's sparse graph with modified scores."""
     torch = _torch()
-    dev, bf16 = _device_of(q, "q"), torch.bfloat16
+    dev, bf16 = _current_device_of(q, "q"), torch.bfloat16
     qs = (plan.batch, plan.heads, plan.q_slots, plan.head_dim)
     ks = (plan.batch, plan.kv_heads, plan.kv_slots, plan.head_dim)
     _want(q, "q", qs, bf16, dev)
@@ -493,7 +497,7 @@ def spattn_fwd_scored(q, k, v, plan: Plan, score: Score, o=None, lse=None, strea
 def spattn_bwd_scored(q, k, v, o, lse, do, plan: Plan, score: Score, dq=None, dk=None, dv=None, stream=None):
     """dQ, dK, dV (bf16) of :func:`spattn_fwd_scored` with the same score, given its O and LSE and the loss gradient dO."""
     torch = _torch()
-    dev, bf16 = _device_of(q, "q"), torch.bfloat16
+    dev, bf16 = _current_device_of(q, "q"), torch.bfloat16
     qs = (plan.batch, plan.heads, plan.q_slots, plan.head_dim)
     ks = (plan.batch, plan.kv_heads, plan.kv_slots, plan.head_dim)
     _want(q, "q", qs, bf16, dev)
@@ -731,7 +735,7 @@ def spattn_paged_fwd(q, k_cache, v_cache, page_table, q_start, kv_len, paged: Pa
     """
     torch = _torch()
     H, Hk, D, ps = paged.heads, paged.kv_heads, paged.head_dim, paged.page_slots
-    dev, bf16, i32 = _device_of(q, "q"), torch.bfloat16, torch.int32
+    dev, bf16, i32 = _current_device_of(q, "q"), torch.bfloat16, torch.int32
     if q.dtype is not bf16 or q.dim() != 3 or q.shape[1:] != (H, D) or q.stride(2) != 1:
         raise ValueError(f"q: expected a CUDA bf16 tensor [tokens, {H}, {D}], contiguous in its last dimension")
     T = q.shape[0]
@@ -775,7 +779,8 @@ def spattn_paged_fwd(q, k_cache, v_cache, page_table, q_start, kv_len, paged: Pa
     elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or workspace.dtype is not torch.uint8 \
             or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous uint8 tensor on {dev}")
-    c = _PACK_PAGED.pack(q.data_ptr(), q.stride(0), q.stride(1), T, k_cache.data_ptr(), v_cache.data_ptr(), *strides,
+    # (the stride of a single token or head means nothing)
+    c = _PACK_PAGED.pack(q.data_ptr(), q.stride(0) if T > 1 else 0, q.stride(1) if H > 1 else 0, T, k_cache.data_ptr(), v_cache.data_ptr(), *strides,
                          pages, page_table.data_ptr(), width, n, q_start.data_ptr(), kv_len.data_ptr(),
                          0 if slopes is None else slopes.data_ptr(), o.data_ptr(), lse.data_ptr(),
                          0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())

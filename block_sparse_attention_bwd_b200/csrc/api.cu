@@ -209,10 +209,11 @@ CapArgs cap_args(float cap, float scale) {
     r.a[i] = twice(t[i] * p);
     fits = fits && std::fabs(t[i] * p) < 1e30;
   }
+  fits = fits && cap2 > 1e-15;
   r.w_max = fits ? static_cast<float>(0.25 / (k * k)) : -1.f;  // never the polynomial where a coefficient overflows
-  r.k2 = static_cast<float>(2 * kLog2E * k);
+  r.k2 = static_cast<float>(std::fmin(2 * kLog2E * k, 1e37));   // finite, so that a score of 0 stays 0
   r.cap2 = static_cast<float>(cap2);
-  r.ng = twice(-1.0 / (cap2 * cap2));
+  r.ng = twice(fits ? -1.0 / (cap2 * cap2) : 0.0);
   return r;
 }
 

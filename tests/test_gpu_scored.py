@@ -210,6 +210,26 @@ def test_large_scores_and_values():
     _check(p, t, out, arrays, 4.0, None)
 
 
+@pytest.mark.parametrize("cap", [1e-40, 1e-20, 1e-6, 1e30])
+def test_extreme_caps(cap):
+    """Caps whose scaled coefficients leave fp32; queries of zeros (scores of exactly 0) among the rows."""
+    p = _token_problem(90, head_dim=64)
+    t = W.make_tensors(p)
+    t["q"][:, :, 20:30] = 0
+    arrays = _score_arrays(p, "causal", 0)
+    dev = {k: v.cuda() for k, v in t.items()}
+    plan, sc = sp.Plan.from_problem(p), _score(arrays, cap, None)
+    o, lse = sp.spattn_fwd_scored(dev["q"], dev["k"], dev["v"], plan, sc)
+    grads = sp.spattn_bwd_scored(dev["q"], dev["k"], dev["v"], o, lse, dev["do"], plan, sc)
+    assert all(bool(torch.isfinite(x).all()) for x in (o, lse) + tuple(grads))
+    f64 = lambda x: x[0, 0].cpu().double().numpy()  # noqa: E731
+    mask = R.score_mask(np.ones((90, 90), bool), arrays["k_pos"], arrays["q_last"])
+    z, _ = R.scores(f64(t["q"]), f64(t["k"]), p.scale, float(np.float32(cap)) or cap)
+    want, wl, tol, lt = R.forward(f64(t["q"]), f64(t["k"]), f64(t["v"]), mask, z)
+    _close(f64(o), want, tol, "o")
+    _close(f64(lse), wl, lt, "lse")
+
+
 def test_device_replan_keeps_the_score():
     p = W.make_problem("tiny_vsa")
     t = W.make_tensors(p)
@@ -300,6 +320,15 @@ def test_gradient_against_differences():
         tol = R.backward(x["q"], x["k"], x["v"], x["do"], mask, z, f, p.scale)["d" + n][1]
         got = float((out["d" + n][0, 0].cpu().double().numpy() * d).sum())
         assert abs(got - num) <= float((tol * np.abs(d)).sum()) + 1e-6 * abs(num), n
+
+
+def test_another_current_device_is_refused(monkeypatch):
+    p = W.make_problem("tiny")
+    t = {k: v.cuda() for k, v in W.make_tensors(p).items()}
+    plan = sp.Plan.from_problem(p)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        sp.spattn_fwd_scored(t["q"], t["k"], t["v"], plan, sp.Score(softcap=1.0))
 
 
 def test_wrong_devices_and_shapes_are_refused():
