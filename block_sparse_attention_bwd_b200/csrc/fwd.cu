@@ -59,7 +59,7 @@ struct FwdCfg {
   // left step st - 2, so kKStages + 2 lines are never overwritten while read.
   static constexpr int kColRing = 8;
   static constexpr int kColBytes = 3 * 64 * 4;
-  static constexpr int kScoreBytes = kColRing * (kColBytes + 16) + 4 * 128 * 4 + 4 * 8;  // + the row pairs' exchange and barriers
+  static constexpr int kScoreBytes = kColRing * (kColBytes + 16) + 4 * 128 * 4 + 4 * 8 + 8;  // + the row pairs' exchange and barriers
   static_assert(kColRing >= kKStages + 2, "column lines outlive their readers");
   static_assert(!F8 || D == 128, "the E4M3 forward has D = 128 (one 128-byte row per chunk)");
 };
@@ -70,9 +70,16 @@ constexpr float kRescaleThreshold = 8.0f;
 
 // 6 warps: 0 = TMA producer, 1 = TMEM owner and MMA issuer, 2..5 = row
 // threads (warp w reaches TMEM lanes 32*(w%4) .. 32*(w%4)+31).
-// The fixed scored form has two row threads per row (score.cuh): warps 2..9.
+// The scored forms have two row threads per row (score.cuh): warps 2..9.  Their
+// weights are taken relative to a fixed reference: 2^0 in a first pass over the
+// list, which suits all but extreme scores.  Where some row's sum of weights then
+// leaves [2^-80, 2^80] (an LSE beyond +-55, as from a bias that every key of a row
+// pays in full; fp32 keeps 2^46 on either side for the values and the smaller
+// keys), the CTA runs over its list twice more: once for the rows' maxima alone and
+// again with those as references.  Other rows pay for no running maximum, no
+// rescaling of O and no exchange between a row's threads.
 template <int SC>
-constexpr int kFwdThreads = SC == kScoreFixed ? 320 : 192;
+constexpr int kFwdThreads = SC == kScoreNone ? 192 : 320;
 
 // ROUTE: the form that reads each item's route flag (the 64-row route of
 // Work::halves); without it every item runs as 128 rows over its whole list.
@@ -112,10 +119,17 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
   auto col_doc = [&](int st) { return col_pos(st) + 64; };
   auto col_posf = [&](int st) { return reinterpret_cast<float*>(col_pos(st) + 128); };
   int4* col_rng = reinterpret_cast<int4*>(score_smem + R * C::kColBytes);
-  float* xrow = reinterpret_cast<float*>(col_rng + R);            // [4][128] sums of the row pairs (fixed form)
+  float* xrow = reinterpret_cast<float*>(col_rng + R);            // [4][128] sums (or maxima) of the row pairs
   uint64_t* pair_bar = reinterpret_cast<uint64_t*>(xrow + 4 * 128);  // [4]
-  const bool use_cols = SC != kScoreNone && SC != kScoreFixed ? (sc.q_last || sc.q_doc || sc.slopes)
-                                                              : SC == kScoreFixed && (sc.q_last || sc.q_doc);
+  volatile int* redo = reinterpret_cast<volatile int*>(pair_bar + 4);  // a row asks for its maximum; the CTA's answer
+  const bool use_cols = SC != kScoreNone && (sc.q_last || sc.q_doc || sc.slopes);
+  // Between the scored forms' passes, by every thread: whether to go on.
+  auto decide = [&]() -> bool {
+    __syncthreads();
+    if (threadIdx.x == 0) redo[1] = redo[0] && !*abort_flag;
+    __syncthreads();
+    return redo[1] != 0;
+  };
 
   if constexpr (SC != kScoreNone) {
     // blocks behind the work items: rows that none of them writes (a launch less)
@@ -135,6 +149,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
+    if constexpr (SC != kScoreNone) redo[0] = 0;
     mbar_init(q_full, 1);
     for (int s = 0; s < KS; ++s) {
       mbar_init(&k_full[s], 1);
@@ -181,10 +196,8 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
     auto page_of = [&](int st) {
       return (st < n_steps && lane < min(NP, n_cols - st * NP)) ? __ldg(col_pages + wk.e0 + st * NP + lane) : 0;
     };
-    int pid_next = page_of(0);
     // scored forms: lane l also holds columns l and l + 32 of a step, loaded a step
     // ahead from page ids that are fetched two ahead
-    int pid_next2 = 0;
     int cpos[2] = {0, 0}, cdoc[2] = {-1, -1};
     bool clive[2] = {false, false};
     auto load_cols = [&](int st, int pid_lane) {
@@ -198,43 +211,48 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
         cdoc[h] = sc.k_doc ? __ldg(sc.k_doc + off) : -1;
       }
     };
-    if (use_cols) {
-      pid_next2 = page_of(1);
-      load_cols(0, pid_next);
-    }
-    int k_issued = 0, v_issued = 0;
-    for (int st = 0; st < n_steps; ++st) {
-      const int n = min(NP, n_cols - st * NP);
-      const int pid = pid_next;
-      const int ks = st % KS, vs = st % VS;
+    int k_issued = 0, v_issued = 0;  // steps over all passes
+    for (int pass = 0; pass < (SC == kScoreNone ? 1 : 3); ++pass) {
+      int pid_next = page_of(0), pid_next2 = 0;
       if (use_cols) {
-        pid_next = pid_next2;
-        pid_next2 = page_of(st + 2);
-      } else {
-        pid_next = page_of(st + 1);
+        pid_next2 = page_of(1);
+        load_cols(0, pid_next);
       }
-      if (st >= KS && !__all_sync(0xffffffffu, mbar_wait(&k_empty[ks], ((st / KS) - 1) & 1, ab))) break;
-      if (use_cols) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          col_pos(st)[lane + 32 * h] = cpos[h];
-          col_doc(st)[lane + 32 * h] = cdoc[h];
-          col_posf(st)[lane + 32 * h] = static_cast<float>(cpos[h]);
+      for (int st = 0; st < n_steps; ++st) {
+        const int g = pass * n_steps + st;  // step over all passes
+        const int n = min(NP, n_cols - st * NP);
+        const int pid = pid_next;
+        const int ks = g % KS, vs = g % VS;
+        if (use_cols) {
+          pid_next = pid_next2;
+          pid_next2 = page_of(st + 2);
+        } else {
+          pid_next = page_of(st + 1);
         }
-        const int4 rg = range_join(column_range(clive[0], cpos[0], cdoc[0]), column_range(clive[1], cpos[1], cdoc[1]));
-        if (lane == 0) col_rng[st % R] = rg;
-        load_cols(st + 1, pid_next);
+        if (g >= KS && !__all_sync(0xffffffffu, mbar_wait(&k_empty[ks], ((g / KS) - 1) & 1, ab))) break;
+        if (use_cols) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            col_pos(g)[lane + 32 * h] = cpos[h];
+            col_doc(g)[lane + 32 * h] = cdoc[h];
+            col_posf(g)[lane + 32 * h] = static_cast<float>(cpos[h]);
+          }
+          const int4 rg = range_join(column_range(clive[0], cpos[0], cdoc[0]), column_range(clive[1], cpos[1], cdoc[1]));
+          if (lane == 0) col_rng[g % R] = rg;
+          load_cols(st + 1, pid_next);
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], n * C::kQKNch * 2048);
         __syncwarp();
+        load_page_runs<C::kQKNch>(sK + ks * C::kKStage, kFwdStageChunk, tm_k, pid, n, kv_bh, &k_full[ks]);
+        k_issued = g + 1;
+        if (g >= VS && !__all_sync(0xffffffffu, mbar_wait(&v_empty[vs], ((g / VS) - 1) & 1, ab))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], n * C::kNch * 2048);
+        __syncwarp();
+        load_page_runs<C::kNch>(sV + vs * C::kVStage, kFwdStageChunk, tm_v, pid, n, kv_bh, &v_full[vs]);
+        v_issued = g + 1;
       }
-      if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], n * C::kQKNch * 2048);
-      __syncwarp();
-      load_page_runs<C::kQKNch>(sK + ks * C::kKStage, kFwdStageChunk, tm_k, pid, n, kv_bh, &k_full[ks]);
-      k_issued = st + 1;
-      if (st >= VS && !__all_sync(0xffffffffu, mbar_wait(&v_empty[vs], ((st / VS) - 1) & 1, ab))) break;
-      if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], n * C::kNch * 2048);
-      __syncwarp();
-      load_page_runs<C::kNch>(sV + vs * C::kVStage, kFwdStageChunk, tm_v, pid, n, kv_bh, &v_full[vs]);
-      v_issued = st + 1;
+      if (SC != kScoreNone && pass == 0 && !decide()) break;
     }
     // no copy may still be landing in shared memory when the CTA exits
     if (lane == 0) {
@@ -251,14 +269,17 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
     const uint32_t idesc_pv64 = idesc_bf16(64, D, false, true);
     bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, ab));
     tc_fence_after();
+    int pass = 0;
     auto issue_pv = [&](int st) -> bool {
-      const int b = st & 1, vs = st % VS;
-      const bool w = mbar_wait(&p_full[b], (st >> 1) & 1, ab) && mbar_wait(&v_full[vs], (st / VS) & 1, ab);
+      const int g = pass * n_steps + st, b = g & 1, vs = g % VS;  // g: step over all passes
+      const bool w = mbar_wait(&p_full[b], (g >> 1) & 1, ab) && mbar_wait(&v_full[vs], (g / VS) & 1, ab);
       if (!__all_sync(0xffffffffu, w)) return false;
       tc_fence_after();
       const int n = min(NP, n_cols - st * NP);
       const uint64_t dv = sdesc_add(dv0, vs * C::kVStage);
-      if (halves) {
+      if (SC != kScoreNone && pass == 1) {
+        // the pass for the maxima has no weights
+      } else if (halves) {
         // O_h += P_h V_h: half h's P (lanes from 16h) against the step's pages 2h, 2h+1
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -271,76 +292,83 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
 #pragma unroll
         for (int j = 0; j < NP; ++j)
           if (j < n)
-            umma_ts_w(tO, tmem + 64 * b + 8 * j + (SC == kScoreFixed && j >= 2 ? 16 : 0), sdesc_add(dv, j * 2048), idesc_pv,
+            umma_ts_w(tO, tmem + 64 * b + 8 * j + (SC != kScoreNone && j >= 2 ? 16 : 0), sdesc_add(dv, j * 2048), idesc_pv,
                       (st > 0 || j > 0) ? 1u : 0u);
       }
       umma_commit_w(&v_empty[vs]);
       umma_commit_w(o_done);
       return true;
     };
-    for (int st = 0; ok && st < n_steps; ++st) {
-      const int ks = st % KS, b = st & 1;
-      // buffer b still holds P(st-2), the TMEM A operand of PV(st-2); let
-      // that MMA finish before S(st) overwrites it (waited every step, in
-      // order, so the parity is unambiguous)
-      const bool w = mbar_wait(&k_full[ks], (st / KS) & 1, ab) && (st < 2 || mbar_wait(o_done, (st - 2) & 1, ab));
-      if (!__all_sync(0xffffffffu, w)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const int n = min(NP, n_cols - st * NP);
-      const uint64_t dk = sdesc_add(dk0, ks * C::kKStage);
-      if (halves) {
-        // S_h = Q_h K_h^T (M = 64, N = 32) for h = 0, 1: query rows 64h.. (8 KB
-        // into each chunk) against stage rows 32h.. (4 KB), written to the
-        // same 32 columns of buffer b at TMEM lanes offset by 16 h, so that
-        // row r of half h sits at lane 16 h + r % 16 + 32 (r / 16)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t d = tmem + 64 * b + (static_cast<uint32_t>(16 * h) << 16);
-          if constexpr (F8) {
-#pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              umma_ss_e4m3_w(d, sdesc_add(dq0, (kk >> 2) * kChunkBytes + (kk & 3) * 32 + h * 8192),
-                             sdesc_add(dk, (kk >> 2) * kFwdStageChunk + (kk & 3) * 32 + h * 4096), idesc_e4m3(64, 32),
-                             kk > 0 ? 1u : 0u);
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss_w(d, sdesc_add(dq0, (kk >> 2) * kChunkBytes + (kk & 3) * 32 + h * 8192),
-                        sdesc_add(dk, (kk >> 2) * kFwdStageChunk + (kk & 3) * 32 + h * 4096),
-                        idesc_bf16(64, 32, false, false), kk > 0 ? 1u : 0u);
-          }
+    for (; pass < (SC == kScoreNone ? 1 : 3); ++pass) {
+      for (int st = 0; ok && st < n_steps; ++st) {
+        const int g = pass * n_steps + st, ks = g % KS, b = g & 1;
+        // buffer b still holds P(st-2), the TMEM A operand of PV(st-2); let
+        // that MMA finish before S(st) overwrites it (waited every step, in
+        // order, so the parity is unambiguous)
+        // (a further pass starts with no product in flight: the last one's phase)
+        const int free_at = pass > 0 && st == 0 ? g - 1 : g - 2;
+        const bool w = mbar_wait(&k_full[ks], (g / KS) & 1, ab) && (free_at < 0 || mbar_wait(o_done, free_at & 1, ab));
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
         }
-      } else if constexpr (F8) {
-        // 32 E4M3 elements (32 bytes) of K per MMA
-        const uint32_t idesc_s = idesc_e4m3(128, 16 * n);
+        tc_fence_after();
+        const int n = min(NP, n_cols - st * NP);
+        const uint64_t dk = sdesc_add(dk0, ks * C::kKStage);
+        if (halves) {
+          // S_h = Q_h K_h^T (M = 64, N = 32) for h = 0, 1: query rows 64h.. (8 KB
+          // into each chunk) against stage rows 32h.. (4 KB), written to the
+          // same 32 columns of buffer b at TMEM lanes offset by 16 h, so that
+          // row r of half h sits at lane 16 h + r % 16 + 32 (r / 16)
 #pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk)
-          umma_ss_e4m3_w(tmem + 64 * b, sdesc_add(dq0, (kk >> 2) * kChunkBytes + (kk & 3) * 32),
-                         sdesc_add(dk, (kk >> 2) * kFwdStageChunk + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
-      } else {
-        const uint32_t idesc_s = idesc_bf16(128, 16 * n, false, false);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t d = tmem + 64 * b + (static_cast<uint32_t>(16 * h) << 16);
+            if constexpr (F8) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss_w(tmem + 64 * b, sdesc_add(dq0, (kk >> 2) * kChunkBytes + (kk & 3) * 32),
-                    sdesc_add(dk, (kk >> 2) * kFwdStageChunk + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < D / 32; ++kk)
+                umma_ss_e4m3_w(d, sdesc_add(dq0, (kk >> 2) * kChunkBytes + (kk & 3) * 32 + h * 8192),
+                               sdesc_add(dk, (kk >> 2) * kFwdStageChunk + (kk & 3) * 32 + h * 4096), idesc_e4m3(64, 32),
+                               kk > 0 ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma_ss_w(d, sdesc_add(dq0, (kk >> 2) * kChunkBytes + (kk & 3) * 32 + h * 8192),
+                          sdesc_add(dk, (kk >> 2) * kFwdStageChunk + (kk & 3) * 32 + h * 4096),
+                          idesc_bf16(64, 32, false, false), kk > 0 ? 1u : 0u);
+            }
+          }
+        } else if constexpr (F8) {
+          // 32 E4M3 elements (32 bytes) of K per MMA
+          const uint32_t idesc_s = idesc_e4m3(128, 16 * n);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            umma_ss_e4m3_w(tmem + 64 * b, sdesc_add(dq0, (kk >> 2) * kChunkBytes + (kk & 3) * 32),
+                           sdesc_add(dk, (kk >> 2) * kFwdStageChunk + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
+        } else {
+          const uint32_t idesc_s = idesc_bf16(128, 16 * n, false, false);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss_w(tmem + 64 * b, sdesc_add(dq0, (kk >> 2) * kChunkBytes + (kk & 3) * 32),
+                      sdesc_add(dk, (kk >> 2) * kFwdStageChunk + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
+        }
+        umma_commit_w(&s_full[b]);
+        if (SC != kScoreNone && lane == 0) mbar_arrive(&s_full[b]);
+        umma_commit_w(&k_empty[ks]);
+        if (st >= 1 && !issue_pv(st - 1)) ok = false;
       }
-      umma_commit_w(&s_full[b]);
-      if (SC != kScoreNone && lane == 0) mbar_arrive(&s_full[b]);
-      umma_commit_w(&k_empty[ks]);
-      if (st >= 1 && !issue_pv(st - 1)) ok = false;
+      ok = ok && n_steps > 0 && issue_pv(n_steps - 1);
+      if (ok) umma_commit_w(o_last);
+      if (SC != kScoreNone && pass == 0 && !decide()) break;
     }
-    if (ok && n_steps > 0 && issue_pv(n_steps - 1)) umma_commit_w(o_last);
     umma_commit_w(drain);
     mbar_wait_drain(drain, 0);
-  } else if constexpr (SC == kScoreFixed) {
-    // ---------------- softmax of the fixed form + epilogue (two threads per row, 32 columns each) ----------------
+  } else if constexpr (SC != kScoreNone) {
+    // ---------------- scored softmax + epilogue (two threads per row, 32 columns each) ----------------
+    constexpr bool kCap = SC == kScoreCap;
     const int grp = (warp - 2) >> 2;
     const int q4 = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    // tile row of this thread's TMEM lane, as in the other forms below; in the
+    // tile row of this thread's TMEM lane, as in the plain form below; in the
     // 64-row route group 0 has the row's 32 columns and group 1 none
     const int hh = (lane >> 4) & 1;
     const int row = halves ? 64 * hh + (lane & 15) + 16 * q4 : q4 * 32 + lane;
@@ -348,8 +376,10 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
     const uint32_t code = wk.row_code(row);
     const int seg = code < 8 ? static_cast<int>(code) : -1;
     float* xr = xrow + row;
-    // this row's side of the masks
+    // this row's side of the masks and the bias
     int row_last = 0, row_doc = -1;
+    float row_pos = 0.f, slope = 0.f;
+    const float mul = kCap ? 1.0f : sl2;  // after the cap the scores are in log2 units
     {
       const int bi = wk.bh / heads;
       const int64_t slot = row < 16 * wk.n_own ? pref_slot(wk.own_page(row >> 4), row & 15) : q_slots;
@@ -357,59 +387,84 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
         const int64_t off = bi * sc.q_batch + slot;
         if (sc.q_last) row_last = __ldg(sc.q_last + off);
         if (sc.q_doc) row_doc = __ldg(sc.q_doc + off);
+        if (sc.slopes) row_pos = static_cast<float>(__ldg(sc.q_pos + off));
       }
+      if (sc.slopes) slope = __ldg(sc.slopes + wk.bh % heads) * kLog2e / mul;
     }
     const int4 rows = row_range(seg >= 0, row_last, row_doc), mine = make_int4(row_last, row_last, row_doc, row_doc);
-    // this row's masks of its two pages, fetched a step ahead
     const uint16_t* mask = reinterpret_cast<const uint16_t*>(col_masks + 2 * static_cast<int64_t>(wk.e0)) + (seg < 0 ? 0 : seg);
-    uint32_t m_lo = 0u, m_hi = 0u;
-    auto fetch_masks = [&](int st) {
-      const int e = st * NP + pg0;
-      m_lo = seg >= 0 && e < n_cols ? __ldg(mask + 8 * e) : 0u;
-      m_hi = seg >= 0 && e + 1 < n_cols ? __ldg(mask + 8 * (e + 1)) : 0u;
-    };
-    if (n_steps > 0) fetch_masks(0);
-    SoftRow r;
     bool ok = true;
-    for (int st = 0; st < n_steps; ++st) {
-      const int b = st & 1;
-      const bool active = halves ? grp == 0 : 2 * grp < n_cols - st * NP;
-      uint32_t bits = m_lo | (m_hi << 16);
-      if (st + 1 < n_steps) fetch_masks(st + 1);
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (st >> 1) & 1, ab));
-      if (!ok) break;
-      if (use_cols && active) {
-        const int4 rg = col_rng[st % R];
-        if (query_none(sc, rg, rows))
-          bits = 0u;
-        else if (__builtin_expect(!query_all(sc, rg, rows), 0) &&
-                 __any_sync(0xffffffffu, mixed_row(bits, query_none(sc, rg, mine), query_all(sc, rg, mine))))
-          bits &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + 16 * pg0, col_doc(st) + 16 * pg0, row_last, row_doc);
-      }
-      tc_fence_after();
-      uint32_t x[32];
-      const uint32_t s_addr = tmem + 64 * b + lane_off + 32 * grp;
-      if (active) {
-        tmem_ld32(s_addr, x);
-        tmem_wait_ld();
-        cap_scores<false>(x, x, sc.c);
-        if (__builtin_expect(bits != 0xFFFFFFFFu, 0)) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((bits >> i) & 1u)) x[i] = 0xFF800000u;  // -inf
-        }
-        soft_weights(x, r, s_addr);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&p_full[b]);
-    }
-    if (ok && n_steps > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(o_last, 0, ab));
-      tc_fence_after();
-    }
+    float ref = 0.f;  // reference of the weights, log2 units
     float l = 0.f, l_true = 0.f;
-    ok = ok && soft_total(r, xr, grp, &pair_bar[q4], ab, l, l_true);
+    for (int pass = 0; pass < 3; ++pass) {
+      SoftRow r;
+      bool seen = false;          // some key is allowed
+      float top = -INFINITY;      // pass 1: this thread's maximum
+      // this row's masks of its two pages, fetched a step ahead
+      uint32_t m_lo = 0u, m_hi = 0u;
+      auto fetch_masks = [&](int st) {
+        const int e = st * NP + pg0;
+        m_lo = seg >= 0 && e < n_cols ? __ldg(mask + 8 * e) : 0u;
+        m_hi = seg >= 0 && e + 1 < n_cols ? __ldg(mask + 8 * (e + 1)) : 0u;
+      };
+      if (n_steps > 0) fetch_masks(0);
+      for (int st = 0; ok && st < n_steps; ++st) {
+        const int g = pass * n_steps + st, b = g & 1;
+        const bool active = halves ? grp == 0 : 2 * grp < n_cols - st * NP;
+        uint32_t bits = m_lo | (m_hi << 16);
+        if (st + 1 < n_steps) fetch_masks(st + 1);
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (g >> 1) & 1, ab));
+        if (!ok) break;
+        if (active && (sc.q_last || sc.q_doc)) {
+          const int4 rg = col_rng[g % R];
+          if (query_none(sc, rg, rows))
+            bits = 0u;
+          else if (__builtin_expect(!query_all(sc, rg, rows), 0) &&
+                   __any_sync(0xffffffffu, mixed_row(bits, query_none(sc, rg, mine), query_all(sc, rg, mine))))
+            bits &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(g) + 16 * pg0, col_doc(g) + 16 * pg0, row_last, row_doc);
+        }
+        tc_fence_after();
+        const uint32_t s_addr = tmem + 64 * b + lane_off + 32 * grp;
+        if (active) {
+          seen |= bits != 0u;
+          uint32_t x[32];
+          tmem_ld32(s_addr, x);
+          tmem_wait_ld();
+          if constexpr (kCap) cap_scores<false>(x, x, sc.c);
+          if (sc.slopes) bias_scores(x, col_posf(g) + 16 * pg0, row_pos, slope);
+          if (__builtin_expect(bits != 0xFFFFFFFFu, 0)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((bits >> i) & 1u)) x[i] = 0xFF800000u;  // -inf
+          }
+          if (__builtin_expect(pass == 1, 0))
+            top = fmaxf(top, local_max(x) * mul);
+          else
+            soft_weights(x, mul, ref, r, s_addr);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[b]);
+      }
+      if (n_steps > 0) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(o_last, pass & 1, ab));
+        tc_fence_after();
+      }
+      if (pass == 1) {
+        xr[128 * grp] = top;
+        ok = ok && pair_sync(&pair_bar[q4], pass, ab);
+        top = fmaxf(xr[0], xr[128]);
+        ref = top > -INFINITY && top < INFINITY ? top : 0.f;
+        ok = ok && pair_sync(&pair_bar[q4], pass + 1, ab);  // before the sums are written there
+        continue;
+      }
+      ok = ok && soft_total(r, xr, grp, &pair_bar[q4], pass + (pass > 0), ab, l, l_true);
+      if (pass == 0) {
+        constexpr float kLow = 8.271806125530277e-25f, kHigh = 1.2089258196146292e24f;  // 2^-80, 2^80
+        if (ok && seen && !(l_true >= kLow && l_true <= kHigh)) redo[0] = 1;
+        if (!decide()) break;
+      }
+    }
     if (ok) {
       const bool owned = code != 15u && row < 16 * wk.n_own;
       const int64_t slot = owned ? pref_slot(wk.own_page(row >> 4), row & 15) : 0;
@@ -427,7 +482,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
         if (write) store_row32(dst + pc * 32, v, inv, empty || n_steps == 0);
       }
       if (write && grp == 0)
-        out_lse[static_cast<int64_t>(wk.bh) * q_slots + slot] = empty ? -INFINITY : lg2(l_true) * kLn2;
+        out_lse[static_cast<int64_t>(wk.bh) * q_slots + slot] = empty ? -INFINITY : (ref + lg2(l_true)) * kLn2;
     }
   } else {
     // ---------------- softmax + epilogue (one row per thread) ----------------
@@ -440,28 +495,11 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
     const uint32_t code = wk.row_code(row);
     const int seg = code < 8 ? static_cast<int>(code) : -1;
     if constexpr (F8) sl2 *= __ldg(q_descale + wk.bh) * __ldg(k_descale + kv_bh);  // scores of the dequantised Q, K
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     StepMasks<NP> raw;
     if (n_steps > 0) raw.fetch(col_masks, wk.e0, min(NP, n_cols), seg);
-    // scored forms: this row's side of the masks and the bias
-    int row_last = 0, row_doc = -1;
-    float row_pos = 0.f, slope = 0.f;
-    constexpr bool kCap = SC == kScoreCap;
-    const float mul = kCap ? 1.0f : sl2;  // after the cap the scores are in log2 units
-    if constexpr (SC != kScoreNone) {
-      const int bi = wk.bh / heads;
-      const int64_t slot = row < 16 * wk.n_own ? pref_slot(wk.own_page(row >> 4), row & 15) : q_slots;
-      if (slot < q_slots) {
-        const int64_t off = bi * sc.q_batch + slot;
-        if (sc.q_last) row_last = __ldg(sc.q_last + off);
-        if (sc.q_doc) row_doc = __ldg(sc.q_doc + off);
-        if (sc.slopes) row_pos = static_cast<float>(__ldg(sc.q_pos + off));
-      }
-      if (sc.slopes) slope = __ldg(sc.slopes + wk.bh % heads) * kLog2e / mul;
-    }
-    const int4 rows = SC != kScoreNone ? row_range(seg >= 0, row_last, row_doc) : make_int4(0, 0, 0, 0);
-    const uint64_t mul2 = f2_pack(mul, mul);
     for (int st = 0; st < n_steps; ++st) {
       const int b = st & 1;
       // the 64-row route: 32 columns (this half's two pages) in the low half of S
@@ -473,38 +511,12 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
       if (st + 1 < n_steps) raw.fetch(col_masks, wk.e0 + (st + 1) * NP, min(NP, n_cols - (st + 1) * NP), seg);
       ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (st >> 1) & 1, ab));
       if (!ok) break;
-      if (SC != kScoreNone && (sc.q_last || sc.q_doc)) {
-        const int4 rg = col_rng[st % R];
-        if (query_none(sc, rg, rows)) {
-          mw[0] = mw[1] = 0u;
-        } else if (__builtin_expect(!query_all(sc, rg, rows), 0)) {
-          const int4 mine = make_int4(row_last, row_last, row_doc, row_doc);
-          const int c0 = halves ? 32 * hh : 0;
-          uint32_t some = mw[0] | mw[1];
-          const bool mixed = mixed_row(some, query_none(sc, rg, mine), query_all(sc, rg, mine));
-          if (some == 0u) mw[0] = mw[1] = 0u;
-          if (__any_sync(0xffffffffu, mixed)) {
-          mw[0] &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + c0, col_doc(st) + c0, row_last, row_doc);
-          if (!halves)
-            mw[1] &= column_bits<true, 32>(sc.q_last, sc.q_doc, col_pos(st) + 32, col_doc(st) + 32, row_last, row_doc);
-          }
-        }
-      }
       tc_fence_after();
       uint32_t sr[2][32];
 #pragma unroll
       for (int pc = 0; pc < 2; ++pc)
         if (pc * 32 < N) tmem_ld32(tmem + 64 * b + lane_off + pc * 32, sr[pc]);
       tmem_wait_ld();
-      if constexpr (SC != kScoreNone) {
-#pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {
-          if (pc * 32 < N) {
-            if constexpr (kCap) cap_scores<false>(sr[pc], sr[pc], sc.c);
-            if (sc.slopes) bias_scores(sr[pc], col_posf(st) + (halves ? 32 * hh : 32 * pc), row_pos, slope);
-          }
-        }
-      }
       // masked row max over four independent chains
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -524,7 +536,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
           }
         }
       }
-      const float mx2 = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * mul;  // log2 units (scale > 0)
+      const float mx2 = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * sl2;  // log2 units (scale > 0)
       const bool resc = mx2 > m_used + kRescaleThreshold;
       const float m_new = resc ? mx2 : m_used;
       const float alpha = resc ? ex2(m_used - m_new) : 1.0f;
@@ -544,7 +556,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[pc][2 * i]), __uint_as_float(sr[pc][2 * i + 1])), mul2, nmu2),
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[pc][2 * i]), __uint_as_float(sr[pc][2 * i + 1])), sl2x2, nmu2),
                         x0, x1);
               const float p0 = ex2(x0), p1 = ex2(x1);
               ls2[i & 1] = f2_add(ls2[i & 1], f2_pack(p0, p1));
@@ -667,12 +679,10 @@ cudaError_t launch_fwd_sc(const TmaPages& tq, const TmaPages& tk, const TmaPages
 template <int D>
 cudaError_t launch_fwd_t(const TmaPages& tq, const TmaPages& tk, const TmaPages& tv, const TileArgs& a,
                          const ScoreArgs* sc, const FillArgs& fill, __nv_bfloat16* o, float* lse, cudaStream_t st) {
-  if (!sc) return launch_fwd_sc<D, false, kScoreNone>(tq, tk, tv, a, ScoreArgs(), FillArgs(), o, lse, nullptr, nullptr, st);
-  if (!(sc->cap > 0.f)) return launch_fwd_sc<D, false, kScoreMask>(tq, tk, tv, a, *sc, fill, o, lse, nullptr, nullptr, st);
-  // a bounded cap without a bias needs no running maximum (kCapFixedMax)
-  if (!sc->slopes && sc->c.cap2 <= kCapFixedMax)
-    return launch_fwd_sc<D, false, kScoreFixed>(tq, tk, tv, a, *sc, fill, o, lse, nullptr, nullptr, st);
-  return launch_fwd_sc<D, false, kScoreCap>(tq, tk, tv, a, *sc, fill, o, lse, nullptr, nullptr, st);
+  if (!sc)
+    return launch_fwd_sc<D, false, kScoreNone>(tq, tk, tv, a, ScoreArgs(), FillArgs(), o, lse, nullptr, nullptr, st);
+  return sc->cap > 0.f ? launch_fwd_sc<D, false, kScoreCap>(tq, tk, tv, a, *sc, fill, o, lse, nullptr, nullptr, st)
+                       : launch_fwd_sc<D, false, kScoreMask>(tq, tk, tv, a, *sc, fill, o, lse, nullptr, nullptr, st);
 }
 
 }  // namespace

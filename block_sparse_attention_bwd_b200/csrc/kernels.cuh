@@ -65,7 +65,7 @@ struct CapArgs {
 };
 CapArgs cap_args(float cap, float scale);
 // Caps up to this (in log2 units) keep 2^z and its sums inside fp32 without a
-// running maximum: z within +-80 leaves 2^47 for values and sums.
+// running maximum: z within +-80 leaves 2^47 for values and sums (paged kernel).
 constexpr float kCapFixedMax = 80.0f;
 
 // Score modification (spattn_score): device arrays, null where unused.

@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
             for (int i = 0; i < 32; ++i)
               if (i >= vis) x[i] = 0xFF800000u;  // -inf
           }
-          soft_weights(x, r, s_addr);
+          soft_weights(x, 1.0f, 0.f, r, s_addr);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
       }
       ok = ok && __all_sync(0xffffffffu, mbar_wait(o_last, 0, ab));
       tc_fence_after();
-      ok = ok && soft_total(r, xrow + row, grp, &pair_bar[q4], ab, l, l_true);
+      ok = ok && soft_total(r, xrow + row, grp, &pair_bar[q4], 0, ab, l, l_true);
     } else {
       const float mul = kCap ? 1.0f : sl2;  // after the cap the scores are in log2 units
       const uint64_t mul2 = f2_pack(mul, mul);

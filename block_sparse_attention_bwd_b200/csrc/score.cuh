@@ -23,7 +23,7 @@ namespace dev {
 //   kScoreNone   the plain kernel
 //   kScoreMask   masks and bias
 //   kScoreCap    the same with a cap
-//   kScoreFixed  (forward) a cap small enough for a fixed softmax reference, no bias
+//   kScoreFixed  (paged) a cap small enough for a fixed softmax reference
 enum : int { kScoreNone = 0, kScoreMask = 1, kScoreCap = 2, kScoreFixed = 3 };
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -238,33 +238,37 @@ __device__ __forceinline__ uint32_t column_bits(bool use_pos, bool use_doc, cons
 }
 
 // ----------------------------------------------------------------------------
-// Softmax of one step in the scored forward forms
+// Softmax of one step with two threads per row
 // ----------------------------------------------------------------------------
-// The fixed form has two threads per row: group g (0, 1) has 32 of the step's 64
-// columns, so that four row warps per scheduler (two CTAs) cover each other's
-// latency and a thread's code is half as long.  They meet once, at the end.
-// (With a running maximum they would exchange their halves' maxima every step;
-// that exchange cost more than the second thread gave, so those forms keep one.)
+// Group g (0, 1) has 32 of the step's 64 columns, so that four row warps per
+// scheduler (two CTAs) cover each other's latency and a thread's code is half as
+// long.  That needs a reference of the weights that is known beforehand: with a
+// running maximum the two threads would exchange their halves' maxima every step,
+// which cost more than the second thread gave (943 us -> 1421 on 12289 causal
+// tokens x 16 heads).  They meet once, at the end.
 struct SoftRow {
   float l = 0.f;   // sum of this thread's weights
   float lr = 0.f;  // the same of the weights rounded to bf16
 };
 
-// Meeting of the two warps of a row pair (a barrier of 64 arrivals).  A bounded
-// wait, so that a warp that gave up cannot strand its partner; false when the CTA
-// is aborting.
-__device__ __forceinline__ bool pair_sync(uint64_t* bar, const Abort& ab) {
+// Meeting of the two warps of a row pair (a barrier of 64 arrivals), the n-th.  A
+// bounded wait, so that a warp that gave up cannot strand its partner; false
+// when the CTA is aborting.
+__device__ __forceinline__ bool pair_sync(uint64_t* bar, int n, const Abort& ab) {
   mbar_arrive(bar);
-  return __all_sync(0xffffffffu, mbar_wait(bar, 0, ab));
+  return __all_sync(0xffffffffu, mbar_wait(bar, n & 1, ab));
 }
 
-// Weights 2^s of this thread's 32 columns to P (bf16, TMEM) and their sums.
-__device__ __forceinline__ void soft_weights(const uint32_t (&s)[32], SoftRow& r, uint32_t p_addr) {
+// Weights 2^(s mul - ref) of this thread's 32 columns to P (bf16, TMEM) and their sums.
+__device__ __forceinline__ void soft_weights(const uint32_t (&s)[32], float mul, float ref, SoftRow& r, uint32_t p_addr) {
+  const uint64_t m2 = f2_pack(mul, mul), n2 = f2_pack(-ref, -ref);
   uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)}, sumr[2] = {sum[0], sum[1]};
   uint32_t pk[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float p0 = ex2(__uint_as_float(s[2 * i])), p1 = ex2(__uint_as_float(s[2 * i + 1]));
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), m2, n2), x0, x1);
+    const float p0 = ex2(x0), p1 = ex2(x1);
     sum[i & 1] = f2_add(sum[i & 1], f2_pack(p0, p1));
     pk[i] = pack_bf16(p0, p1);
     sumr[i & 1] = f2_add(sumr[i & 1], f2_pack(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xFFFF0000u)));
@@ -280,17 +284,28 @@ __device__ __forceinline__ void soft_weights(const uint32_t (&s)[32], SoftRow& r
 }
 
 // Sums of both threads of the row (xsum: this row's entries of [4][128] floats).
-// `l`, the divisor of O, sums the rounded weights: no weight is 1 in this form, so
-// a row with few keys would keep its weights' rounding otherwise.  l_true is
+// `l`, the divisor of O, sums the rounded weights: no weight need be 1 here, so a
+// row with few keys would keep its weights' rounding otherwise.  l_true is
 // the sum in LSE.
-__device__ __forceinline__ bool soft_total(const SoftRow& r, float* xsum, int grp, uint64_t* bar, const Abort& ab,
-                                           float& l, float& l_true) {
+__device__ __forceinline__ bool soft_total(const SoftRow& r, float* xsum, int grp, uint64_t* bar, int n,
+                                           const Abort& ab, float& l, float& l_true) {
   xsum[128 * grp] = r.l;
   xsum[256 + 128 * grp] = r.lr;
-  if (!pair_sync(bar, ab)) return false;
+  if (!pair_sync(bar, n, ab)) return false;
   l_true = xsum[0] + xsum[128];
   l = xsum[256] + xsum[256 + 128];
   return true;
+}
+
+// The row's maximum over both threads (-inf: no key).
+__device__ __forceinline__ float local_max(const uint32_t (&s)[32]) {
+  float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    mx[0] = fmax3(mx[0], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+    mx[1] = fmax3(mx[1], __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+  }
+  return fmaxf(mx[0], mx[1]);
 }
 
 }  // namespace dev

@@ -210,6 +210,53 @@ def test_large_scores_and_values():
     _check(p, t, out, arrays, 4.0, None)
 
 
+def _lift(t):
+    """Adds +-96 * 8 * scale (+-96 for head_dim 64, +-68 for 128, exact in fp32) to every score of two
+    thirds of the rows: their LSE leaves +-55, the others' stays.  All scores stay below 2^7, for which the
+    oracle's fp32 share (2^-24 * 2^7 * 8 = 2^-14 of a weight) is what it allows."""
+    t["k"][..., 0] = 8.0
+    rows = torch.arange(t["q"].shape[2]) % 3
+    t["q"][..., 0] = torch.where(rows == 0, 96.0, torch.where(rows == 1, -96.0, 0.0)).to(t["q"].dtype)
+
+
+@pytest.mark.parametrize("n,head_dim", [(1, 64), (40, 64), (65, 128), (130, 64), (200, 128)])
+@pytest.mark.parametrize("cap", [0.0, 250.0])
+@pytest.mark.parametrize("kind", ["causal", "docs"])
+def test_rows_of_extreme_scores(n, head_dim, cap, kind):
+    p = _token_problem(n, heads=2, head_dim=head_dim)
+    t = W.make_tensors(p)
+    _lift(t)
+    arrays = _score_arrays(p, kind, n)
+    out = _run(p, t, sp.Plan.from_problem(p), _score(arrays, cap, None))
+    _check(p, t, out, arrays, cap, None)
+
+
+@pytest.mark.parametrize("pack", ["route64", "split", "slot"])
+def test_rows_of_extreme_scores_in_forced_packings(pack, monkeypatch):
+    monkeypatch.setenv("SPATTN_PLAN_PACK", pack)
+    p = W.make_problem("tiny_svg2")
+    t = W.make_tensors(p)
+    kept = {n: t[n].clone() for n in ("q", "k")}
+    _lift(t)
+    for n, group in (("q", p.q_group), ("k", p.kv_group)):  # the padded rows keep their sentinel
+        pad = torch.from_numpy(group < 0)
+        t[n][:, :, pad] = kept[n][:, :, pad]
+    arrays = _score_arrays(p, "prefix", 2)
+    out = _run(p, t, sp.Plan.from_problem(p), _score(arrays, 0.0, None))
+    _check(p, t, out, arrays, 0.0, None)
+
+
+@pytest.mark.parametrize("n", [5, 70, 150])
+def test_keys_all_far_away(n):
+    """A bias of 100 and more on every key of every row (one head) leaves weights, O and gradients whole."""
+    p = _token_problem(n, heads=2)
+    t = W.make_tensors(p)
+    arrays = dict(q_pos=np.arange(n) % 32 + 400, k_pos=np.arange(n) % 32, q_last=np.arange(n))
+    slopes = [0.25, 0.001]
+    out = _run(p, t, sp.Plan.from_problem(p), _score(arrays, 0.0, slopes))
+    _check(p, t, out, arrays, 0.0, slopes)
+
+
 @pytest.mark.parametrize("cap", [1e-40, 1e-20, 1e-6, 1e30])
 def test_extreme_caps(cap):
     """Caps whose scaled coefficients leave fp32; queries of zeros (scores of exactly 0) among the rows."""
