@@ -460,8 +460,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
       }
       ok = ok && soft_total(r, xr, grp, &pair_bar[q4], pass + (pass > 0), ab, l, l_true);
       if (pass == 0) {
-        constexpr float kLow = 8.271806125530277e-25f, kHigh = 1.2089258196146292e24f;  // 2^-80, 2^80
-        if (ok && seen && !(l_true >= kLow && l_true <= kHigh)) redo[0] = 1;
+        if (ok && seen && !(l_true >= kSumLow && l_true <= kSumHigh)) redo[0] = 1;
         if (!decide()) break;
       }
     }

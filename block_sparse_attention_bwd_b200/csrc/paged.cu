@@ -520,9 +520,11 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
   }
 }
 
-// Join of split rows, one warp per (token, head): with M the largest maximum,
-// O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s (m_s, l_s: a split's reference
-// and divisor; LSE has the sum of its unrounded weights).
+// Join of split rows, one warp per (token, head): O = sum_s 2^(m_s - M) O_s /
+// sum_s 2^(m_s - M) l_s (m_s, l_s: a split's reference and divisor; LSE has the sum
+// t_s of its unrounded weights).  M is the largest m_s + log2 t_s, not the largest
+// reference: a sum relative to a fixed reference may be 2^80 away from 1, so the
+// references alone do not tell which split counts.  No 2^(m_s - M) t_s passes 1.
 constexpr int kJoinWarps = 4;
 
 template <int D>
@@ -552,7 +554,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
   const int64_t part0 = tile * a.splits * a.tile_rows + row;
   const float4* ml = reinterpret_cast<const float4*>(a.part + n_part * D);
   float m = -INFINITY;
-  for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[part0 + static_cast<int64_t>(s) * a.tile_rows].x);
+  for (int s = lane; s < n; s += 32) {
+    const float4 x = ml[part0 + static_cast<int64_t>(s) * a.tile_rows];
+    if (x.x > -INFINITY) m = fmaxf(m, x.x + lg2(x.y));
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   constexpr int E = D / 32;  // elements per lane

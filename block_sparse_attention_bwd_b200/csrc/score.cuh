@@ -23,7 +23,7 @@ namespace dev {
 //   kScoreNone   the plain kernel
 //   kScoreMask   masks and bias
 //   kScoreCap    the same with a cap
-//   kScoreFixed  (paged) a cap small enough for a fixed softmax reference
+//   kScoreFixed  (paged) a cap within kCapFixedMax: a fixed softmax reference
 enum : int { kScoreNone = 0, kScoreMask = 1, kScoreCap = 2, kScoreFixed = 3 };
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -250,6 +250,10 @@ struct SoftRow {
   float l = 0.f;   // sum of this thread's weights
   float lr = 0.f;  // the same of the weights rounded to bf16
 };
+
+// Sums of weights within these leave fp32 2^46 on either side, for the values and for
+// the smaller keys; a row outside (an LSE beyond +-55 of its reference) needs its maximum.
+constexpr float kSumLow = 8.271806125530277e-25f, kSumHigh = 1.2089258196146292e24f;  // 2^-80, 2^80
 
 // Meeting of the two warps of a row pair (a barrier of 64 arrivals), the n-th.  A
 // bounded wait, so that a warp that gave up cannot strand its partner; false

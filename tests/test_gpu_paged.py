@@ -32,6 +32,8 @@ class Setup:
             at += need[i]
             self.table[i, :need[i]] = mine
             a, b = (torch.randn((kv, kv_heads, head_dim), generator=gen).bfloat16() for _ in range(2))
+            if kw.get("lift"):
+                a[:, :, 0] = torch.where(torch.arange(kv) < kv // 16, 8.0, -8.0)[:, None]
             for j, p in enumerate(mine):
                 n = min(page_slots, kv - j * page_slots)
                 k[p, :n], v[p, :n] = a[j * page_slots:j * page_slots + n], b[j * page_slots:j * page_slots + n]
@@ -41,6 +43,8 @@ class Setup:
         self.k, self.v = k.cuda(), v.cuda()
         self.T = sum(q for q, _ in lens) + 3  # rows behind the last sequence
         self.q = (torch.randn((self.T, heads, head_dim), generator=gen) * 1.5).bfloat16().cuda()
+        if kw.get("lift"):
+            self.q[:, :, 0] = torch.tensor([96.0, -96.0, 0.0]).cuda()[torch.arange(self.T).cuda() % 3][:, None]
         self.d_table = torch.from_numpy(self.table.astype(np.int32)).cuda()
         self.q_start = torch.tensor(np.cumsum([0] + [q for q, _ in lens]), dtype=torch.int32).cuda()
         self.kv_len = torch.tensor([kv for _, kv in lens], dtype=torch.int32).cuda()
@@ -95,6 +99,24 @@ CASES = [
 @pytest.mark.parametrize("lens,heads,kv_heads,d,ps,kw", CASES)
 def test_paged_parity(lens, heads, kv_heads, d, ps, kw):
     s = Setup(lens, heads, kv_heads, d, ps, **kw)
+    s.check(*s.run())
+
+
+@pytest.mark.parametrize("lens,heads,kv_heads,d,ps,kw", [
+    ([(1, 1)], 1, 1, 64, 16, {}),
+    ([(1, 5000)], 2, 1, 64, 32, {}),
+    ([(1, 5000)], 2, 1, 64, 32, dict(slopes=[0.02, 0.01])),
+    ([(1, 5000)], 2, 1, 64, 32, dict(slopes=[0.0203, 0.019], softcap=55.0)),
+    ([(7, 900), (1, 40), (0, 0), (2, 65)], 4, 2, 64, 16, dict(slopes=[0.0, 0.05, -0.05, 0.1])),
+    ([(150, 333)], 3, 3, 128, 48, dict(softcap=250.0)),
+    ([(65, 2000)], 4, 1, 128, 64, {}),
+])
+def test_extreme_scores(lens, heads, kv_heads, d, ps, kw):
+    """Scores raised by up to 96 (68 for head_dim 128) for the first sixteenth of the keys and lowered for
+    the rest, in a third of the rows; the other way round in another third.  Scores that count stay below 2^7,
+    for which the oracle's fp32 share (2^-24 * 2^7 * 8 = 2^-14 of a weight) holds; the biases make the
+    splits' references differ by as much."""
+    s = Setup(lens, heads, kv_heads, d, ps, lift=True, **kw)
     s.check(*s.run())
 
 
