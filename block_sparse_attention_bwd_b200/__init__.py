@@ -565,10 +565,10 @@ def rope_freqs(sections, base=10000.0, scaling=None, factor=1.0, original_slots=
     return torch.from_numpy(np.concatenate(ladders) if ladders else np.zeros(0)).to(device), mscale
 
 
-def _span(t):
-    """[first, end) byte addresses that a tensor's elements touch."""
-    last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
-    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+def _rope_span(t):
+    """[first, end) byte addresses that a [B, H, S, D] tensor's rows touch."""
+    (b, h, n, d), (x, y, z, _), at = t.shape, t.stride(), t.data_ptr()
+    return at, at + ((b - 1) * x + (h - 1) * y + (n - 1) * z + d) * t.element_size()
 
 
 def _rope_rows(t, what, name, dtype, device, shape=None):
@@ -583,18 +583,21 @@ def _rope_rows(t, what, name, dtype, device, shape=None):
 
 def _rope_overlaps(name, ins, outs):
     """Refuses outputs that overlap an input without being in place of it."""
-    own = [y.data_ptr() == x.data_ptr() and all(a == b or n == 1 for a, b, n in zip(x.stride(), y.stride(), x.shape))
-           for x, y in zip(ins, outs)]
-    for i, y in enumerate(outs):
-        if any(n > 1 and st == 0 for n, st in zip(y.shape, y.stride())):
+    for y in outs:
+        if 0 in y.stride() and any(n > 1 and st == 0 for n, st in zip(y.shape, y.stride())):
             raise ValueError(f"{name}: an output has elements that share an address")
-        for j, x in enumerate(ins):
-            (a0, a1), (b0, b1) = _span(y), _span(x)
-            # views of one packed buffer interleave; both in place is the case that is allowed
-            if a0 < b1 and b0 < a1 and not (own[i] and (i == j or own[j])):
-                raise ValueError(f"{name}: an output overlaps an input without being in place of it")
     if len(outs) == 2 and outs[0].data_ptr() == outs[1].data_ptr():
         raise ValueError(f"{name}: the two outputs share an address")
+    spans = [_rope_span(x) for x in ins]
+    meet = [(i, j) for i, y in enumerate(outs) for (a0, a1) in (_rope_span(y),)
+            for j, (b0, b1) in enumerate(spans) if a0 < b1 and b0 < a1]
+    if not meet:
+        return
+    own = [y.data_ptr() == x.data_ptr() and all(a == b or n == 1 for a, b, n in zip(x.stride(), y.stride(), x.shape))
+           for x, y in zip(ins, outs)]
+    # views of one packed buffer interleave; both in place is the case that is allowed
+    if any(not (own[i] and (i == j or own[j])) for i, j in meet):
+        raise ValueError(f"{name}: an output overlaps an input without being in place of it")
 
 
 def _rope(name, inverse, q, k, pos, freqs, rot_dim, interleaved, sections, mscale, q_out, k_out, stream):
@@ -780,8 +783,8 @@ def spattn_paged_fwd(q, k_cache, v_cache, page_table, q_start, kv_len, paged: Pa
             or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous uint8 tensor on {dev}")
     # (the stride of a single token or head means nothing)
-    c = _PACK_PAGED.pack(q.data_ptr(), q.stride(0) if T > 1 else 0, q.stride(1) if H > 1 else 0, T, k_cache.data_ptr(), v_cache.data_ptr(), *strides,
-                         pages, page_table.data_ptr(), width, n, q_start.data_ptr(), kv_len.data_ptr(),
+    c = _PACK_PAGED.pack(q.data_ptr(), q.stride(0) if T > 1 else 0, q.stride(1) if H > 1 else 0, T,
+                         k_cache.data_ptr(), v_cache.data_ptr(), *strides, pages, page_table.data_ptr(), width, n, q_start.data_ptr(), kv_len.data_ptr(),
                          0 if slopes is None else slopes.data_ptr(), o.data_ptr(), lse.data_ptr(),
                          0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     _check(_lib().spattn_paged_fwd(paged.handle, c, _raw_stream(stream, dev)), "spattn_paged_fwd")
