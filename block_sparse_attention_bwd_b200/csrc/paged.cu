@@ -140,10 +140,12 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
   float* xrow = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + C::kBars);
   uint64_t* pair_bar = reinterpret_cast<uint64_t*>(xrow + 4 * 128);  // [4]
 
-  const int qt = blockIdx.x / a.splits, split = blockIdx.x - qt * a.splits;
-  const int hk = blockIdx.y, sq = blockIdx.z;
+  // tiles and then K/V heads vary fastest: CTAs that run together read the same
+  // range, and the heads of its pages side by side
+  const int split = blockIdx.x / (a.q_tiles * a.kv_heads), tile_hk = blockIdx.x - split * a.q_tiles * a.kv_heads;
+  const int hk = tile_hk / a.q_tiles, qt = tile_hk - hk * a.q_tiles, sq = blockIdx.y;
   const Seq seq = load_seq(a, sq);
-  if (!seq.ok && threadIdx.x == 0 && blockIdx.x == 0 && hk == 0) atomicCAS(a.err, 0, kErrBadWork);
+  if (!seq.ok && threadIdx.x == 0 && blockIdx.x == 0) atomicCAS(a.err, 0, kErrBadWork);
   const int rows = min(kRows, seq.nq * a.group - qt * kRows);
   if (rows <= 0) return;  // uniform over the CTA
   const int keys = tile_keys(a, seq, qt);
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
     if (ok) {
       const int64_t out = static_cast<int64_t>(seq.t0 + tok) * a.heads + head;
       const int64_t tile = (static_cast<int64_t>(sq) * a.kv_heads + hk) * a.q_tiles + qt;
-      const int64_t n_part = static_cast<int64_t>(gridDim.z) * a.kv_heads * a.q_tiles * a.splits * a.tile_rows;
+      const int64_t n_part = static_cast<int64_t>(gridDim.y) * a.kv_heads * a.q_tiles * a.splits * a.tile_rows;
       const int64_t part = (tile * a.splits + split) * a.tile_rows + row;
       const bool empty = !(l > 0.f);
       const float inv = empty ? 0.f : 1.0f / l;
@@ -596,8 +598,7 @@ cudaError_t launch_paged_t(const TmaPages& tk, const TmaPages& tv, const PagedAr
   cudaError_t e =
       cudaFuncSetAttribute(paged_kernel<D, FORM, SMALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(a.q_tiles * a.splits), static_cast<unsigned>(a.kv_heads),
-                  static_cast<unsigned>(n_seqs));
+  const dim3 grid(static_cast<unsigned>(a.q_tiles * a.kv_heads * a.splits), static_cast<unsigned>(n_seqs));
   paged_kernel<D, FORM, SMALL><<<grid, C::kThreads, C::kSmem, st>>>(tk, tv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
