@@ -95,35 +95,6 @@ bool make_strided_map(CUtensorMap* m, const void* ptr, int head_dim, int64_t row
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Maps of a paged cache: [slots, head_dim] rows of each head, with the strides
-// given (elements), in 16-, 32- and 64-row boxes and 64 rows x every chunk.
-bool make_cache_maps(TmaPages* t, const void* ptr, int head_dim, int64_t slots, int64_t slot_stride, int64_t heads,
-                     int64_t head_stride) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t row = static_cast<cuuint64_t>(slot_stride) * 2;
-  const cuuint64_t head = heads > 1 ? static_cast<cuuint64_t>(head_stride) * 2 : row;
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  CUtensorMap* maps[3] = {&t->m16, &t->m32, &t->m64};
-  for (int i = 0; i < 3; ++i) {
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(slots),
-                                static_cast<cuuint64_t>(heads)};
-    const cuuint64_t strides[2] = {row, head};
-    const cuuint32_t box[3] = {64, 16u << i, 1};
-    if (fn(maps[i], map_type(2), 3, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return false;
-  }
-  const int nch = head_dim / 64;
-  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(slots), static_cast<cuuint64_t>(nch),
-                              static_cast<cuuint64_t>(heads)};
-  const cuuint64_t strides[3] = {row, 128, head};
-  const cuuint32_t box[4] = {64, 64, static_cast<cuuint32_t>(nch), 1};
-  return fn(&t->m64w, map_type(2), 4, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 bool make_pages(TmaPages* t, const void* ptr, int head_dim, int64_t rows, int64_t bh, int eb = 2) {
   if (!make_strided_map(&t->m4s, ptr, head_dim, rows, bh, eb)) return false;
@@ -353,9 +324,25 @@ int run_bwd(const void* q, const void* k, const void* v, const void* o, const fl
 bool make_tensor_pages(TmaPages* t, const void* ptr, int head_dim, int64_t rows, int64_t bh) {
   return make_pages(t, ptr, head_dim, rows, bh);
 }
-bool make_cache_pages(TmaPages* t, const void* ptr, int head_dim, int64_t slots, int64_t slot_stride, int64_t heads,
+bool make_cache_pages(CachePages* t, const void* ptr, int head_dim, int64_t slots, int64_t slot_stride, int64_t heads,
                       int64_t head_stride) {
-  return make_cache_maps(t, ptr, head_dim, slots, slot_stride, heads, head_stride);
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(slot_stride) * 2;
+  const cuuint64_t head = heads > 1 ? static_cast<cuuint64_t>(head_stride) * 2 : row;
+  const cuuint32_t nch = static_cast<cuuint32_t>(head_dim / 64);
+  const cuuint64_t dims[5] = {64, 8, nch, static_cast<cuuint64_t>(slots / 8), static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, head};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  CUtensorMap* maps[3] = {&t->m16, &t->m32, &t->m64};
+  for (int i = 0; i < 3; ++i) {
+    const cuuint32_t box[5] = {64, 8, nch, 2u << i, 1};
+    if (fn(maps[i], map_type(2), 5, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  return true;
 }
 TileArgs make_tile_args(const spattn_plan_s* P, const WorkList& w, int64_t own_slots, int64_t col_slots) {
   return tile_args(P, w, own_slots, col_slots);

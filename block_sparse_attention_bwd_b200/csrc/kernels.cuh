@@ -29,6 +29,17 @@ struct TmaPages {
   CUtensorMap m4s;
 };
 
+// Descriptors over a paged cache's [slots, head_dim] rows of each head, with the
+// call's strides, in boxes of 16, 32 and 64 rows.  5D (64 columns, 8 rows, 64-column
+// chunk, 8-row group, head): a box lands group by group, each 8 rows of every chunk
+// (1 KB apiece), so that whole rows of any run of pages take one request, and
+// pages of 16 rows stand behind each other as the MMA descriptors want them.
+struct CachePages {
+  CUtensorMap m16, m32, m64;
+};
+bool make_cache_pages(CachePages* t, const void* ptr, int head_dim, int64_t slots, int64_t slot_stride, int64_t heads,
+                      int64_t head_stride);
+
 // Everything one attention launch needs besides its tensor maps.
 struct TileArgs {
   const int32_t* work = nullptr;    // n_work x 32 words (see spattn_plan_work)

@@ -32,16 +32,12 @@
 #include "spattn.h"
 
 namespace spattn {
-bool make_cache_pages(TmaPages* t, const void* ptr, int head_dim, int64_t slots, int64_t slot_stride, int64_t heads,
-                      int64_t head_stride);
-
 namespace {
 
 using namespace dev;
 
 constexpr int kStepKeys = 64;
 constexpr int kStep16 = kStepKeys / 16;
-constexpr int kStageChunk = kStepKeys * 128;
 constexpr float kRescale = 8.0f;  // rescale O when the running maximum grows by more than 2^8, as in the plan's forward
 
 // FORM: kScoreMask (no cap) and kScoreCap run with a running maximum, one thread
@@ -56,7 +52,8 @@ struct PagedCfg {
   static constexpr int kNch = D / 64;
   static constexpr int kQChunk = SMALL ? 32 * 128 : kChunkBytes;
   static constexpr int kTile = kNch * kQChunk;
-  static constexpr int kStage = kNch * kStageChunk;
+  static constexpr int kStage = kNch * kStepKeys * 128;
+  static constexpr int kGroup = kNch * 1024;  // 8 rows of a stage
   static constexpr int kKStages = D == 128 ? (SMALL ? 3 : 2) : (SMALL ? 6 : 4);
   static constexpr int kVStages = kKStages;
   static constexpr int kRowThreads = FORM == kScoreFixed ? 256 : 128;
@@ -111,9 +108,29 @@ __device__ __forceinline__ int tile_keys(const PagedArgs& a, const Seq& s, int q
   return s.kv - s.nq + last + 1;
 }
 
+// Load n 16-slot pages (lane j: page pid of step page j) into a stage, one box per
+// run of consecutive pages and power of two.  All 32 lanes call this.
+template <int NCH>
+__device__ __forceinline__ void load_cache_runs(uint8_t* dst, const CachePages& maps, int pid, int n, int head,
+                                                uint64_t* bar) {
+  const int lane = lane_id();
+  const int nxt = __shfl_down_sync(0xffffffffu, pid, 1);
+  const unsigned cont = __ballot_sync(0xffffffffu, lane + 1 < n && nxt == pid + 1);  // bit j: page j + 1 follows page j
+  if (lane >= n || (lane > 0 && ((cont >> (lane - 1)) & 1u))) return;
+  int rem = __ffs(~(cont >> lane)), j = 0;  // the run: at most kStep16 pages; j of them are on their way
+  auto box = [&](const CUtensorMap* m, int pages) {
+    tma_load_5d(dst + (lane + j) * NCH * 2048, m, 0, 0, 0, 2 * (pid + j), head, bar);
+    j += pages;
+    rem -= pages;
+  };
+  if (rem >= 4) box(&maps.m64, 4);
+  if (rem >= 2) box(&maps.m32, 2);
+  if (rem == 1) box(&maps.m16, 1);
+}
+
 template <int D, int FORM, bool SMALL>
 __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
-    paged_kernel(const __grid_constant__ TmaPages tm_k, const __grid_constant__ TmaPages tm_v, const PagedArgs a) {
+    paged_kernel(const __grid_constant__ CachePages tm_k, const __grid_constant__ CachePages tm_v, const PagedArgs a) {
   using C = PagedCfg<D, FORM, SMALL>;
   constexpr bool kFixed = FORM == kScoreFixed, kCap = kFixed || FORM == kScoreCap;
   constexpr int KS = C::kKStages, VS = C::kVStages;
@@ -218,12 +235,12 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
       if (st >= KS && !__all_sync(0xffffffffu, mbar_wait(&k_empty[ks], ((st / KS) - 1) & 1, ab))) break;
       if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], n * C::kNch * 2048);
       __syncwarp();
-      load_page_runs<C::kNch>(sK + ks * C::kStage, kStageChunk, tm_k, pid, n, hk, &k_full[ks]);
+      load_cache_runs<C::kNch>(sK + ks * C::kStage, tm_k, pid, n, hk, &k_full[ks]);
       k_issued = st + 1;
       if (st >= VS && !__all_sync(0xffffffffu, mbar_wait(&v_empty[vs], ((st / VS) - 1) & 1, ab))) break;
       if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], n * C::kNch * 2048);
       __syncwarp();
-      load_page_runs<C::kNch>(sV + vs * C::kStage, kStageChunk, tm_v, pid, n, hk, &v_full[vs]);
+      load_cache_runs<C::kNch>(sV + vs * C::kStage, tm_v, pid, n, hk, &v_full[vs]);
       v_issued = st + 1;
     }
     // no copy may still be landing in shared memory when the CTA exits
@@ -234,8 +251,8 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, 1024);
-    const uint64_t dv0 = sdesc_sw128(smem_u32(sV), kStageChunk, 1024);
+    const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, C::kGroup);
+    const uint64_t dv0 = sdesc_sw128(smem_u32(sV), 1024, C::kGroup);
     const uint32_t idesc_pv = idesc_bf16(128, D, false, true);
     bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, ab));
     tc_fence_after();
@@ -250,8 +267,8 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
       if (live < 16 * n) {
         for (int i = lane; i < (16 * n - live) * 8 * C::kNch; i += 32) {
           const int r = live + i / (8 * C::kNch), c = i % (8 * C::kNch);
-          *reinterpret_cast<uint4*>(sV + vs * C::kStage + (c >> 3) * kStageChunk + r * 128 + (c & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(sV + vs * C::kStage + (r >> 3) * C::kGroup + (c >> 3) * 1024 + (r & 7) * 128 +
+                                    (c & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -261,7 +278,7 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
 #pragma unroll
       for (int j = 0; j < kStep16; ++j)
         if (j < n)
-          umma_ts_w(tO, tmem + 64 * b + 8 * j + (kFixed && j >= 2 ? 16 : 0), sdesc_add(dv, j * 2048), idesc_pv,
+          umma_ts_w(tO, tmem + 64 * b + 8 * j + (kFixed && j >= 2 ? 16 : 0), sdesc_add(dv, j * 2 * C::kGroup), idesc_pv,
                     (st > 0 || j > 0) ? 1u : 0u);
       umma_commit_w(&v_empty[vs]);
       umma_commit_w(o_done);
@@ -282,7 +299,7 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         umma_ss_w(tmem + 64 * b, sdesc_add(dq0, (kk >> 2) * C::kQChunk + (kk & 3) * 32),
-                  sdesc_add(dk, (kk >> 2) * kStageChunk + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
+                  sdesc_add(dk, (kk >> 2) * 1024 + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
       umma_commit_w(&s_full[b]);
       umma_commit_w(&k_empty[ks]);
       if (st >= 1 && !issue_pv(st - 1)) ok = false;
@@ -593,7 +610,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
 }
 
 template <int D, int FORM, bool SMALL>
-cudaError_t launch_paged_t(const TmaPages& tk, const TmaPages& tv, const PagedArgs& a, int n_seqs, cudaStream_t st) {
+cudaError_t launch_paged_t(const CachePages& tk, const CachePages& tv, const PagedArgs& a, int n_seqs, cudaStream_t st) {
   using C = PagedCfg<D, FORM, SMALL>;
   cudaError_t e =
       cudaFuncSetAttribute(paged_kernel<D, FORM, SMALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -608,13 +625,13 @@ cudaError_t launch_paged_t(const TmaPages& tk, const TmaPages& tv, const PagedAr
 }
 
 template <int D, int FORM>
-cudaError_t launch_paged_f(const TmaPages& tk, const TmaPages& tv, const PagedArgs& a, int n_seqs, cudaStream_t st) {
+cudaError_t launch_paged_f(const CachePages& tk, const CachePages& tv, const PagedArgs& a, int n_seqs, cudaStream_t st) {
   return a.tile_rows <= 32 ? launch_paged_t<D, FORM, true>(tk, tv, a, n_seqs, st)
                            : launch_paged_t<D, FORM, false>(tk, tv, a, n_seqs, st);
 }
 
 template <int D>
-cudaError_t launch_paged(const TmaPages& tk, const TmaPages& tv, const PagedArgs& a, int n_seqs, cudaStream_t st) {
+cudaError_t launch_paged(const CachePages& tk, const CachePages& tv, const PagedArgs& a, int n_seqs, cudaStream_t st) {
   if (!(a.cap > 0.f)) return launch_paged_f<D, kScoreMask>(tk, tv, a, n_seqs, st);
   return a.c.cap2 <= kCapFixedMax ? launch_paged_f<D, kScoreFixed>(tk, tv, a, n_seqs, st)
                                   : launch_paged_f<D, kScoreCap>(tk, tv, a, n_seqs, st);
@@ -765,7 +782,7 @@ int spattn_paged_fwd(spattn_paged_t p, const spattn_paged_call* c, void* stream)
   const int64_t need = split_bytes(p, sp, c->n_seqs);
   if (c->workspace_bytes < need || (need > 0 && !aligned(c->workspace, 16))) return SPATTN_ERR_INVALID_ARG;
   const int64_t slots = c->n_pages * L.page_slots;
-  TmaPages tk, tv;
+  CachePages tk, tv;
   if (!make_cache_pages(&tk, c->k_cache, L.head_dim, slots, c->k_slot_stride, L.kv_heads, c->k_head_stride) ||
       !make_cache_pages(&tv, c->v_cache, L.head_dim, slots, c->v_slot_stride, L.kv_heads, c->v_head_stride))
     return SPATTN_ERR_CUDA;
