@@ -17,6 +17,13 @@
 // step that read the column tiles, warp 10 issues the accumulating products,
 // and warps 2..9 turn each step's scores into P / dS, one tile row per lane,
 // two warp groups per step (32 columns each).
+//
+// Scored forms (spattn_score): P from the modified scores z, dS = P (dP - Delta)
+// (1 - tanh^2), four warp groups of 16 columns, -LSE, positions and documents of the
+// columns in lines beside the stages.  Bound: the row threads' instructions and the
+// latency of a step (tensor pipe busy 0.40 to 0.45).  12289 causal tokens with a
+// prefix and a cap of 50, 16 heads over 4, D = 128: dK / dV 1724 us and dQ 1461
+// (masks alone 1473 and 1053, unmodified 1238 and 906).
 #include <algorithm>
 #include <type_traits>
 
@@ -185,7 +192,8 @@ struct DkvCfg {
 //
 // The scored forms do several times the arithmetic per pair; two row warps per
 // scheduler left most of its latency in the open (issue slots 0.38 busy), so they
-// split a step over four groups of 16 columns (16 row warps).
+// split a step over four groups of 16 columns (16 row warps): dK / dV of 12289
+// causal tokens 2817 -> 2112 us.
 // The producer of the second column tensor (dO stages for dK / dV, V stages for
 // dQ; warp 0 produces the Q or K stages) is the last warp: a TMA request holds
 // its issuing thread for hundreds of cycles, so one producer for both column
@@ -898,7 +906,8 @@ struct DqCfg {
 // rounding of dS; in a row of two or five keys dP - Delta is a difference of like
 // numbers, and dQ came out 1% off (its own roundings are 0.24%).  Items of up to
 // 256 keys therefore get this pass (their rows are where keys are few, and it costs
-// a few steps each); it overwrites what Delta = dO.O gave.
+// a few steps each: 9 of 84 us for two rows of 777 tokens with 4 heads); it
+// overwrites what Delta = dO.O gave.
 template <int D, int SC, bool DELTA>
 __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     dq_kernel(const __nv_bfloat16* __restrict__ q, const __grid_constant__ TmaPages tm_do,

@@ -10,16 +10,23 @@
 // head) pairs of that head's group, token by token, so that a cached row is
 // read once for all heads that share it.  The rest is the tile form of the
 // plan's forward: 64 keys a step gathered by TMA, S = Q K^T and O += P V on
-// tcgen05 with S double-buffered in TMEM, one row per softmax thread, two CTAs
-// per SM.  A page of the cache is a run of 16-slot pages, so the table's
-// entries go through the same box merging as the plan's page lists.
+// tcgen05 with S double-buffered in TMEM, one or two threads per row, two CTAs
+// per SM.  A page of the cache is a run of 16-slot pages; a run of consecutive
+// ones takes one request per 64 rows, whole rows at a time (CachePages).  The
+// TMA engine's time goes by requests: with one per 64-column chunk, 64 sequences in
+// pages of 16 slots took 328 us, not 270.
 //
 // Bound: with few rows per tile the cache's bytes (one step moves 32 KB at
 // head_dim 128 for 0.27 us of tensor work on an SM that gets 44 GB/s: memory
 // sets the pace), with full tiles the softmax and the tensor core as in the
 // plan's forward.  Long caches with few tiles are split along the keys into
 // ranges of `chunk` keys; split rows go to a workspace in fp32 with their
-// running maximum and sum, and paged_join_kernel adds them.
+// reference and sum, and paged_join_kernel adds them.
+//
+// Measured (head_dim 128): 64 decoding sequences of 500 .. 9000 keys, 32 heads over
+// 8, in 241 us (5.4 TB/s); 2048 tokens over 131072 keys, 16 heads over 4, in
+// 2185 us (1.0 PFLOP/s); 777 keys of one sequence in 16 us, of which the launches and
+// the host are most.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -42,16 +49,24 @@ constexpr float kRescale = 8.0f;  // rescale O when the running maximum grows by
 
 // FORM: kScoreMask (no cap) and kScoreCap run with a running maximum, one thread
 // per row; kScoreFixed (a cap within kCapFixedMax) has a fixed reference and two
-// threads per row (score.cuh).
-// SMALL: tiles of at most 32 rows (decoding).  Q then takes 4 KB per chunk, not 16,
-// and the K and V rings are a stage deeper: with one warp of rows memory sets the
-// pace, and it needs the bytes in flight.  The tensor core still reads 128 rows,
-// the other 96 from the stages behind Q; their products land in lanes nothing reads.
+// threads per row (score.cuh).  Without a cap two threads and the plan's forward's
+// passes for extreme rows were slower here, where no column lines are compared:
+// 2420 us, not 2288, for 2048 tokens over 131072 keys.
+// SMALL: tiles of at most 32 rows (decoding).  Memory sets the pace there, and in
+// a long run the board's power: products of 128 rows, four of them live and the others
+// whatever stood in shared memory, throttled the clocks to 1.57 GHz (64 sequences:
+// 235 us in a short run, 280 in one of a second).  So the products have 64 rows, and
+// all but the live ones are zeros, which cost little (241 and 255 us).  Q takes 4 KB per
+// chunk and 4 KB of zeros behind them (rows 32 .. 63 of a chunk are what follows it), and the K
+// and V rings are a stage deeper.  Row r of an M = 64 product is TMEM lane
+// r % 16 + 32 (r / 16).
 template <int D, int FORM, bool SMALL>
 struct PagedCfg {
   static constexpr int kNch = D / 64;
   static constexpr int kQChunk = SMALL ? 32 * 128 : kChunkBytes;
-  static constexpr int kTile = kNch * kQChunk;
+  static constexpr int kM = SMALL ? 64 : 128;  // rows of a product
+  static constexpr int kWarpRows = kM / 4;
+  static constexpr int kTile = kNch * kQChunk + (SMALL ? kQChunk : 0);
   static constexpr int kStage = kNch * kStepKeys * 128;
   static constexpr int kGroup = kNch * 1024;  // 8 rows of a stage
   static constexpr int kKStages = D == 128 ? (SMALL ? 3 : 2) : (SMALL ? 6 : 4);
@@ -171,12 +186,12 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
   const bool whole = keys <= a.chunk;  // the only split of this tile
   const int n16 = (k1 - k0 + 15) / 16;
   const int n_steps = (n16 + kStep16 - 1) / kStep16;
-  const int row_warps = (rows + 31) / 32;
+  const int row_warps = (rows + C::kWarpRows - 1) / C::kWarpRows;
   const int warp = warp_id(), lane = lane_id();
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    mbar_init(q_full, 32 * row_warps);  // group 0 of the row threads loads Q
+    mbar_init(q_full, SMALL ? C::kRowThreads : 32 * row_warps);  // group 0 of the row threads loads Q
     for (int s = 0; s < KS; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
@@ -204,6 +219,16 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
   const uint32_t tmem = *tslot;
   const uint32_t tO = tmem + 128;
 
+  if constexpr (SMALL) {
+    // every row thread: zeros wherever Q has no live row
+    if (warp >= 2) {
+      for (int i = threadIdx.x - 64; i < C::kTile / 16; i += C::kRowThreads)
+        if (((i >> 3) & 31) >= rows || i >= C::kNch * C::kQChunk / 16)
+          reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      if (warp >= 6 || (warp & 3) >= row_warps) mbar_arrive(q_full);  // (the others when they have loaded their rows)
+    }
+  }
   if (warp == 0) {
     // ---------------- producer: lane j < 4 owns 16-slot page j of a step ----------------
     if (lane == 0) {
@@ -253,7 +278,7 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
     const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
     const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, C::kGroup);
     const uint64_t dv0 = sdesc_sw128(smem_u32(sV), 1024, C::kGroup);
-    const uint32_t idesc_pv = idesc_bf16(128, D, false, true);
+    const uint32_t idesc_pv = idesc_bf16(C::kM, D, false, true);
     bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, ab));
     tc_fence_after();
     auto issue_pv = [&](int st) -> bool {
@@ -295,7 +320,7 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
       tc_fence_after();
       const int n = min(kStep16, n16 - st * kStep16);
       const uint64_t dk = sdesc_add(dk0, ks * C::kStage);
-      const uint32_t idesc_s = idesc_bf16(128, 16 * n, false, false);
+      const uint32_t idesc_s = idesc_bf16(C::kM, 16 * n, false, false);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
         umma_ss_w(tmem + 64 * b, sdesc_add(dq0, (kk >> 2) * C::kQChunk + (kk & 3) * 32),
@@ -312,22 +337,22 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
     const int grp = kFixed ? (warp - 2) >> 2 : 0;  // fixed form: column half of a step, and of O
     const int q4 = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    const int row = q4 * 32 + lane;
-    const int rr = qt * kRows + row;
-    const int tok = min(rr / a.group, seq.nq - 1);  // rows behind the last repeat its token and are not stored
-    const int head = hk * a.group + rr % a.group;
-    const bool live = row < rows;
-    const int last = seq.kv - seq.nq + tok;  // this row's position
+    const int row = C::kWarpRows * q4 + lane;
+    const bool live = lane < C::kWarpRows && row < rows;  // the others are zeros, attend nothing and are not stored
+    const int rr = qt * kRows + (live ? row : 0);
+    const int tok = rr / a.group, head = hk * a.group + rr % a.group;
+    const int last = live ? seq.kv - seq.nq + tok : -1;  // this row's position
     if (grp == 0) {
       // the row's 16-byte pieces go to their places in the 128-byte swizzle
       const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(seq.t0 + tok) * a.q_token +
                                                         static_cast<int64_t>(head) * a.q_head);
       uint4 v[D / 8];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) v[i] = __ldg(src + i);
+      for (int i = 0; i < D / 8; ++i) v[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<uint4*>(sQ + (i >> 3) * C::kQChunk + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = v[i];
+        if (live || !SMALL)
+          *reinterpret_cast<uint4*>(sQ + (i >> 3) * C::kQChunk + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = v[i];
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     }
@@ -389,7 +414,7 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
       }
       ok = ok && __all_sync(0xffffffffu, mbar_wait(o_last, 0, ab));
       tc_fence_after();
-      ok = ok && soft_total(r, xrow + row, grp, &pair_bar[q4], 0, ab, l, l_true);
+      ok = ok && soft_total(r, xrow + 32 * q4 + lane, grp, &pair_bar[q4], 0, ab, l, l_true);
     } else {
       const float mul = kCap ? 1.0f : sl2;  // after the cap the scores are in log2 units
       const uint64_t mul2 = f2_pack(mul, mul);
@@ -642,8 +667,15 @@ cudaError_t launch_paged(const CachePages& tk, const CachePages& tv, const Paged
 
 using namespace spattn;
 
+namespace {
+struct Split {
+  int q_tiles = 0, tile_rows = 0, splits = 0, chunk = 0;
+};
+}  // namespace
+
 struct spattn_paged_s {
   spattn_paged_layout lay;
+  Split one;  // the split of calls with one sequence
   int device = -1;
   int sms = 148;
   int* d_err = nullptr;
@@ -658,12 +690,12 @@ namespace {
 // the split count with the fewest rounds x cost wins.  Of several, the host knows
 // only the bounds: with half of them as the mean length, ranges of about
 // sqrt(work x overhead / slots) keys balance that overhead against the last
-// CTA's tail (1.5 times that measured best: 64 sequences of 500 .. 9000 keys
-// took 271, 253, 243 and 247 us with factors 0.5, 1, 1.5 and 2.5).
-struct Split {
-  int q_tiles, tile_rows, splits, chunk;
-};
+// CTA's tail.  1.5 times that measured best over both kinds of call: with factors
+// 1, 1.5, 2 and 2.7, 64 decoding sequences of 500 .. 9000 keys took 243, 235, 230
+// and 240 us, eight of 4000 .. 60000 keys 232, 201, 201 and 219, and five
+// sequences of chunks up to 700 tokens 375, 384, 427 and 475.
 Split choose_split(const spattn_paged_s* p, int64_t n_seqs) {
+  if (n_seqs == 1 && p->one.splits) return p->one;
   const auto& L = p->lay;
   const int64_t group = L.heads / L.kv_heads;
   Split s;
@@ -738,6 +770,7 @@ int spattn_paged_create(const spattn_paged_layout* L, spattn_paged_t* out) {
   } else {
     cudaGetLastError();  // no device: checks and workspace sizes only
   }
+  p->one = choose_split(p, 1);
   *out = p;
   return SPATTN_OK;
 }
