@@ -430,22 +430,25 @@ class Score:
 
 
 _TORCH = None
+_CURRENT_RAW_STREAM = None
 
 
 def _torch():
-    global _TORCH
+    global _TORCH, _CURRENT_RAW_STREAM
     if _TORCH is None:
         import torch
 
+        # (without the Stream object around the handle, where torch offers that)
+        _CURRENT_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                      lambda index: torch.cuda.current_stream(index).cuda_stream)
         _TORCH = torch
     return _TORCH
 
 
-
 def _want(t, name, shape, dtype, device):
-    """_need, and on the given device."""
-    if not isinstance(t, _torch().Tensor) or t.dtype is not dtype or t.device != device or t.shape != shape \
-            or not t.is_contiguous() or not t.is_cuda:
+    """_need, and on the given device (a CUDA one)."""
+    if not isinstance(t, _TORCH.Tensor) or t.dtype is not dtype or t.device != device or t.shape != shape \
+            or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
@@ -453,13 +456,12 @@ def _raw_stream(stream, device):
     """The stream's handle; without one, that of the current stream of ``device``."""
     if stream is not None:
         return stream.cuda_stream
-    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)  # without the Stream object around it
-    return raw(device.index) if raw is not None else _torch().cuda.current_stream(device).cuda_stream
+    return _CURRENT_RAW_STREAM(device.index)
 
 
 def _device_of(t, name):
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
+        raise ValueError(f"{name}: expected a CUDA tensor, not {type(t).__name__}")
     return t.device
 
 
@@ -482,7 +484,7 @@ def spattn_fwd_scored(q, k, v, plan: Plan, score: Score, o=None, lse=None, strea
     _want(v, "v", ks, bf16, dev)
     sc = score._packed(plan, dev)
     if o is None:
-        o = q.new_empty(qs)
+        o = torch.empty_like(q)
     else:
         _want(o, "o", qs, bf16, dev)
     if lse is None:
@@ -508,15 +510,15 @@ def spattn_bwd_scored(q, k, v, o, lse, do, plan: Plan, score: Score, dq=None, dk
     _want(lse, "lse", qs[:3], torch.float32, dev)
     sc = score._packed(plan, dev)
     if dq is None:
-        dq = q.new_empty(qs)
+        dq = torch.empty_like(q)
     else:
         _want(dq, "dq", qs, bf16, dev)
     if dk is None:
-        dk = q.new_empty(ks)
+        dk = torch.empty_like(k)
     else:
         _want(dk, "dk", ks, bf16, dev)
     if dv is None:
-        dv = q.new_empty(ks)
+        dv = torch.empty_like(k)
     else:
         _want(dv, "dv", ks, bf16, dev)
     _check(_lib().spattn_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
@@ -571,14 +573,20 @@ def _rope_span(t):
     return at, at + ((b - 1) * x + (h - 1) * y + (n - 1) * z + d) * t.element_size()
 
 
-def _rope_rows(t, what, name, dtype, device, shape=None):
-    """Checks a [B, H, S, D] tensor of a rope call."""
-    if not isinstance(t, _torch().Tensor) or t.dim() != 4 or t.dtype is not dtype or t.device != device:
+def _rope_rows(t, what, name, dtype, device):
+    """Shape and strides of a [B, H, S, D] tensor of a rope call, checked."""
+    if not isinstance(t, _TORCH.Tensor) or t.dtype is not dtype or t.device != device or t.dim() != 4:
         raise ValueError(f"{name}: {what} must be a {dtype} tensor [B, H, S, D] on {device}, as q is")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: {what} must have shape {tuple(shape)}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    shape, stride = t.shape, t.stride()
+    if stride[3] != 1 and shape[3] > 1:
         raise ValueError(f"{name}: {what} must be contiguous in its last dimension")
+    return shape, stride
+
+
+def _rope_out(t, shape):
+    """A contiguous tensor like t, and its strides."""
+    y = _TORCH.empty_like(t) if t.is_contiguous() else t.new_empty(tuple(shape))
+    return y, y.stride()
 
 
 def _rope_overlaps(name, ins, outs):
@@ -602,17 +610,17 @@ def _rope_overlaps(name, ins, outs):
 
 def _rope(name, inverse, q, k, pos, freqs, rot_dim, interleaved, sections, mscale, q_out, k_out, stream):
     torch = _torch()
-    dev, dt = _device_of(q, f"{name}: q"), q.dtype
+    dev, dt = _device_of(q, name), q.dtype
     code = 0 if dt is torch.bfloat16 else 1 if dt is torch.float16 else 2 if dt is torch.float32 else None
     if code is None:
         raise ValueError(f"{name}: q must be bf16, fp16 or fp32")
-    _rope_rows(q, "q", name, dt, dev)
-    B, H, S, D = q.shape
-    Hk = 0
+    qs, a = _rope_rows(q, "q", name, dt, dev)
+    B, H, S, D = qs
+    Hk, ks, b = 0, None, a
     if k is not None:
-        _rope_rows(k, "k", name, dt, dev)
-        Hk = k.shape[1]
-        if k.shape != (B, Hk, S, D) or Hk < 1:
+        ks, b = _rope_rows(k, "k", name, dt, dev)
+        Hk = ks[1]
+        if Hk < 1 or ks[0] != B or ks[2] != S or ks[3] != D:
             raise ValueError(f"{name}: k must have shape {(B, 'heads', S, D)}")
     elif k_out is not None:
         raise ValueError(f"{name}: an output for k without k")
@@ -622,7 +630,7 @@ def _rope(name, inverse, q, k, pos, freqs, rot_dim, interleaved, sections, mscal
     if rot < 0 or rot > D or rot % 2:
         raise ValueError(f"{name}: rot_dim must be even and between 0 and {D}")
     pairs = rot // 2
-    sec = (pairs,) if sections is None else tuple(int(n) for n in sections)
+    sec = (pairs,) if sections is None else tuple(map(int, sections))
     axes = len(sec)
     if not 1 <= axes <= 3 or min(sec) < 0 or sum(sec) != pairs:
         raise ValueError(f"{name}: sections must be one to three counts that sum to rot_dim / 2 = {pairs}")
@@ -631,21 +639,24 @@ def _rope(name, inverse, q, k, pos, freqs, rot_dim, interleaved, sections, mscal
                                                or (axes == 1 and pos.shape == (S,))):
         raise ValueError(f"{name}: pos must be a contiguous int32 tensor {(axes, S)} or {(B, axes, S)}"
                          + (f" or {(S,)}" if axes == 1 else "") + f" on {dev}")
-    _want(freqs, f"{name}: freqs", (pairs,), torch.float64, dev)
+    _want(freqs, "freqs", (pairs,), torch.float64, dev)
     given = q_out is not None or k_out is not None
     if q_out is None:
-        q_out = q.new_empty((B, H, S, D))
+        q_out, c = _rope_out(q, qs)
     else:
-        _rope_rows(q_out, "the output for q", name, dt, dev, (B, H, S, D))
-    if k is not None:
+        shape, c = _rope_rows(q_out, "the output for q", name, dt, dev)
+        if shape != qs:
+            raise ValueError(f"{name}: the output for q must have shape {tuple(qs)}")
+    d = c
+    if Hk:
         if k_out is None:
-            k_out = k.new_empty((B, Hk, S, D))
+            k_out, d = _rope_out(k, ks)
         else:
-            _rope_rows(k_out, "the output for k", name, dt, dev, (B, Hk, S, D))
+            shape, d = _rope_rows(k_out, "the output for k", name, dt, dev)
+            if shape != ks:
+                raise ValueError(f"{name}: the output for k must have shape {tuple(ks)}")
     if given and q.numel():
-        _rope_overlaps(name, [q] if k is None else [q, k], [q_out] if k is None else [q_out, k_out])
-    a, c = q.stride(), q_out.stride()
-    b, d = (k.stride(), k_out.stride()) if Hk else (a, c)
+        _rope_overlaps(name, [q, k] if Hk else [q], [q_out, k_out] if Hk else [q_out])
     lay = _PACK_ROPE.pack(code, B, H, Hk, D, rot, 1 if interleaved else 0, 1 if inverse else 0, S, a[0], a[1], a[2],
                           b[0], b[1], b[2], c[0], c[1], c[2], d[0], d[1], d[2], axes, sec[0],
                           sec[1] if axes > 1 else 0, sec[2] if axes > 2 else 0, axes * S if pos.dim() == 3 else 0,

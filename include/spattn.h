@@ -263,9 +263,11 @@ typedef struct {
  * empty counts as empty.  LSE is that of the modified scores, and the backward
  * takes the O and LSE of spattn_fwd_scored with the same score: with P =
  * exp(z - LSE) and dZ = P * (dP - Delta), dS = dZ * (1 - tanh^2(x / softcap)).
- * No gradient of slopes is formed.  Masked K and V rows, like padded ones, may
- * hold any finite values.  A score that modifies nothing runs the plain
- * kernels.  (Score caps, distance biases and packed documents have no
+ * No gradient of slopes is formed.  Rows that the masks leave without a pair,
+ * of Q and dO as of K and V, may like padded ones hold any finite values.
+ * Weights relative to a fixed reference reach 2^80 in rows whose LSE does not
+ * pass 55, so V has to stay below 2^46 there.  A score that modifies nothing
+ * runs the plain kernels.  (Score caps, distance biases and packed documents have no
  * counterpart in the paper.) */
 int spattn_fwd_scored(const void* q, const void* k, const void* v, spattn_plan_t plan, const spattn_score* score,
                       void* o, float* lse, void* stream);
