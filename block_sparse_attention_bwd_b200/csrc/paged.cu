@@ -172,6 +172,8 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
   float* xrow = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + C::kBars);
   uint64_t* pair_bar = reinterpret_cast<uint64_t*>(xrow + 4 * 128);  // [4]
 
+  // the join may be launched while this kernel runs; it waits for its end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // tiles and then K/V heads vary fastest: CTAs that run together read the same
   // range, and the heads of its pages side by side
   const int split = blockIdx.x / (a.q_tiles * a.kv_heads), tile_hk = blockIdx.x - split * a.q_tiles * a.kv_heads;
@@ -575,6 +577,10 @@ template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PagedArgs a, int n_seqs) {
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  // the partial rows are there when the kernel before has ended; block 0 waits in any
+  // case, so that this kernel does not end (and let the stream go on) before that one
+  auto wait_parts = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
+  if (blockIdx.x == 0) wait_parts();
   if (item >= a.tokens * a.heads) return;
   const int at = static_cast<int>(item / a.heads), head = static_cast<int>(item % a.heads);
   // the sequence of row `at`: the last one that starts at or before it, 32 ways per pass
@@ -593,6 +599,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
   const int qt = rr / kRows, row = rr % kRows;
   const int n = (tile_keys(a, seq, qt) + a.chunk - 1) / a.chunk;
   if (n <= 1) return;  // written by the tile itself
+  wait_parts();
   const int64_t tile = (static_cast<int64_t>(sq) * a.kv_heads + hk) * a.q_tiles + qt;
   const int64_t n_part = static_cast<int64_t>(n_seqs) * a.kv_heads * a.q_tiles * a.splits * a.tile_rows;
   const int64_t part0 = tile * a.splits * a.tile_rows + row;
@@ -645,8 +652,16 @@ cudaError_t launch_paged_t(const CachePages& tk, const CachePages& tv, const Pag
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
   const int64_t blocks = (a.tokens * a.heads + kJoinWarps - 1) / kJoinWarps;
-  paged_join_kernel<D><<<static_cast<unsigned>(blocks), 32 * kJoinWarps, 0, st>>>(a, n_seqs);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute behind = {};
+  behind.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  behind.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &behind;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a, n_seqs);
 }
 
 template <int D, int FORM>
