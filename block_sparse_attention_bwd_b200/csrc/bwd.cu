@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
               m &= column_bits<false, CW>(sc.q_last, sc.q_doc, col_last(qs) + CW * grp, col_doc(qs) + CW * grp, key_pos, key_doc);
           }
           // d = dP^T - Delta (from the augmented product); a = S^T -> log2 P^T
-          if constexpr (SC == kScoreCap) cap_scores<true>(a, d, sc.c);
+          if constexpr (SC == kScoreCap) cap_scores<true>(a, d, sc.c, m != 0u);
           constexpr bool kCap = SC == kScoreCap;
           if (sc.slopes) bias_scores(a, col_posf(qs) + CW * grp, static_cast<float>(key_pos), col_slope(qs)[grp]);
           add_columns(a, col_lse(qs) + CW * grp, kCap ? 1.0f : sl2);
@@ -1265,7 +1265,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
             d[i + 1] = __float_as_uint(x1);
           }
         }
-        if constexpr (kCap) cap_scores<!DELTA>(a, d, sc.c);
+        if constexpr (kCap) cap_scores<!DELTA>(a, d, sc.c, m != 0u);
         if (sc.slopes) bias_scores(a, col_posf(ks) + 64 * (st % SPS) + CW * grp, row_pos, slope);
 #pragma unroll
         for (int i = 0; i < CW; i += 2) {

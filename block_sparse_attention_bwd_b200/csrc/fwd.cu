@@ -438,7 +438,14 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
           uint32_t x[32];
           tmem_ld32(s_addr, x);
           tmem_wait_ld();
-          if constexpr (kCap) cap_scores<false>(x, x, sc.c);
+          if constexpr (kCap) {
+            // (the columns of a page that the step does not have are those of an earlier one)
+            if (pg0 + 1 >= n_cols - st * NP) {
+#pragma unroll
+              for (int i = 16; i < 32; ++i) x[i] = 0u;
+            }
+            cap_scores<false>(x, x, sc.c, bits != 0u);
+          }
           if (sc.slopes) bias_scores(x, col_posf(g) + 16 * pg0, row_pos, slope);
           if (__builtin_expect(bits != 0xFFFFFFFFu, 0)) {
 #pragma unroll

@@ -96,6 +96,7 @@ struct PagedArgs {
   int64_t n_pages;
   int heads, kv_heads, group, page16;  // page16: 16-slot pages per page
   int max_q, max_kv, q_tiles, tile_rows, splits, chunk;
+  int sms;
   float scale, cap;
   CapArgs c;
   int* err;
@@ -121,6 +122,16 @@ __device__ __forceinline__ Seq load_seq(const PagedArgs& a, int s) {
 __device__ __forceinline__ int tile_keys(const PagedArgs& a, const Seq& s, int qt) {
   const int last = min(s.nq - 1, (qt * kRows + kRows - 1) / a.group);
   return s.kv - s.nq + last + 1;
+}
+
+// Scores that a row does not see (columns from `vis` on) to zero before the cap: slots
+// behind the cache's end and columns of an earlier step may hold anything.
+__device__ __forceinline__ void clear_hidden(uint32_t (&s)[32], bool live, int vis) {
+  if (__builtin_expect(live && vis < 32, 0)) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i >= vis) s[i] = 0u;
+  }
 }
 
 // Load n 16-slot pages (lane j: page pid of step page j) into a stage, one box per
@@ -383,7 +394,8 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
           uint32_t x[32];
           tmem_ld32(s_addr, x);
           tmem_wait_ld();
-          cap_scores<false>(x, x, a.c);
+          clear_hidden(x, live, vis);
+          cap_scores<false>(x, x, a.c, live);
           if (a.slopes) {
             // - slope (distance - d_ref) = slope (column - (last - base - d_ref))
             const float b0 = -slope2 * static_cast<float>(last - base - d_ref);
@@ -438,7 +450,10 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
 #pragma unroll
         for (int pc = 0; pc < 2; ++pc) {
           if (pc * 32 < N) {
-            if constexpr (kCap) cap_scores<false>(sr[pc], sr[pc], a.c);
+            if constexpr (kCap) {
+              clear_hidden(sr[pc], live, vis - 32 * pc);
+              cap_scores<false>(sr[pc], sr[pc], a.c, live);
+            }
             if (a.slopes) {
               const float b0 = -slope * static_cast<float>(last - base);
               const uint64_t b2 = f2_pack(b0, b0), s2 = f2_pack(slope, slope);
@@ -566,17 +581,28 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
   }
 }
 
-// Join of split rows, one warp per (token, head): O = sum_s 2^(m_s - M) O_s /
+// Join of split rows, W warps per (token, head): O = sum_s 2^(m_s - M) O_s /
 // sum_s 2^(m_s - M) l_s (m_s, l_s: a split's reference and divisor; LSE has the sum
 // t_s of its unrounded weights).  M is the largest m_s + log2 t_s, not the largest
 // reference: a sum relative to a fixed reference may be 2^80 away from 1, so the
 // references alone do not tell which split counts.  No 2^(m_s - M) t_s passes 1.
-constexpr int kJoinWarps = 4;
+//
+// Bound: the latency of the partial rows' loads, four in flight per warp.  Where one
+// warp per row would leave the SMs short of warps, a block's warps share a row (one
+// token of 16 heads over 8000 keys, 63 splits: 14.4 us for the call, not 26.7; 15
+// splits: 12.3, not 16.4).  With many rows that costs more than it gives (2048 tokens
+// over 131072 keys: 2275 us, not 2193).
+constexpr int kJoinWarps = 8;
+constexpr int kJoinShare = 4;        // splits from which warps may share a row,
+constexpr int kJoinRowsPerSm = 8;    // up to as many rows per SM
 
-template <int D>
+template <int D, int W>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PagedArgs a, int n_seqs) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  static_assert(W == 1 || W == kJoinWarps, "a warp's row or a block's");
+  __shared__ float4 part_o[W > 1 ? W : 1][D / 4];
+  __shared__ float2 part_l[W > 1 ? W : 1];
+  const int lane = threadIdx.x & 31, sub = W > 1 ? threadIdx.x >> 5 : 0;
+  const int64_t item = W > 1 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   // the partial rows are there when the kernel before has ended; block 0 waits in any
   // case, so that this kernel does not end (and let the stream go on) before that one
   auto wait_parts = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
@@ -614,7 +640,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
   constexpr int E = D / 32;  // elements per lane
   float acc[E] = {}, l = 0.f, l_true = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < n; ++s) {
+  for (int s = sub; s < n; s += W) {
     const int64_t p = part0 + static_cast<int64_t>(s) * a.tile_rows;
     const float4 x = ml[p];
     const float w = x.x == -INFINITY ? 0.f : ex2(x.x - m);
@@ -631,6 +657,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
       const float2 v = *reinterpret_cast<const float2*>(src);
       acc[0] = fmaf(w, v.x, acc[0]);
       acc[1] = fmaf(w, v.y, acc[1]);
+    }
+  }
+  if constexpr (W > 1) {  // (a block's threads have the same row and come here together)
+    float* mine = reinterpret_cast<float*>(part_o[sub]);
+#pragma unroll
+    for (int i = 0; i < E; ++i) mine[lane * E + i] = acc[i];
+    if (lane == 0) part_l[sub] = make_float2(l, l_true);
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      const float* other = reinterpret_cast<const float*>(part_o[w]);
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] += other[lane * E + i];
+      l += part_l[w].x;
+      l_true += part_l[w].y;
     }
   }
   const float inv = l > 0.f ? 1.0f / l : 0.f;
@@ -651,7 +693,8 @@ cudaError_t launch_paged_t(const CachePages& tk, const CachePages& tv, const Pag
   paged_kernel<D, FORM, SMALL><<<grid, C::kThreads, C::kSmem, st>>>(tk, tv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
-  const int64_t blocks = (a.tokens * a.heads + kJoinWarps - 1) / kJoinWarps;
+  const bool share = a.splits >= kJoinShare && a.tokens * a.heads <= kJoinRowsPerSm * a.sms;
+  const int64_t blocks = share ? a.tokens * a.heads : (a.tokens * a.heads + kJoinWarps - 1) / kJoinWarps;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(32 * kJoinWarps);
@@ -661,7 +704,7 @@ cudaError_t launch_paged_t(const CachePages& tk, const CachePages& tv, const Pag
   behind.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &behind;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a, n_seqs);
+  return cudaLaunchKernelEx(&cfg, share ? paged_join_kernel<D, kJoinWarps> : paged_join_kernel<D, 1>, a, n_seqs);
 }
 
 template <int D, int FORM>
@@ -858,6 +901,7 @@ int spattn_paged_fwd(spattn_paged_t p, const spattn_paged_call* c, void* stream)
   a.tile_rows = sp.tile_rows;
   a.splits = sp.splits;
   a.chunk = sp.chunk;
+  a.sms = p->sms;
   a.scale = L.scale;
   a.cap = L.softcap;
   a.c = cap_args(L.softcap, L.scale);

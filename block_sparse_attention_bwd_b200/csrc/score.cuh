@@ -47,10 +47,12 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // folded in by the host: five FMA-pipe operations per pair more than a plain
 // score.  Beyond that it is 1 - 2 / (1 + e^2u) with two special-function
 // operations per pair, of which the softmax already spends one.  Scores well
-// inside the cap are the ordinary case; a warp decides per step.
+// inside the cap are the ordinary case; a warp decides per step.  `votes`: whether
+// this thread's scores count for that.  Those of rows without a pair do not: they
+// may be whatever stood in tensor memory, and the two branches differ in their last bits.
 constexpr float kTanhExpMax = 126.0f;  // e^2u held at 2^126: 1 - tanh^2 = 4 r (e r), r = 1 / (1 + e), stays finite
 template <bool GRAD, int N>
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], uint32_t (&d)[N], const CapArgs& c) {
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], uint32_t (&d)[N], const CapArgs& c, bool votes) {
   auto pair = [&](int i) { return f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])); };
   constexpr bool kKeep = N <= 16;  // wider rows form the squares twice rather than hold them
   uint64_t sq[kKeep ? N / 2 : 1];
@@ -63,7 +65,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], uint32_t (&d)[N], c
     f2_unpack(w, a, b);
     mx[i & 1] = fmax3(mx[i & 1], a, b);  // a NaN drops out here and keeps its NaN in either form
   }
-  if (__builtin_expect(!__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > c.w_max), 1)) {
+  if (__builtin_expect(!__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > (votes ? c.w_max : INFINITY)), 1)) {
     const uint64_t a0 = c.a[0], a1 = c.a[1], a2 = c.a[2], a3 = c.a[3], a4 = c.a[4], ng = c.ng, one = f2_pack(1.f, 1.f);
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {

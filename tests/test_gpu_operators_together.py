@@ -103,3 +103,45 @@ def test_serving_from_a_cache_matches_the_full_forward(chunks):
         assert float((o.double() - want).norm() / want.norm()) <= 2 * 2.0 ** -8
         assert float((lse - full_lse[0, :, rows].T).abs().max()) <= 2 * (2.0 ** -15 + 2.0 ** -20 * 20)
         at += c
+
+
+@pytest.mark.parametrize("n", [9, 70, 150])
+def test_results_do_not_depend_on_what_ran_before(n):
+    """Tiles with rows and columns that nothing fills (tensor memory then holds what an earlier kernel left
+    there) give the same bits after kernels that left zeros and after kernels that left large scores."""
+    gen = torch.Generator().manual_seed(n)
+
+    def problem(tokens, heads):
+        nb = -(-tokens // 64)
+        group = (np.arange(tokens) // 64).astype(np.int32)
+        plan = sp.Plan(group, group, nb, nb, np.arange(0, heads * nb * nb + 1, nb), np.tile(np.arange(nb), heads * nb),
+                       batch=1, heads=heads, head_dim=64)
+        t = [torch.randn((1, heads, tokens, 64), generator=gen).bfloat16().cuda() for _ in range(4)]
+        return plan, t
+
+    def scored(plan, q, k, v, do):
+        sc = sp.Score(softcap=20.0)
+        o, lse = sp.spattn_fwd_scored(q, k, v, plan, sc)
+        return (o, lse) + tuple(sp.spattn_bwd_scored(q, k, v, o, lse, do, plan, sc))
+
+    def paged(cap, tokens, cached, heads, q, kv):
+        p = sp.PagedPlan(heads=heads, kv_heads=1, head_dim=64, page_slots=16, max_seqs=1, max_q=tokens, max_kv=cached,
+                         softcap=cap)
+        pages = -(-cached // 16)
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+        return sp.spattn_paged_fwd(q, kv[:pages], kv[:pages], i32([list(range(pages))]), i32([0, tokens]), i32([cached]), p)
+
+    plan, x = problem(n, 2)
+    wide, y = problem(1024, 40)
+    kv = torch.randn((128, 16, 1, 64), generator=gen).bfloat16().cuda()
+    one = torch.randn((1, 5, 64), generator=gen).bfloat16().cuda()
+    many = torch.randn((32, 128, 64), generator=gen).bfloat16().cuda()
+    got = []
+    for size in (0.0, 1000.0):
+        for f in (lambda: scored(plan, *x), lambda: paged(20.0, 1, n, 5, one, kv), lambda: paged(70.0, 1, n, 5, one, kv)):
+            scored(wide, y[0] * size, *y[1:])
+            paged(20.0, 32, 2048, 128, many * size, kv)
+            got.append(f())
+    for a, b in zip(got[:3], got[3:]):
+        for u, w in zip(a, b):
+            assert torch.equal(u, w)
