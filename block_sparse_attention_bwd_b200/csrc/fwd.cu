@@ -29,8 +29,8 @@
 // Scored forms (spattn_score): the same pipeline with 10 warps, two threads per
 // row; see kFwdThreads and score.cuh.  Bound: the row threads' instructions
 // (the cap's polynomial, the bias, masks) beside the products.  12289 causal
-// tokens with a prefix, 16 heads, D = 128: 837 us with masks alone, 980 with a cap
-// of 50 as well, 701 unmodified; 16384 tokens of packed documents, 16 heads: 201 us.
+// tokens with a prefix, 16 heads, D = 128: 815 us with masks alone, 960 with a cap
+// of 50 as well, 701 unmodified; 16384 tokens of packed documents, 16 heads: 200 us.
 #include "kernels.cuh"
 #include "score.cuh"
 #include "tile.cuh"
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
             col_doc(g)[lane + 32 * h] = cdoc[h];
             col_posf(g)[lane + 32 * h] = static_cast<float>(cpos[h]);
           }
-          const int4 rg = range_join(column_range(clive[0], cpos[0], cdoc[0]), column_range(clive[1], cpos[1], cdoc[1]));
+          const int4 rg = columns_range(clive, cpos, cdoc);
           if (lane == 0) col_rng[g % R] = rg;
           load_cols(st + 1, pid_next);
           __syncwarp();

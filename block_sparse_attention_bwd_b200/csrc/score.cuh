@@ -176,8 +176,14 @@ __device__ __forceinline__ int4 column_range(bool live, int pos, int doc) {
   return make_int4(__reduce_min_sync(0xffffffffu, live ? pos : kHigh), __reduce_max_sync(0xffffffffu, live ? pos : kLow),
                    __reduce_min_sync(0xffffffffu, live ? doc : kHigh), __reduce_max_sync(0xffffffffu, live ? doc : kLow));
 }
-__device__ __forceinline__ int4 range_join(int4 a, int4 b) {
-  return make_int4(min(a.x, b.x), max(a.y, b.y), min(a.z, b.z), max(a.w, b.w));
+// The same of two columns per lane.  (All four reductions at once: leaving out those that
+// no mask asks for put branches between them and cost 2% on 12289 tokens.)
+__device__ __forceinline__ int4 columns_range(const bool (&live)[2], const int (&pos)[2], const int (&doc)[2]) {
+  constexpr int kLow = static_cast<int>(0x80000000), kHigh = 0x7FFFFFFF;
+  return make_int4(__reduce_min_sync(0xffffffffu, min(live[0] ? pos[0] : kHigh, live[1] ? pos[1] : kHigh)),
+                   __reduce_max_sync(0xffffffffu, max(live[0] ? pos[0] : kLow, live[1] ? pos[1] : kLow)),
+                   __reduce_min_sync(0xffffffffu, min(live[0] ? doc[0] : kHigh, live[1] ? doc[1] : kHigh)),
+                   __reduce_max_sync(0xffffffffu, max(live[0] ? doc[0] : kLow, live[1] ? doc[1] : kLow)));
 }
 
 // Range of a warp's rows: of last positions (query rows) or positions (key rows),
