@@ -22,8 +22,8 @@
 // (1 - tanh^2), four warp groups of 16 columns, -LSE, positions and documents of the
 // columns in lines beside the stages.  Bound: the row threads' instructions and the
 // latency of a step (tensor pipe busy 0.40 to 0.45).  12289 causal tokens with a
-// prefix and a cap of 50, 16 heads over 4, D = 128: dK / dV 1724 us and dQ 1461
-// (masks alone 1473 and 1053, unmodified 1238 and 906).
+// prefix and a cap of 50, 16 heads over 4, D = 128: dK / dV 1695 us and dQ 1435
+// (masks alone 1455 and 1040, unmodified 1240 and 905).
 #include <algorithm>
 #include <type_traits>
 

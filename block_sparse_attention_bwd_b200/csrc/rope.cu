@@ -9,7 +9,10 @@
 // less its nearest integer), which keeps 1e-7 rad at position 2^31; only the
 // fraction is rounded to fp32.  Rotation is fp32, rounded once on the store.
 //
-// Bound: memory (each element read and written once, 3 flops per element).
+// Bound: memory (each element read and written once, 3 flops per element): 75600
+// slots of 40 + 40 heads, D = 128, bf16, three axes take 490 us (6.3 TB/s); a row
+// whose alignment leaves single 16-bit elements runs at 2.4 TB/s.  64 slots of
+// 32 + 8 heads take 4.2 us, a launch and one round of loads.
 // A thread computes the sines of its pairs once and walks over the heads of
 // its slot, Q's heads and then K's, so that the fp64 angle costs little per
 // byte; two to four heads are in flight per thread to cover DRAM latency.  Input and

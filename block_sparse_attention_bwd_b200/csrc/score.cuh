@@ -176,8 +176,10 @@ __device__ __forceinline__ int4 column_range(bool live, int pos, int doc) {
   return make_int4(__reduce_min_sync(0xffffffffu, live ? pos : kHigh), __reduce_max_sync(0xffffffffu, live ? pos : kLow),
                    __reduce_min_sync(0xffffffffu, live ? doc : kHigh), __reduce_max_sync(0xffffffffu, live ? doc : kLow));
 }
-// The same of two columns per lane.  (All four reductions at once: leaving out those that
-// no mask asks for put branches between them and cost 2% on 12289 tokens.)
+// The same of two columns per lane, which halves the reductions.  (Leaving out
+// those that no mask asks for puts branches between them: 2% slower on 12289
+// tokens; so are ranges of 64 columns in the dQ kernel, 573 -> 587 us on the video
+// layout, where more steps then count as mixed.)
 __device__ __forceinline__ int4 columns_range(const bool (&live)[2], const int (&pos)[2], const int (&doc)[2]) {
   constexpr int kLow = static_cast<int>(0x80000000), kHigh = 0x7FFFFFFF;
   return make_int4(__reduce_min_sync(0xffffffffu, min(live[0] ? pos[0] : kHigh, live[1] ? pos[1] : kHigh)),

@@ -267,7 +267,8 @@ typedef struct {
  * of Q and dO as of K and V, may like padded ones hold any finite values.
  * Weights relative to a fixed reference reach 2^80 in rows whose LSE does not
  * pass 55, so V has to stay below 2^46 there.  A score that modifies nothing
- * runs the plain kernels.  (Score caps, distance biases and packed documents have no
+ * runs the plain kernels.  One plan serves one stream at a time, replays of
+ * captured graphs included.  (Score caps, distance biases and packed documents have no
  * counterpart in the paper.) */
 int spattn_fwd_scored(const void* q, const void* k, const void* v, spattn_plan_t plan, const spattn_score* score,
                       void* o, float* lse, void* stream);
