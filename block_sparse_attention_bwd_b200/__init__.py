@@ -567,12 +567,6 @@ def rope_freqs(sections, base=10000.0, scaling=None, factor=1.0, original_slots=
     return torch.from_numpy(np.concatenate(ladders) if ladders else np.zeros(0)).to(device), mscale
 
 
-def _rope_span(t):
-    """[first, end) byte addresses that a [B, H, S, D] tensor's rows touch."""
-    (b, h, n, d), (x, y, z, _), at = t.shape, t.stride(), t.data_ptr()
-    return at, at + ((b - 1) * x + (h - 1) * y + (n - 1) * z + d) * t.element_size()
-
-
 def _rope_rows(t, what, name, dtype, device):
     """Shape and strides of a [B, H, S, D] tensor of a rope call, checked."""
     if not isinstance(t, _TORCH.Tensor) or t.dtype is not dtype or t.device != device or t.dim() != 4:
@@ -589,20 +583,25 @@ def _rope_out(t, shape):
     return y, y.stride()
 
 
-def _rope_overlaps(name, ins, outs):
-    """Refuses outputs that overlap an input without being in place of it."""
-    for y in outs:
-        if 0 in y.stride() and any(n > 1 and st == 0 for n, st in zip(y.shape, y.stride())):
+def _rope_overlaps(name, ins, outs, size):
+    """Refuses outputs that overlap an input without being in place of it.
+
+    ``ins``, ``outs``: (address, shape, strides) of the [B, H, S, D] tensors; ``size``: bytes of an element.
+    """
+    spans = []  # [first, end) byte addresses that the rows touch
+    for at, (b, h, n, d), (x, y, z, _) in ins + outs:
+        spans.append((at, at + ((b - 1) * x + (h - 1) * y + (n - 1) * z + d) * size))
+    for _, shape, stride in outs:
+        if 0 in stride and any(n > 1 and st == 0 for n, st in zip(shape, stride)):
             raise ValueError(f"{name}: an output has elements that share an address")
-    if len(outs) == 2 and outs[0].data_ptr() == outs[1].data_ptr():
+    if len(outs) == 2 and outs[0][0] == outs[1][0]:
         raise ValueError(f"{name}: the two outputs share an address")
-    spans = [_rope_span(x) for x in ins]
-    meet = [(i, j) for i, y in enumerate(outs) for (a0, a1) in (_rope_span(y),)
-            for j, (b0, b1) in enumerate(spans) if a0 < b1 and b0 < a1]
+    n = len(ins)
+    meet = [(i, j) for i in range(n) for j in range(n)
+            if spans[n + i][0] < spans[j][1] and spans[j][0] < spans[n + i][1]]
     if not meet:
         return
-    own = [y.data_ptr() == x.data_ptr() and all(a == b or n == 1 for a, b, n in zip(x.stride(), y.stride(), x.shape))
-           for x, y in zip(ins, outs)]
+    own = [y[0] == x[0] and all(a == b or m == 1 for a, b, m in zip(x[2], y[2], x[1])) for x, y in zip(ins, outs)]
     # views of one packed buffer interleave; both in place is the case that is allowed
     if any(not (own[i] and (i == j or own[j])) for i, j in meet):
         raise ValueError(f"{name}: an output overlaps an input without being in place of it")
@@ -655,14 +654,16 @@ def _rope(name, inverse, q, k, pos, freqs, rot_dim, interleaved, sections, mscal
             shape, d = _rope_rows(k_out, "the output for k", name, dt, dev)
             if shape != ks:
                 raise ValueError(f"{name}: the output for k must have shape {tuple(ks)}")
-    if given and q.numel():
-        _rope_overlaps(name, [q, k] if Hk else [q], [q_out, k_out] if Hk else [q_out])
+    q_at, o_at = q.data_ptr(), q_out.data_ptr()
+    k_at, p_at = (k.data_ptr(), k_out.data_ptr()) if Hk else (None, None)
+    if given and B and S:
+        _rope_overlaps(name, [(q_at, qs, a), (k_at, ks, b)] if Hk else [(q_at, qs, a)],
+                       [(o_at, qs, c), (p_at, ks, d)] if Hk else [(o_at, qs, c)], 4 if code == 2 else 2)
     lay = _PACK_ROPE.pack(code, B, H, Hk, D, rot, 1 if interleaved else 0, 1 if inverse else 0, S, a[0], a[1], a[2],
                           b[0], b[1], b[2], c[0], c[1], c[2], d[0], d[1], d[2], axes, sec[0],
                           sec[1] if axes > 1 else 0, sec[2] if axes > 2 else 0, axes * S if pos.dim() == 3 else 0,
                           mscale)
-    args = (lay, q.data_ptr(), k.data_ptr() if Hk else None, pos.data_ptr(), freqs.data_ptr(), q_out.data_ptr(),
-            k_out.data_ptr() if Hk else None, _raw_stream(stream, dev))
+    args = (lay, q_at, k_at, pos.data_ptr(), freqs.data_ptr(), o_at, p_at, _raw_stream(stream, dev))
     if torch.cuda.current_device() == dev.index:
         status = _lib().spattn_rope(*args)
     else:
