@@ -255,7 +255,8 @@ __device__ __forceinline__ uint32_t column_bits(bool use_pos, bool use_doc, cons
 // long.  That needs a reference of the weights that is known beforehand: with a
 // running maximum the two threads would exchange their halves' maxima every step,
 // which cost more than the second thread gave (943 us -> 1421 on 12289 causal
-// tokens x 16 heads).  They meet once, at the end.
+// tokens x 16 heads).  They meet once, at the end.  Four threads per row would have 56
+// registers each and were slower again (981 -> 1235 us with a cap and a prefix).
 struct SoftRow {
   float l = 0.f;   // sum of this thread's weights
   float lr = 0.f;  // the same of the weights rounded to bf16
