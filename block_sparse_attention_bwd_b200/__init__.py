@@ -6,6 +6,10 @@ runs in the CUDA kernels of ``libspattn.so`` behind the C ABI declared in
 stream.  There is no fallback: if the library is missing, importing this
 package raises.
 
+Calls launch on ``stream`` (by default the current one), and the tensors that
+they make themselves come from that stream's memory pool: a program that reads
+them on another stream orders the two and keeps the tensors until it has.
+
 Names follow the C ABI: :class:`Plan` wraps ``spattn_plan``;
 :func:`spattn_fwd`, :func:`spattn_bwd` and :func:`spattn_check` call the
 entry points of the same names.
@@ -13,6 +17,7 @@ entry points of the same names.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -302,6 +307,25 @@ def _stream_handle(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _making_on(stream, t):
+    """The context in which a call on ``stream`` makes its own tensors (results and workspaces), on the device of t.
+
+    Memory from the current stream's pool may have just been freed there with its last kernels still
+    running, and nothing orders those before a launch on another stream: the given stream's own pool it is.
+    """
+    torch = _torch()
+    if stream is None or not isinstance(t, torch.Tensor) or not t.is_cuda:  # (no CUDA tensor: refused further on)
+        return _HERE
+    if stream.cuda_stream == _CURRENT_RAW_STREAM(t.device.index):
+        return _HERE
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=t.device)
+    return torch.cuda.stream(stream)
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
@@ -323,10 +347,11 @@ def spattn_fwd(q, k, v, plan: Plan, o=None, lse=None, stream=None):
     _need(q, "q", qs, torch.bfloat16)
     _need(k, "k", ks, torch.bfloat16)
     _need(v, "v", ks, torch.bfloat16)
-    if o is None:
-        o = torch.empty(qs, dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty(qs[:3], dtype=torch.float32, device=q.device)
+    with _making_on(stream, q):
+        if o is None:
+            o = torch.empty(qs, dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty(qs[:3], dtype=torch.float32, device=q.device)
     _need(o, "o", qs, torch.bfloat16)
     _need(lse, "lse", qs[:3], torch.float32)
     _check(_lib().spattn_fwd(_ptr(q), _ptr(k), _ptr(v), plan.handle, _ptr(o), _ptr(lse), _stream_handle(stream)),
@@ -342,8 +367,9 @@ def quantize_fp8(x, stream=None):
     if x.dim() != 4 or x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("quantize_fp8: x must be a contiguous CUDA bf16 tensor [B, H, S, D]")
     B, H, S, D = x.shape
-    x8 = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-    descale = torch.empty((B, H), dtype=torch.float32, device=x.device)
+    with _making_on(stream, x):
+        x8 = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        descale = torch.empty((B, H), dtype=torch.float32, device=x.device)
     _check(_lib().spattn_quantize_fp8(_ptr(x), B * H, S, D, _ptr(x8), _ptr(descale), _stream_handle(stream)),
            "spattn_quantize_fp8")
     return x8, descale
@@ -360,10 +386,11 @@ def spattn_fwd_fp8(q8, k8, q_descale, k_descale, v, plan: Plan, o=None, lse=None
     _need(v, "v", ks, torch.bfloat16)
     _need(q_descale, "q_descale", qs[:2], torch.float32)
     _need(k_descale, "k_descale", ks[:2], torch.float32)
-    if o is None:
-        o = torch.empty(qs, dtype=torch.bfloat16, device=q8.device)
-    if lse is None:
-        lse = torch.empty(qs[:3], dtype=torch.float32, device=q8.device)
+    with _making_on(stream, q8):
+        if o is None:
+            o = torch.empty(qs, dtype=torch.bfloat16, device=q8.device)
+        if lse is None:
+            lse = torch.empty(qs[:3], dtype=torch.float32, device=q8.device)
     _need(o, "o", qs, torch.bfloat16)
     _need(lse, "lse", qs[:3], torch.float32)
     _check(_lib().spattn_fwd_fp8(_ptr(q8), _ptr(k8), _ptr(q_descale), _ptr(k_descale), _ptr(v), plan.handle, _ptr(o),
@@ -380,9 +407,10 @@ def spattn_bwd(q, k, v, o, lse, do, plan: Plan, dq=None, dk=None, dv=None, strea
     for t, nm, sh in ((q, "q", qs), (k, "k", ks), (v, "v", ks), (o, "o", qs), (do, "do", qs)):
         _need(t, nm, sh, torch.bfloat16)
     _need(lse, "lse", qs[:3], torch.float32)
-    dq = torch.empty(qs, dtype=torch.bfloat16, device=q.device) if dq is None else dq
-    dk = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dk is None else dk
-    dv = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dv is None else dv
+    with _making_on(stream, q):
+        dq = torch.empty(qs, dtype=torch.bfloat16, device=q.device) if dq is None else dq
+        dk = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dk is None else dk
+        dv = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dv is None else dv
     _need(dq, "dq", qs, torch.bfloat16)
     _need(dk, "dk", ks, torch.bfloat16)
     _need(dv, "dv", ks, torch.bfloat16)
@@ -483,14 +511,15 @@ def spattn_fwd_scored(q, k, v, plan: Plan, score: Score, o=None, lse=None, strea
     _want(k, "k", ks, bf16, dev)
     _want(v, "v", ks, bf16, dev)
     sc = score._packed(plan, dev)
-    if o is None:
-        o = torch.empty_like(q)
-    else:
-        _want(o, "o", qs, bf16, dev)
-    if lse is None:
-        lse = q.new_empty(qs[:3], dtype=torch.float32)
-    else:
-        _want(lse, "lse", qs[:3], torch.float32, dev)
+    with _making_on(stream, q):
+        if o is None:
+            o = torch.empty_like(q)
+        else:
+            _want(o, "o", qs, bf16, dev)
+        if lse is None:
+            lse = q.new_empty(qs[:3], dtype=torch.float32)
+        else:
+            _want(lse, "lse", qs[:3], torch.float32, dev)
     _check(_lib().spattn_fwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), plan.handle, sc,
                                     o.data_ptr(), lse.data_ptr(), _raw_stream(stream, dev)), "spattn_fwd_scored")
     return o, lse
@@ -509,18 +538,19 @@ def spattn_bwd_scored(q, k, v, o, lse, do, plan: Plan, score: Score, dq=None, dk
     _want(do, "do", qs, bf16, dev)
     _want(lse, "lse", qs[:3], torch.float32, dev)
     sc = score._packed(plan, dev)
-    if dq is None:
-        dq = torch.empty_like(q)
-    else:
-        _want(dq, "dq", qs, bf16, dev)
-    if dk is None:
-        dk = torch.empty_like(k)
-    else:
-        _want(dk, "dk", ks, bf16, dev)
-    if dv is None:
-        dv = torch.empty_like(k)
-    else:
-        _want(dv, "dv", ks, bf16, dev)
+    with _making_on(stream, q):
+        if dq is None:
+            dq = torch.empty_like(q)
+        else:
+            _want(dq, "dq", qs, bf16, dev)
+        if dk is None:
+            dk = torch.empty_like(k)
+        else:
+            _want(dk, "dk", ks, bf16, dev)
+        if dv is None:
+            dv = torch.empty_like(k)
+        else:
+            _want(dv, "dv", ks, bf16, dev)
     _check(_lib().spattn_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
                                     do.data_ptr(), plan.handle, sc, dq.data_ptr(), dk.data_ptr(),
                                     dv.data_ptr(), _raw_stream(stream, dev)), "spattn_bwd_scored")
@@ -640,20 +670,21 @@ def _rope(name, inverse, q, k, pos, freqs, rot_dim, interleaved, sections, mscal
                          + (f" or {(S,)}" if axes == 1 else "") + f" on {dev}")
     _want(freqs, "freqs", (pairs,), torch.float64, dev)
     given = q_out is not None or k_out is not None
-    if q_out is None:
-        q_out, c = _rope_out(q, qs)
-    else:
-        shape, c = _rope_rows(q_out, "the output for q", name, dt, dev)
-        if shape != qs:
-            raise ValueError(f"{name}: the output for q must have shape {tuple(qs)}")
-    d = c
-    if Hk:
-        if k_out is None:
-            k_out, d = _rope_out(k, ks)
+    with _making_on(stream, q):
+        if q_out is None:
+            q_out, c = _rope_out(q, qs)
         else:
-            shape, d = _rope_rows(k_out, "the output for k", name, dt, dev)
-            if shape != ks:
-                raise ValueError(f"{name}: the output for k must have shape {tuple(ks)}")
+            shape, c = _rope_rows(q_out, "the output for q", name, dt, dev)
+            if shape != qs:
+                raise ValueError(f"{name}: the output for q must have shape {tuple(qs)}")
+        d = c
+        if Hk:
+            if k_out is None:
+                k_out, d = _rope_out(k, ks)
+            else:
+                shape, d = _rope_rows(k_out, "the output for k", name, dt, dev)
+                if shape != ks:
+                    raise ValueError(f"{name}: the output for k must have shape {tuple(ks)}")
     q_at, o_at = q.data_ptr(), q_out.data_ptr()
     k_at, p_at = (k.data_ptr(), k_out.data_ptr()) if Hk else (None, None)
     if given and B and S:
@@ -777,22 +808,20 @@ def spattn_paged_fwd(q, k_cache, v_cache, page_table, q_start, kv_len, paged: Pa
     slopes = paged.slopes
     if slopes is not None:
         _want(slopes, "slopes", (H,), torch.float32, dev)
-    if o is None:
-        o = q.new_empty((T, H, D))
-    else:
-        _want(o, "o", (T, H, D), bf16, dev)
-    if lse is None:
-        lse = q.new_empty((T, H), dtype=torch.float32)
-    else:
-        _want(lse, "lse", (T, H), torch.float32, dev)
     need = paged.workspace_bytes(n)
-    if workspace is None:
-        if need:
+    with _making_on(stream, q):
+        if o is None:
+            o = q.new_empty((T, H, D))
+        else:
+            _want(o, "o", (T, H, D), bf16, dev)
+        if lse is None:
+            lse = q.new_empty((T, H), dtype=torch.float32)
+        else:
+            _want(lse, "lse", (T, H), torch.float32, dev)
+        if workspace is None and need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            if stream is not None:
-                workspace.record_stream(stream)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or workspace.dtype is not torch.uint8 \
-            or not workspace.is_contiguous():
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or workspace.device != dev
+                                  or workspace.dtype is not torch.uint8 or not workspace.is_contiguous()):
         raise ValueError(f"workspace: expected a contiguous uint8 tensor on {dev}")
     # (the stride of a single token or head means nothing)
     c = _PACK_PAGED.pack(q.data_ptr(), q.stride(0) if T > 1 else 0, q.stride(1) if H > 1 else 0, T,
