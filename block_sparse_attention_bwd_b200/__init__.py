@@ -613,28 +613,93 @@ def _rope_out(t, shape):
     return y, y.stride()
 
 
+def _sums_reach(terms, lo, hi):
+    """Whether some sum of k_i stride_i, k_i from first_i to last_i, lies in [lo, hi].
+
+    ``terms``: (stride, first, last), those of one stride added up.  With the largest strides first, few k_i of each leave a sum that the
+    smaller ones can still bring there, wherever strides nest as a tensor's do.  True without an
+    answer after some thousand of them.
+    """
+    ranges = {}
+    for st, first, last in terms:
+        if st:
+            a, b = ranges.get(st, (0, 0))
+            ranges[st] = (a + first, b + last)
+    terms = [(st, *ranges[st]) for st in sorted(ranges, reverse=True)]
+    least, most = [0], [0]  # of the sums of the last terms
+    for st, first, last in reversed(terms):
+        least.append(least[-1] + st * first)
+        most.append(most[-1] + st * last)
+    left = 4000
+
+    def search(i, lo, hi):
+        nonlocal left
+        if i == len(terms):
+            return lo <= 0 <= hi
+        st, first, last = terms[i]
+        rest = len(terms) - 1 - i
+        for k in range(max(first, -((most[rest] - lo) // st)), min(last, (hi - least[rest]) // st) + 1):
+            left -= 1
+            if left < 0 or search(i + 1, lo - k * st, hi - k * st):
+                return True
+        return False
+
+    return search(0, lo, hi)
+
+
+def _view_repeats(shape, stride):
+    """Whether two elements of a [B, H, S, D] view share an address."""
+    (b, h, n, d), (x, y, z, _) = shape, stride
+    e, f = (n - 1) * z + d, (h - 1) * y + d  # what the rows of a head span, and those of a slot
+    if (n == 1 or z >= d) and (h == 1 or y >= e) and (b == 1 or x >= e + f - d):
+        return False  # every stride passes over what the smaller ones reach, heads in order ...
+    if (h == 1 or y >= d) and (n == 1 or z >= f) and (b == 1 or x >= e + f - d):
+        return False  # ... or slots
+    dims = sorted(((st, m) for st, m in ((x, b), (y, h), (z, n)) if m > 1), reverse=True)
+    return any(_sums_reach([(dims[i][0], 1, dims[i][1] - 1)] + [(st, 1 - n, n - 1) for st, n in dims[i + 1:]], 1 - d, d - 1)
+               for i in range(len(dims)))
+
+
+def _views_meet(x, y, size):
+    """Whether two [B, H, S, D] views (address, shape, strides) share an address."""
+    (at, (bx, hx, sx, d), (b0, h0, s0, _)), (to, (by, hy, sy, _), (b1, h1, s1, _)) = x, y
+    gap = (to - at) // size
+    # Parts of one packed buffer: both repeat with one period, in which they lie apart (slots of a
+    # [B, S, heads, D] one, rows of a [B, H, S, 2 D] one).
+    if s0 == s1 and b0 == b1 and s0 > 0 and b0 % s0 == 0:
+        if h0 % s0 == 0 and h1 % s0 == 0:
+            if d <= gap % s0 <= s0 - d:
+                return False
+        elif (hx - 1) * h0 + d <= gap % s0 <= s0 - (hy - 1) * h1 - d:
+            return False
+    return _sums_reach([(b0, 0, bx - 1), (h0, 0, hx - 1), (s0, 0, sx - 1), (b1, 1 - by, 0), (h1, 1 - hy, 0), (s1, 1 - sy, 0)],
+                       gap + 1 - d, gap + d - 1)
+
+
 def _rope_overlaps(name, ins, outs, size):
-    """Refuses outputs that overlap an input without being in place of it.
+    """Refuses outputs that share an address with each other or, without being in place of it, with an input.
 
     ``ins``, ``outs``: (address, shape, strides) of the [B, H, S, D] tensors; ``size``: bytes of an element.
     """
     spans = []  # [first, end) byte addresses that the rows touch
     for at, (b, h, n, d), (x, y, z, _) in ins + outs:
         spans.append((at, at + ((b - 1) * x + (h - 1) * y + (n - 1) * z + d) * size))
-    for _, shape, stride in outs:
-        if 0 in stride and any(n > 1 and st == 0 for n, st in zip(shape, stride)):
-            raise ValueError(f"{name}: an output has elements that share an address")
-    if len(outs) == 2 and outs[0][0] == outs[1][0]:
-        raise ValueError(f"{name}: the two outputs share an address")
     n = len(ins)
-    meet = [(i, j) for i in range(n) for j in range(n)
-            if spans[n + i][0] < spans[j][1] and spans[j][0] < spans[n + i][1]]
-    if not meet:
-        return
-    own = [y[0] == x[0] and all(a == b or m == 1 for a, b, m in zip(x[2], y[2], x[1])) for x, y in zip(ins, outs)]
-    # views of one packed buffer interleave; both in place is the case that is allowed
-    if any(not (own[i] and (i == j or own[j])) for i, j in meet):
-        raise ValueError(f"{name}: an output overlaps an input without being in place of it")
+    for _, shape, stride in outs:
+        if _view_repeats(shape, stride):
+            raise ValueError(f"{name}: an output has elements that share an address")
+    if n == 2 and spans[2][0] < spans[3][1] and spans[3][0] < spans[2][1] and _views_meet(outs[0], outs[1], size):
+        raise ValueError(f"{name}: the two outputs share an address")
+    for i in range(n):
+        first, end = spans[n + i]
+        for j in range(n):
+            if first >= spans[j][1] or spans[j][0] >= end:
+                continue
+            x, y = ins[j], outs[i]
+            if i == j and y[0] == x[0] and all(a == b or m == 1 for a, b, m in zip(x[2], y[2], x[1])):
+                continue  # in place: an element is read and written by one thread
+            if _views_meet(y, x, size):
+                raise ValueError(f"{name}: an output overlaps an input without being in place of it")
 
 
 def _rope(name, inverse, q, k, pos, freqs, rot_dim, interleaved, sections, mscale, q_out, k_out, stream):
@@ -709,8 +774,8 @@ def rope(q, k, pos, freqs, *, rot_dim=None, interleaved=False, sections=None, ms
     """Rotary positions of Q [B,H,S,D] and K [B,Hk,S,D] (or None) in one launch; returns both.
 
     Inputs and outputs may be strided views (bf16, fp16 or fp32; the last dimension
-    contiguous), an output may be its input; new outputs are contiguous, as
-    spattn_fwd wants them.  ``pos``: int32 [S], [axes, S] or [B, axes, S];
+    contiguous), an output may be its input, and views of one buffer are told
+    apart by their addresses; new outputs are contiguous, as spattn_fwd wants them.  ``pos``: int32 [S], [axes, S] or [B, axes, S];
     ``sections``: pairs per position axis (one axis by default); ``freqs``, ``mscale``:
     see :func:`rope_freqs`.  ``interleaved`` pairs elements 2p and 2p + 1, else p
     and p + rot_dim / 2; elements from ``rot_dim`` on are copied.
