@@ -434,11 +434,11 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
         }
       };
       // Augmented row of a column: -LSE / scale for Q (a column that attends
-      // nothing, LSE = -inf, is masked everywhere, like a dead one: zeros), or
-      // -Delta for dO.
+      // nothing, LSE = -inf, is masked everywhere, like a dead one: zeros; a NaN stays),
+      // or -Delta for dO.
       auto term_row = [&](float t, bool okr) {
         const float x = is_q ? t * inv_scale : t;
-        return aug_row(okr && isfinite(x) ? x : 0.f);
+        return aug_row(okr && fabsf(x) != INFINITY ? x : 0.f);
       };
       int pid = page_id(0), pid_next = page_id(1);
       int cbh = col_bh(0), cbh_next = col_bh(1);

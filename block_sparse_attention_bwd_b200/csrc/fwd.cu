@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
       const bool owned = code != 15u && row < 16 * wk.n_own;
       const int64_t slot = owned ? pref_slot(wk.own_page(row >> 4), row & 15) : 0;
       const bool write = owned && slot < q_slots;
-      const bool empty = !(l > 0.f);
+      const bool empty = l == 0.f;  // (a NaN score is no empty row: its O and LSE are NaN)
       const float inv = empty ? 0.f : 1.0f / l;
       __nv_bfloat16* dst = out_o + (static_cast<int64_t>(wk.bh) * q_slots + slot) * D + grp * (D / 2);
 #pragma unroll
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kFwdThreads<SC>, 2)
       const bool owned = code != 15u && row < 16 * wk.n_own;
       const int64_t slot = owned ? pref_slot(wk.own_page(row >> 4), row & 15) : 0;
       const bool write = owned && slot < q_slots;
-      const bool empty = !(l > 0.f);
+      const bool empty = l == 0.f;  // (a NaN score is no empty row: its O and LSE are NaN)
       const float inv = empty ? 0.f : 1.0f / l;
       __nv_bfloat16* dst = out_o + (static_cast<int64_t>(wk.bh) * q_slots + slot) * D;
 #pragma unroll

@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(PagedCfg<D, FORM, SMALL>::kThreads, 2)
       const int64_t tile = (static_cast<int64_t>(sq) * a.kv_heads + hk) * a.q_tiles + qt;
       const int64_t n_part = static_cast<int64_t>(gridDim.y) * a.kv_heads * a.q_tiles * a.splits * a.tile_rows;
       const int64_t part = (tile * a.splits + split) * a.tile_rows + row;
-      const bool empty = !(l > 0.f);
+      const bool empty = l == 0.f;  // (a NaN score is no empty row: its O and LSE are NaN)
       const float inv = empty ? 0.f : 1.0f / l;
       constexpr int kOut = kFixed ? D / 2 : D;  // columns of O that this thread writes
       const int col = grp * kOut;
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
   float m = -INFINITY;
   for (int s = lane; s < n; s += 32) {
     const float4 x = ml[part0 + static_cast<int64_t>(s) * a.tile_rows];
-    if (x.x > -INFINITY) m = fmaxf(m, x.x + lg2(x.y));
+    if (x.z != 0.f) m = fmaxf(m, x.x + lg2(x.y));  // (a NaN drops out here and comes back with its weight below)
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
   for (int s = sub; s < n; s += W) {
     const int64_t p = part0 + static_cast<int64_t>(s) * a.tile_rows;
     const float4 x = ml[p];
-    const float w = x.x == -INFINITY ? 0.f : ex2(x.x - m);
+    const float w = x.z == 0.f ? 0.f : ex2(x.x - m);
     l_true = fmaf(w, x.y, l_true);
     l = fmaf(w, x.z, l);
     const float* src = a.part + p * D + lane * E;
@@ -675,12 +675,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
       l_true += part_l[w].y;
     }
   }
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
   const int64_t out = static_cast<int64_t>(seq.t0 + tok) * a.heads + head;
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D + lane * E);
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) dst[i] = pack_bf16(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-  if (a.lse && lane == 0) a.lse[out] = l > 0.f ? (m + lg2(l_true)) * kLn2 : -INFINITY;
+  if (a.lse && lane == 0) a.lse[out] = l == 0.f ? -INFINITY : (m + lg2(l_true)) * kLn2;
 }
 
 template <int D, int FORM, bool SMALL>

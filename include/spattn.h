@@ -37,7 +37,8 @@
  *   Every pointer must be 16-byte aligned.  head_dim is 64 or 128.
  *   Padded input rows may hold any finite values; outputs on padded or
  *   attention-free query rows are O = 0, LSE = -inf, dQ = 0, and on padded
- *   key rows dK = dV = 0.
+ *   key rows dK = dV = 0.  A row with a NaN among its scores is no empty row:
+ *   its O and LSE are NaN, and so are the gradients that it has a part in.
  *
  * Errors: every call returns an SPATTN_* status; nothing throws across the
  * ABI.  fwd/bwd are asynchronous on `stream` (a cudaStream_t, NULL = the
