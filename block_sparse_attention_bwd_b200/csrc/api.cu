@@ -285,12 +285,13 @@ int run_bwd(const void* q, const void* k, const void* v, const void* o, const fl
     return launch_delta(D, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), plan->d_delta,
                         bh * plan->q.slots, s);
   });
-  if (sc && e == cudaSuccess && (!plan->wq.ordered || plan->wq.n_short > 0)) {
+  if (sc && e == cudaSuccess) {
     TileArgs t = tile_args(plan, plan->wq, plan->q.slots, plan->k.slots);
     t.beside = !plan->profiling;
     e = timed(plan, SPATTN_K_DELTA, s, [&] {
-      return launch_delta_exact(D, static_cast<const __nv_bfloat16*>(q), tdo, tk, tv, t, sc, plan->wq.n_short,
-                                kShortEntries, lse, plan->d_delta, s);
+      return launch_few_keys(D, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+                             static_cast<const __nv_bfloat16*>(v), static_cast<const __nv_bfloat16*>(d_o), t, *sc, lse,
+                             plan->d_delta, s);
     });
   }
   if (e == cudaSuccess)

@@ -1,5 +1,6 @@
-// Backward kernels: K2 (Delta = rowsum(dO * O)), K3 (dK, dV owned per key
-// tile, no atomics) and K4 (dQ owned per query tile, no atomics).
+// Backward kernels: K2 (Delta = rowsum(dO * O); scored forms: K2b, from the
+// weights in rows of few keys), K3 (dK, dV owned per key tile, no atomics) and
+// K4 (dQ owned per query tile, no atomics).
 //
 // Method (KPage abstract, "KPage: block-sparse attention for partially
 // occupied 3D blocks", zhuanzhiai.com, abstract paragraph): the backward pass
@@ -86,7 +87,7 @@ struct PrepArgs {
 };
 template <int D>
 __global__ void __launch_bounds__(256) prep_kernel(const PrepArgs a) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the exact Delta of short items waits on its own
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // Delta of rows with few keys waits on its own
   if (static_cast<int>(blockIdx.x) >= a.n_delta) {
     const int64_t first = blockIdx.x - a.n_delta, step = gridDim.x - a.n_delta;
     for (int64_t i = first; i < a.q.n * a.q.bh; i += step) fill_rows<D>(a.q, i % a.q.n, i / a.q.n);
@@ -115,6 +116,230 @@ __global__ void __launch_bounds__(256) prep_kernel(const PrepArgs a) {
 #pragma unroll
     for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off, TPR);
     if (t < total && t % TPR == 0) a.delta[t / TPR] = acc;
+  }
+}
+
+// ----------------------------------------------------------------------------
+// K2b: Delta of rows with few keys (scored forms)
+// ----------------------------------------------------------------------------
+// Delta = dO.O inherits the rounding of O, 2^-9 of |dO| |O| or so.  In a row of many
+// keys O is small against V and that is lost in the rounding of dS; in a row of few,
+// dP - Delta is a difference of like numbers.  Simulated at D = 128 with scores of
+// deviation 1.5, dQ is off by 0.43% with 2 keys, 0.33% with 4, 0.29% with 8 and 0.26% with
+// 16, of which its own roundings are 0.235%.  So a row with up to 16 keys gets
+//   Delta_i = sum_j P_ij dP_ij / sum_j P_ij
+// from the weights themselves, in fp32.  The rule goes by the row's allowed keys, the
+// masks included: rows at a document's start stand in items whose lists are long.
+//
+// One CTA per query-owned item, one thread per row.  The keys are counted over the
+// item's list, sixteen pages at a time, until every row has more than 16 or the list
+// ends; most rows leave in the first pass.  A row compares pair by pair only in pages
+// that their range leaves open.  The (row, key) pairs that remain are shared out over
+// the CTA, eight lanes each, whose loads are then 128 bytes of a row; a row sums its
+// pairs in list order.  Bound: latency of dependent loads.  K2 and this kernel, 16
+// heads, D = 128: 40 us of a backward of 3140 on 12289 tokens with a prefix (no row of few
+// keys), 81 of 673 on 16384 tokens in documents of 900, 130 of 497 in documents of 60.
+constexpr int kFewKeys = 16;
+constexpr int kFewPages = 16;  // pages per pass
+constexpr int kFewLanes = 8;   // lanes per pair
+
+struct FewArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const __nv_bfloat16* d_o;
+  const float* lse;
+  float* delta;
+  const int32_t* work;
+  const int32_t* pages;
+  const uint64_t* masks;
+  int64_t q_slots, kv_slots;
+  int heads, kv_group;
+  float scale;
+  ScoreArgs sc;
+};
+
+// sum + a.b of eight bf16 pairs
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float sum) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
+    sum = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), sum);
+  }
+  return sum;
+}
+
+// Range over the 16 lanes of a half warp.
+__device__ __forceinline__ int2 half_range(bool live, int x) {
+  int lo = live ? x : 0x7FFFFFFF, hi = live ? x : static_cast<int>(0x80000000);
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+  }
+  return make_int2(lo, hi);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRows) few_keys_kernel(const FewArgs a) {
+  constexpr int NC = kFewPages * 16 / kRows;  // columns per thread and pass
+  __shared__ __align__(16) int s_pos[kFewPages * 16];  // positions and documents of a pass
+  __shared__ __align__(16) int s_doc[kFewPages * 16];
+  __shared__ int4 s_rng[kFewPages];
+  __shared__ uint4 s_mask[kFewPages];
+  __shared__ int s_key[kFewKeys][kRows];  // a row's pages with keys (entries of the list), then its keys, then their weights
+  __shared__ union {
+    uint16_t bits[kFewKeys][kRows];  // the pages' keys
+    float dp[kFewKeys][kRows];
+  } s_x;
+  __shared__ uint8_t s_row[kFewKeys * kRows];  // row of a pair
+  __shared__ int s_first[kRows];               // first pair of a row
+  __shared__ int s_total[kRows / 32];
+  const ScoreArgs& sc = a.sc;
+  const Work wk = load_work(a.work, blockIdx.x);
+  const int n_cols = wk.e1 - wk.e0;
+  const int row = threadIdx.x, lane = lane_id();
+  const int64_t k_off = (wk.bh / a.heads) * sc.k_batch;
+  const bool masked = sc.q_last || sc.q_doc;
+  auto page_of = [&](int e) { return e < n_cols ? __ldg(a.pages + wk.e0 + e) : 0; };
+  int page[NC];
+#pragma unroll
+  for (int h = 0; h < NC; ++h) page[h] = page_of((row >> 4) + 8 * h);
+  auto mask_of = [&](int e) {
+    return row < kFewPages && e < n_cols
+               ? __ldg(reinterpret_cast<const uint4*>(a.masks + 2 * (static_cast<int64_t>(wk.e0) + e)))
+               : make_uint4(0, 0, 0, 0);
+  };
+  uint4 words = mask_of(row);
+  const bool own = row < 16 * wk.n_own;
+  const uint32_t code = own ? wk.row_code(row) : 15u;
+  const int64_t slot = own ? pref_slot(wk.own_page(row >> 4), row & 15) : a.q_slots;
+  const bool real = code < 8u && slot < a.q_slots;
+  bool open = real;  // the row may yet turn out to have few keys
+  int last = 0, doc = -1, n = 0, n_pages = 0;
+  if (open) {
+    const int64_t off = (wk.bh / a.heads) * sc.q_batch + slot;
+    if (sc.q_last) last = __ldg(sc.q_last + off);
+    if (sc.q_doc) doc = __ldg(sc.q_doc + off);
+  }
+  const int4 mine = make_int4(last, last, doc, doc);
+  for (int e0 = 0; e0 < n_cols; e0 += kFewPages) {
+    if (!__syncthreads_or(open)) break;
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      const int c = row + kRows * h, e = e0 + (c >> 4);
+      const int64_t ks = pref_slot(page[h], row & 15);
+      const bool live = e < n_cols && ks < a.kv_slots;
+      const int64_t off = k_off + (live ? ks : 0);
+      if (sc.q_last) s_pos[c] = __ldg(sc.k_pos + off);
+      if (sc.q_doc) s_doc[c] = __ldg(sc.k_doc + off);
+      if (masked) {
+        const int2 rp = half_range(live, sc.q_last ? s_pos[c] : 0), rd = half_range(live, sc.q_doc ? s_doc[c] : 0);
+        if ((lane & 15) == 0) s_rng[c >> 4] = make_int4(rp.x, rp.y, rd.x, rd.y);
+      }
+      page[h] = page_of(e + kFewPages);
+    }
+    if (row < kFewPages) s_mask[row] = words;
+    words = mask_of(e0 + kFewPages + row);
+    __syncthreads();
+    for (int j = 0; open && j < min(kFewPages, n_cols - e0); ++j) {
+      uint32_t m = reinterpret_cast<const uint16_t*>(&s_mask[j])[code];
+      if (m == 0u) continue;
+      if (masked) {
+        const int4 rg = s_rng[j];
+        if (query_none(sc, rg, mine)) continue;
+        if (!query_all(sc, rg, mine)) m &= column_bits<true, 16>(sc.q_last, sc.q_doc, s_pos + 16 * j, s_doc + 16 * j, last, doc);
+        if (m == 0u) continue;
+      }
+      n += __popc(m);
+      open = n <= kFewKeys;
+      if (open) {
+        s_key[n_pages][row] = e0 + j;
+        s_x.bits[n_pages++][row] = static_cast<uint16_t>(m);
+      }
+    }
+  }
+  const bool few = real && open && n > 0;
+  const int mine_n = few ? n : 0;
+  int upto = mine_n;  // pairs of the warp's rows up to this one
+#pragma unroll
+  for (int off = 1; off < 32; off *= 2) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += x;
+  }
+  if (lane == 31) s_total[row >> 5] = upto;
+  __syncthreads();
+  int first = upto - mine_n, pairs = 0;
+#pragma unroll
+  for (int w = 0; w < kRows / 32; ++w) {
+    if (w < row >> 5) first += s_total[w];
+    pairs += s_total[w];
+  }
+  // the kernel before writes every row's Delta first; block 0 waits for it in any case,
+  // so that this kernel does not end (and let the stream go on) before that one
+  if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (pairs == 0) return;
+  if (few) {
+    // pages to keys (16 entry + slot), last ones first, so that none is written over unread
+    s_first[row] = first;
+    for (int i = n_pages - 1, k = n; i >= 0; --i) {
+      const int entry = s_key[i][row];
+      for (uint32_t m = s_x.bits[i][row]; m != 0u;) {
+        const int top = 31 - __clz(m);
+        s_key[--k][row] = 16 * entry + top;
+        m ^= 1u << top;
+      }
+    }
+    for (int k = 0; k < n; ++k) s_row[first + k] = static_cast<uint8_t>(row);
+  }
+  __syncthreads();
+  const int kv_bh = (wk.bh / a.heads) * (a.heads / a.kv_group) + (wk.bh % a.heads) / a.kv_group;
+  const float slope = sc.slopes ? __ldg(sc.slopes + wk.bh % a.heads) : 0.f;
+  const int part = lane % kFewLanes;
+  for (int w = row / 32 * (32 / kFewLanes); w < pairs; w += kRows / kFewLanes) {  // the warp's four pairs
+    const bool live = w + lane / kFewLanes < pairs;
+    const int i = live ? w + lane / kFewLanes : w;  // (the others repeat the warp's first, which is still a key)
+    const int r = s_row[i], k = i - s_first[r], key = s_key[k][r];
+    const int64_t qs = pref_slot(wk.own_page(r >> 4), r & 15), qrow = static_cast<int64_t>(wk.bh) * a.q_slots + qs;
+    const int64_t ks = pref_slot(__ldg(a.pages + wk.e0 + (key >> 4)), key & 15);
+    const int64_t krow = static_cast<int64_t>(kv_bh) * a.kv_slots + ks;
+    float s = 0.f, dp = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 8 / kFewLanes; ++c) {
+      const int at = c * kFewLanes + part;
+      s = dot8(__ldg(reinterpret_cast<const uint4*>(a.q + qrow * D) + at), __ldg(reinterpret_cast<const uint4*>(a.k + krow * D) + at), s);
+      dp = dot8(__ldg(reinterpret_cast<const uint4*>(a.d_o + qrow * D) + at), __ldg(reinterpret_cast<const uint4*>(a.v + krow * D) + at), dp);
+    }
+#pragma unroll
+    for (int off = kFewLanes / 2; off > 0; off >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, off);
+      dp += __shfl_xor_sync(0xffffffffu, dp, off);
+    }
+    float z = s * a.scale;
+    if (sc.cap > 0.f) {
+      const float u = z / sc.cap;
+      if (!(fabsf(u) < 1e-4f)) z = sc.cap * tanhf(u);  // (tanh u = u to 3e-9 there, and u may leave fp32's normals)
+    }
+    if (sc.slopes)
+      z -= slope * fabsf(static_cast<float>(__ldg(sc.q_pos + (wk.bh / a.heads) * sc.q_batch + qs)) -
+                         static_cast<float>(__ldg(sc.k_pos + k_off + ks)));
+    const float p = expf(z - __ldg(a.lse + qrow));
+    __syncwarp();
+    if (part == 0 && live) {
+      s_key[k][r] = __float_as_int(p);
+      s_x.dp[k][r] = p != 0.f ? p * dp : 0.f;
+    }
+  }
+  __syncthreads();
+  if (few) {
+    float sum = 0.f, dsum = 0.f;
+    for (int k = 0; k < n; ++k) {
+      sum += __int_as_float(s_key[k][row]);
+      dsum += s_x.dp[k][row];
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (sum > 0.f) a.delta[static_cast<int64_t>(wk.bh) * a.q_slots + slot] = dsum / sum;  // (NaN scores: dO.O, which is NaN)
   }
 }
 
@@ -899,24 +1124,14 @@ struct DqCfg {
 };
 
 // SC: the scored forms (score.cuh).
-//
-// DELTA: no dQ, but Delta_i = sum_j P_ij dP_ij for the rows of an item, from the
-// weights themselves.  Delta = dO.O inherits the rounding of O, 2^-9 of |dO| |O|
-// or so.  In a row of many keys O is small against V and that is lost in the
-// rounding of dS; in a row of two or five keys dP - Delta is a difference of like
-// numbers, and dQ came out 1% off (its own roundings are 0.24%).  Items of up to
-// 256 keys therefore get this pass (their rows are where keys are few, and it costs
-// a few steps each: 9 of 84 us for two rows of 777 tokens with 4 heads); it
-// overwrites what Delta = dO.O gave.
-template <int D, int SC, bool DELTA>
+template <int D, int SC>
 __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     dq_kernel(const __nv_bfloat16* __restrict__ q, const __grid_constant__ TmaPages tm_do,
               const __grid_constant__ TmaPages tm_k, const __grid_constant__ TmaPages tm_v,
               const int32_t* __restrict__ work, const int32_t* __restrict__ col_pages,
               const uint64_t* __restrict__ col_masks, const float* __restrict__ lse, const float* __restrict__ delta,
               __nv_bfloat16* __restrict__ out_dq, int64_t q_slots, float sl2, float scale, int heads, int kv_group,
-              int* err, const ScoreArgs sc, int64_t kv_slots, const int32_t* __restrict__ order, int short_entries,
-              float* __restrict__ out_delta) {
+              int* err, const ScoreArgs sc, int64_t kv_slots, const int32_t* __restrict__ order) {
   using C = DqCfg<D>;
   constexpr bool kScored = SC != kScoreNone, kCap = SC == kScoreCap;
   using W = BwdWarps<kScored>;
@@ -960,12 +1175,6 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
   const int n_cols = wk.e1 - wk.e0;
   const int n_steps = (n_cols + NP - 1) / NP;
   const int warp = warp_id(), lane = lane_id();
-  if constexpr (DELTA) {
-    if (n_cols > short_entries || n_cols == 0) {  // (a row without keys keeps its 0)
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      return;
-    }
-  }
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -1138,7 +1347,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       const uint64_t bk = sdesc_add(dkm, ks * C::kStageTile + half * kHalfStage);
 #pragma unroll
       for (int j = 0; j < NP; ++j)
-        if (!DELTA && j < n) umma_ts_w(tDQ, tPk(p) + 8 * j, sdesc_add(bk, j * 2048), idesc_acc, (st > 0 || j > 0) ? 1u : 0u);
+        if (j < n) umma_ts_w(tDQ, tPk(p) + 8 * j, sdesc_add(bk, j * 2048), idesc_acc, (st > 0 || j > 0) ? 1u : 0u);
       if (stage_end) umma_commit_w(&k_empty[ks]);
       umma_commit_w(&dq_done[p]);
     }
@@ -1184,8 +1393,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     }
     const float lse_row = (valid_slot && seg >= 0) ? __ldg(lse + roff) : 0.f;
     const float nlse2 = lse_row == -INFINITY ? -INFINITY : -lse_row * kLog2e;  // -inf: no key, every weight 0
-    const float dl = (!DELTA && valid_slot && seg >= 0) ? __ldg(delta + roff) : 0.f;
-    float delta_sum = 0.f;  // DELTA: this group's part of the row's sum
+    const float dl = (valid_slot && seg >= 0) ? __ldg(delta + roff) : 0.f;
     // this row's side of the masks and the bias
     int row_last = 0, row_doc = -1;
     float row_pos = 0.f, slope = 0.f;
@@ -1256,16 +1464,14 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       tc_fence_before();
       mbar_arrive(&s_free[b]);
       if (active) {
-        if constexpr (!DELTA) {
 #pragma unroll
-          for (int i = 0; i < CW; i += 2) {
-            float x0, x1;
-            f2_unpack(f2_add(f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), ndl), x0, x1);
-            d[i] = __float_as_uint(x0);
-            d[i + 1] = __float_as_uint(x1);
-          }
+        for (int i = 0; i < CW; i += 2) {
+          float x0, x1;
+          f2_unpack(f2_add(f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), ndl), x0, x1);
+          d[i] = __float_as_uint(x0);
+          d[i + 1] = __float_as_uint(x1);
         }
-        if constexpr (kCap) cap_scores<!DELTA>(a, d, sc.c, m != 0u);
+        if constexpr (kCap) cap_scores<true>(a, d, sc.c, m != 0u);
         if (sc.slopes) bias_scores(a, col_posf(ks) + 64 * (st % SPS) + CW * grp, row_pos, slope);
 #pragma unroll
         for (int i = 0; i < CW; i += 2) {
@@ -1274,13 +1480,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
           a[i] = __float_as_uint(x0);
           a[i + 1] = __float_as_uint(x1);
         }
-        if constexpr (DELTA) {
-#pragma unroll
-          for (int i = 0; i < CW; ++i)
-            if ((m >> i) & 1u) delta_sum = fmaf(ex2(__uint_as_float(a[i])), __uint_as_float(d[i]), delta_sum);
-        } else {
-          weights_and_ds(a, d, m, pd);
-        }
+        weights_and_ds(a, d, m, pd);
       }
       // Packed set b still feeds dQ(st-2).  Every row thread waits, active or not:
       // dq_done(st-2) implies that ds_full finished the phase of step st-2.
@@ -1289,7 +1489,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
         break;
       }
       tc_fence_after();
-      if (!DELTA && active) {
+      if (active) {
         tmem_st8(tPk(b) + lane_off + grp * (CW / 2), pd);
         tmem_wait_st();
       }
@@ -1300,9 +1500,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, ab));
       tc_fence_after();
     }
-    // (the dO tile's last readers, the products of the last step, are done)
-    if constexpr (DELTA) reinterpret_cast<float*>(sDO)[128 * grp + row] = delta_sum;
-    if (!DELTA && ok) {
+    if (ok) {
       // group g writes columns [g*D/4, (g+1)*D/4) of dQ
       constexpr int kOut = D / NG;  // 32 or 16
       const int col = grp * kOut;
@@ -1455,19 +1653,9 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // launched beside the dK / dV kernel (DELTA: beside the one that writes every
-  // row's Delta first): what follows in the stream waits for this kernel only, so
-  // this one ends after that one
+  // launched beside the dK / dV kernel: what follows in the stream waits for this
+  // kernel only, so this one ends after that one
   if constexpr (kScored) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if constexpr (DELTA) {
-    const int row = threadIdx.x;
-    if (row < 16 * wk.n_own && wk.row_code(row) < 8u && !*abort_flag) {
-      const int64_t slot = pref_slot(wk.own_page(row >> 4), row & 15);
-      const float* part = reinterpret_cast<const float*>(sDO) + row;
-      if (slot < q_slots)
-        out_delta[static_cast<int64_t>(wk.bh) * q_slots + slot] = (part[0] + part[128]) + (part[256] + part[384]);
-    }
-  }
 }
 
 }  // namespace
@@ -1519,17 +1707,16 @@ static cudaError_t launch_dkdv_t(const TmaPages& tk, const TmaPages& tv, const T
   return cudaGetLastError();
 }
 
-template <int D, int SC, bool DELTA>
+template <int D, int SC>
 static cudaError_t launch_dq_t(const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
                                const TmaPages& tv, const TileArgs& a, const ScoreArgs& sc, const float* lse,
-                               const float* delta, __nv_bfloat16* dq, int64_t n_items, int short_entries,
-                               float* out_delta, cudaStream_t st) {
+                               const float* delta, __nv_bfloat16* dq, cudaStream_t st) {
   using C = DqCfg<D>;
   constexpr int kSmem = C::kSmem + (SC != kScoreNone ? C::kScoreBytes : 0);
-  cudaError_t e = cudaFuncSetAttribute(dq_kernel<D, SC, DELTA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess || n_items == 0) return e;
+  cudaError_t e = cudaFuncSetAttribute(dq_kernel<D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess || a.n_work == 0) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(n_items));
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_work));
   cfg.blockDim = dim3(BwdWarps<SC != kScoreNone>::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
@@ -1538,11 +1725,9 @@ static cudaError_t launch_dq_t(const __nv_bfloat16* q, const TmaPages& tdo, cons
   beside.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &beside;
   cfg.numAttrs = a.beside ? 1 : 0;
-  // short items are the last ones of the order
-  const int32_t* order = DELTA && a.order ? a.order + (a.n_work - n_items) : a.order;
-  return cudaLaunchKernelEx(&cfg, dq_kernel<D, SC, DELTA>, q, tdo, tk, tv, a.work, a.pages, a.masks, lse, delta, dq,
+  return cudaLaunchKernelEx(&cfg, dq_kernel<D, SC>, q, tdo, tk, tv, a.work, a.pages, a.masks, lse, delta, dq,
                             a.own_slots, a.scale * kLog2e, a.scale, a.heads, a.kv_group, a.err, sc, a.col_slots,
-                            order, short_entries, out_delta);
+                            a.order);
 }
 
 // Calls `go` with the head size and the form of the scores as constants.
@@ -1571,21 +1756,28 @@ cudaError_t launch_dq(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo,
                       const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, const float* lse,
                       const float* delta, __nv_bfloat16* dq, cudaStream_t st) {
   const auto go = [&](auto d, auto form) {
-    return launch_dq_t<decltype(d)::value, decltype(form)::value, false>(q, tdo, tk, tv, a, sc ? *sc : ScoreArgs(), lse,
-                                                                         delta, dq, a.n_work, 0, nullptr, st);
+    return launch_dq_t<decltype(d)::value, decltype(form)::value>(q, tdo, tk, tv, a, sc ? *sc : ScoreArgs(), lse, delta,
+                                                                  dq, st);
   };
   return by_form(head_dim, sc, go);
 }
 
-cudaError_t launch_delta_exact(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
-                               const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, int64_t n_short,
-                               int short_entries, const float* lse, float* delta, cudaStream_t st) {
-  const auto go = [&](auto d, auto form) {
-    constexpr int kForm = decltype(form)::value == kScoreNone ? kScoreMask : decltype(form)::value;  // always scored
-    return launch_dq_t<decltype(d)::value, kForm, true>(q, tdo, tk, tv, a, *sc, lse, nullptr, nullptr,
-                                                        a.order ? n_short : a.n_work, short_entries, delta, st);
-  };
-  return by_form(head_dim, sc, go);
+cudaError_t launch_few_keys(int head_dim, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                            const __nv_bfloat16* d_o, const TileArgs& a, const ScoreArgs& sc, const float* lse,
+                            float* delta, cudaStream_t st) {
+  if (a.n_work == 0) return cudaSuccess;
+  const FewArgs f{q,           k,           v,           d_o,     lse,        delta,   a.work, a.pages,
+                  a.masks,     a.own_slots, a.col_slots, a.heads, a.kv_group, a.scale, sc};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.n_work));
+  cfg.blockDim = dim3(kRows);
+  cfg.stream = st;
+  cudaLaunchAttribute behind = {};
+  behind.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  behind.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &behind;
+  cfg.numAttrs = a.beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, head_dim == 128 ? few_keys_kernel<128> : few_keys_kernel<64>, f);
 }
 
 }  // namespace spattn

@@ -56,7 +56,8 @@ struct TileArgs {
   // pass, entry e's column head is the item's first query head + col_heads[e].
   int heads = 1, kv_heads = 1, kv_group = 1;
   const uint16_t* col_heads = nullptr;
-  // launch_dq right behind launch_dkdv, both scored: it may run beside that kernel
+  // launch_dq right behind launch_dkdv, both scored, and launch_few_keys behind
+  // launch_prep: it may run beside that kernel
   bool beside = false;
   const int32_t* order = nullptr;  // the items longest first over all heads (scored forms; null: as listed)
   // some query-owned item takes the 64-row route (the forward then runs the
@@ -107,12 +108,11 @@ struct FillArgs {
 cudaError_t launch_prep(int head_dim, const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* delta, int64_t rows,
                         int* sched, const FillArgs& q, const FillArgs& k, cudaStream_t st);
 
-// Exact Delta for the query-owned items of at most `short_entries` entries
-// (`n_short`: how many the end of a.order holds; without an order every item
-// is looked at), right behind launch_prep and beside it.
-cudaError_t launch_delta_exact(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
-                               const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, int64_t n_short,
-                               int short_entries, const float* lse, float* delta, cudaStream_t st);
+// K2b: Delta from the weights for the rows of at most 16 allowed keys, over the
+// query-owned items, right behind launch_prep and (a.beside) beside it.
+cudaError_t launch_few_keys(int head_dim, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                            const __nv_bfloat16* d_o, const TileArgs& a, const ScoreArgs& sc, const float* lse,
+                            float* delta, cudaStream_t st);
 
 // K1: O, LSE for every query-owned work item; `sc` (may be null) modifies the scores,
 // and with it the launch also does `fill`.

@@ -1196,7 +1196,6 @@ int build_plan(const spattn_layout* L, const spattn_graph* G, spattn_plan_s* P) 
       std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return len(a) > len(b); });
       if ((st = upload(order, &w->d_order, bytes, &w->cap_order))) return st;
       w->ordered = true;
-      w->n_short = std::count_if(order.begin(), order.end(), [&](int32_t i) { return len(i) <= kShortEntries; });
     }
   }
   if ((st = upload(P->q_fill, &P->d_q_fill, bytes))) return st;

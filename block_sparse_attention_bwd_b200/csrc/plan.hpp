@@ -76,7 +76,6 @@ struct WorkList {
   int32_t* d_order = nullptr;
   int64_t cap_order = 0;
   bool ordered = false;
-  int64_t n_short = 0;  // items of at most kShortEntries entries, the last ones of d_order
   // capacities of the device arrays (elements) and, after a device re-plan,
   // the number of entries on the device
   int64_t cap_work = 0, cap_pages = 0, cap_masks = 0, cap_heads = 0;
@@ -90,10 +89,6 @@ struct WorkList {
 // tokens, 16 query heads over 4: forward 630 -> 540, dK / dV 1360 -> 1140; on 16384
 // tokens of short documents, 16 heads: 111 -> 94 and 201 -> 186.
 constexpr int64_t kOrderMax = 32 * 148;
-
-// Query-owned items of up to this many entries (256 keys) get Delta from their
-// weights in a scored backward (see the kernel).
-constexpr int32_t kShortEntries = 16;
 
 // Work item templates of one pass for the device planner: the slot-order
 // tiles of the layout split into items, without their column lists.

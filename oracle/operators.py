@@ -8,7 +8,8 @@ outputs to bf16 may be from it, element by element:
 * a rounding to bf16 is off by at most 2^-8 of the value (half a unit of eps =
   2^-7), so O = sum P v with rounded weights and a rounded result is off by at
   most 2^-8 (sum P |v| + |O|);
-* Delta = sum_d dO O, formed from the rounded O, inherits that bound times |dO|;
+* Delta = sum_d dO O, formed from the rounded O, inherits that bound times |dO|
+  (rows in ``exact_delta`` have it from their weights: fp32's part only);
 * dS = P f (dP - Delta) (f = 1 - tanh^2) is off by P f of Delta's bound and by
   its own rounding, dV's weights by theirs;
 * fp32 adds sums of D products, the score and exp, covered by ``_FP32`` of the
@@ -70,7 +71,7 @@ def forward(q, k, v, mask, z):
     return o, lse, o_tol, lse_tol
 
 
-def backward(q, k, v, do, mask, z, f, scale):
+def backward(q, k, v, do, mask, z, f, scale, exact_delta=None):
     """{name: (value, bound)} of dq, dk, dv of one head."""
     p, _ = softmax(z, mask)
     o = p @ v
@@ -79,6 +80,8 @@ def backward(q, k, v, do, mask, z, f, scale):
     adp = np.abs(do) @ np.abs(v).T
     delta = (p * dp).sum(axis=1, keepdims=True)
     delta_tol = (np.abs(do) * o_tol).sum(axis=1, keepdims=True)
+    if exact_delta is not None:
+        delta_tol = np.where(np.asarray(exact_delta)[:, None], 0.0, delta_tol)
     ds = p * f * (dp - delta)
     mass = adp + (p * adp).sum(axis=1, keepdims=True)
     fuzz = p * f * (delta_tol + _FP32 * mass) + _F_FLOOR * p * mass
