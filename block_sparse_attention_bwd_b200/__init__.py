@@ -567,8 +567,9 @@ def rope_freqs(sections, base=10000.0, scaling=None, factor=1.0, original_slots=
     ``"ntk"`` raises the base by ``factor ** (n / (n - 1))``, so that the slowest
     pair is divided by the factor and the fastest kept; ``"yarn"`` divides pairs
     that make fewer than ``beta_slow`` turns over ``original_slots`` positions, keeps
-    those above ``beta_fast`` turns, blends between, and sets mscale = 0.1
-    ln(factor) + 1.
+    those above ``beta_fast`` turns, blends between (linearly in the turns, as the
+    method's paper has it; where a checkpoint ramps linearly in the pair's index
+    instead, pass its own ``freqs`` to :func:`rope`), and sets mscale = 0.1 ln(factor) + 1.
     """
     import math
 
@@ -578,6 +579,8 @@ def rope_freqs(sections, base=10000.0, scaling=None, factor=1.0, original_slots=
         raise ValueError(f"rope_freqs: unknown scaling {scaling!r}")
     if not (base > 0 and factor > 0):
         raise ValueError("rope_freqs: base and factor must be positive")
+    if scaling == "yarn" and not (original_slots > 0 and beta_fast > beta_slow):
+        raise ValueError("rope_freqs: original_slots must be positive and beta_fast above beta_slow")
     sections = [int(sections)] if isinstance(sections, (int, np.integer)) else [int(n) for n in sections]
     if any(n < 0 for n in sections):
         raise ValueError("rope_freqs: sections must not be negative")
