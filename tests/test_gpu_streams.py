@@ -111,3 +111,26 @@ def test_paged_calls_on_the_current_and_a_side_stream_at_once():
         assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
     sp.spattn_paged_check(paged)
     assert bool(torch.isfinite(want[0][1]).all())
+
+
+def test_a_forked_stream_inside_a_capture():
+    keep, calls = _calls()
+    side = torch.cuda.Stream()
+    for name in ("fwd_scored", "rope", "paged"):
+        call = calls[name][1]
+        want = [x.clone() for x in call(None)]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            here = torch.cuda.current_stream()
+            side.wait_stream(here)
+            got = call(side)
+            here.wait_stream(side)
+        for _ in range(3):
+            for x in got:
+                x.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            for x, y in zip(want, got):
+                assert torch.equal(x, y), name
+        del g, got
