@@ -276,23 +276,35 @@ int run_bwd(const void* q, const void* k, const void* v, const void* o, const fl
   auto* dQ = static_cast<__nv_bfloat16*>(dq);
   auto* dK = static_cast<__nv_bfloat16*>(dk);
   auto* dV = static_cast<__nv_bfloat16*>(dv);
+  // a scored backward's query-owned items with long lists and with short ones (all, where
+  // they have no order)
+  const WorkList& wq = plan->wq;
+  const int64_t n_long = wq.ordered ? wq.n_work - wq.n_short : wq.n_work, n_short = wq.ordered ? wq.n_short : wq.n_work;
+  const TileArgs tile_q = tile_args(plan, wq, plan->q.slots, plan->k.slots);
   cudaError_t e = timed(plan, SPATTN_K_DELTA, s, [&] {
-    if (sc)  // with the counter and the fills, in one launch
+    if (sc)  // with the counter, the fills and the scan, in one launch
       return launch_prep(D, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), plan->d_delta,
-                         bh * plan->q.slots, plan->d_sched,
+                         bh * plan->q.slots, tile_q, n_long, kShortEntries, *sc, plan->few,
                          fill_args(plan->d_q_fill, plan->q_fill, bh, plan->q.slots, dQ, nullptr, nullptr),
                          fill_args(plan->d_k_fill, plan->k_fill, bh_kv, plan->k.slots, dK, dV, nullptr), s);
     return launch_delta(D, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), plan->d_delta,
                         bh * plan->q.slots, s);
   });
   if (sc && e == cudaSuccess) {
-    TileArgs t = tile_args(plan, plan->wq, plan->q.slots, plan->k.slots);
+    TileArgs t = tile_q;
     t.beside = !plan->profiling;
-    e = timed(plan, SPATTN_K_DELTA, s, [&] {
-      return launch_few_keys(D, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-                             static_cast<const __nv_bfloat16*>(v), static_cast<const __nv_bfloat16*>(d_o), t, *sc, lse,
-                             plan->d_delta, s);
-    });
+    if (n_long > 0)
+      e = timed(plan, SPATTN_K_DELTA, s, [&] {
+        return launch_few_keys(D, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+                               static_cast<const __nv_bfloat16*>(v), static_cast<const __nv_bfloat16*>(d_o), t, n_long, *sc,
+                               plan->few, lse, plan->d_delta, s);
+      });
+    if (e != cudaSuccess) cudaMemsetAsync(plan->few.counts, 0, 3 * sizeof(int), s);  // (that kernel leaves them at zero)
+    if (e == cudaSuccess && n_short > 0)
+      e = timed(plan, SPATTN_K_DELTA, s, [&] {
+        return launch_delta_exact(D, static_cast<const __nv_bfloat16*>(q), tdo, tk, tv, t, sc, n_short, kShortEntries, lse,
+                                  plan->d_delta, s);
+      });
   }
   if (e == cudaSuccess)
     e = timed(plan, SPATTN_K_DKDV, s, [&] {
@@ -301,7 +313,7 @@ int run_bwd(const void* q, const void* k, const void* v, const void* o, const fl
     });
   if (e == cudaSuccess)
     e = timed(plan, SPATTN_K_DQ, s, [&] {
-      TileArgs t = tile_args(plan, plan->wq, plan->q.slots, plan->k.slots);
+      TileArgs t = tile_q;
       // (an event between the two, when profiling, keeps them apart)
       t.beside = sc && plan->wk.n_work > 0 && !plan->profiling;
       return launch_dq(D, static_cast<const __nv_bfloat16*>(q), tdo, tk, tv, t, sc, lse, plan->d_delta, dQ, s);

@@ -72,33 +72,159 @@ __global__ void delta_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfl
   }
 }
 
-// Start of a scored backward in one launch: Delta, the work-item counter of the
-// dK / dV kernel, and the zero rows that no work item writes.  Blocks 0 ..
-// n_delta - 1 form Delta, one warp-row group per pass as above; the others take
-// (fill entry, batch*head) pairs.
+// ----------------------------------------------------------------------------
+// Start of a scored backward
+// ----------------------------------------------------------------------------
+// In one launch: the scan for rows of few keys (see K2b below), Delta, the work-item counter
+// of the dK / dV kernel, and the zero rows that no work item writes.  n_scan blocks scan
+// one query-owned item each, n_delta form Delta, one warp-row group per pass as above, and
+// the others take (fill entry, batch*head) pairs.  The first two take turns, so that the
+// scan's waits and Delta's bytes meet on an SM.
+constexpr int kFewKeys = 127;
+constexpr int kFewPages = 16;   // pages per pass of the scan
+
 struct PrepArgs {
   const __nv_bfloat16* o;
   const __nv_bfloat16* d_o;
   float* delta;
   int64_t rows;
+  int64_t n_scan;
+  int short_entries;  // items of no more are not scanned
   int n_delta;
   int* sched;
   FillArgs q, k;  // dQ; dK and dV
+  // the scan's side
+  const int32_t* work;
+  const int32_t* pages;
+  const uint64_t* masks;
+  int64_t q_slots, kv_slots;
+  int heads;
+  const int32_t* order;
+  FewList few;
+  ScoreArgs sc;
 };
+
+// Range over the 16 lanes of a half warp.
+__device__ __forceinline__ int2 half_range(bool live, int lo, int hi) {
+  if (!live) lo = 0x7FFFFFFF, hi = static_cast<int>(0x80000000);
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+  }
+  return make_int2(lo, hi);
+}
+
+// One item: thread r < 128 counts row r's allowed keys over the item's list, sixteen
+// pages at a time, until every row has more than kFewKeys or the list ends; most rows
+// leave in the first pass.  Pairs are compared one by one only in pages that their range
+// leaves open.
+__device__ void scan_few_keys(const PrepArgs& a, int64_t item) {
+  __shared__ __align__(16) int s_pos[kFewPages * 16];  // positions and documents of a pass, a thread each
+  __shared__ __align__(16) int s_doc[kFewPages * 16];
+  __shared__ int4 s_rng[kFewPages];
+  __shared__ uint4 s_mask[kFewPages];
+  const ScoreArgs& sc = a.sc;
+  const Work wk = load_work(a.work, a.order ? __ldg(a.order + item) : item);
+  const int n_cols = wk.e1 - wk.e0;
+  if (n_cols <= a.short_entries) return;
+  const int row = threadIdx.x, lane = lane_id();
+  const int64_t k_off = (wk.bh / a.heads) * sc.k_batch;
+  const bool masked = sc.q_last || sc.q_doc;
+  auto page_of = [&](int e) { return masked && e < n_cols ? __ldg(a.pages + wk.e0 + e) : 0; };
+  auto mask_of = [&](int e) {
+    return row < kFewPages && e < n_cols
+               ? __ldg(reinterpret_cast<const uint4*>(a.masks + 2 * (static_cast<int64_t>(wk.e0) + e)))
+               : make_uint4(0, 0, 0, 0);
+  };
+  int page = page_of(row >> 4);
+  uint4 words = mask_of(row);
+  const bool own = row < 16 * wk.n_own;
+  const uint32_t code = own ? wk.row_code(row) : 15u;
+  const int64_t slot = own ? pref_slot(wk.own_page(row >> 4), row & 15) : a.q_slots;
+  const bool real = code < 8u && slot < a.q_slots;
+  bool open = real;  // the row may yet turn out to have few keys
+  int last = 0, doc = -1, n = 0, first_e = 0, last_e = 0;
+  uint64_t seen = 0;  // entries with an allowed key, from the first one on
+  if (open) {
+    const int64_t off = (wk.bh / a.heads) * sc.q_batch + slot;
+    if (sc.q_last) last = __ldg(sc.q_last + off);
+    if (sc.q_doc) doc = __ldg(sc.q_doc + off);
+  }
+  const int4 mine = make_int4(last, last, doc, doc);
+  for (int e0 = 0; e0 < n_cols; e0 += kFewPages) {
+    if (!__syncthreads_or(open)) break;
+    if (masked) {
+      const int e = e0 + (row >> 4);
+      const int64_t ks = pref_slot(page, row & 15);
+      const bool live = e < n_cols && ks < a.kv_slots;
+      const int64_t off = k_off + (live ? ks : 0);
+      const int pos = sc.q_last ? __ldg(sc.k_pos + off) : 0, kd = sc.q_doc ? __ldg(sc.k_doc + off) : 0;
+      s_pos[row] = pos;
+      s_doc[row] = kd;
+      const int2 rp = half_range(live, pos, pos), rd = half_range(live, kd, kd);
+      if ((lane & 15) == 0) s_rng[row >> 4] = make_int4(rp.x, rp.y, rd.x, rd.y);
+      page = page_of(e + kFewPages);
+    }
+    if (row < kFewPages) s_mask[row] = words;
+    words = mask_of(e0 + kFewPages + row);
+    __syncthreads();
+    for (int j = 0; open && j < min(kFewPages, n_cols - e0); ++j) {
+      uint32_t m = reinterpret_cast<const uint16_t*>(&s_mask[j])[code];
+      if (m == 0u) continue;
+      if (masked) {
+        const int4 rg = s_rng[j];
+        if (query_none(sc, rg, mine)) continue;
+        if (!query_all(sc, rg, mine)) m &= column_bits<true, 16>(sc.q_last, sc.q_doc, s_pos + 16 * j, s_doc + 16 * j, last, doc);
+        if (m == 0u) continue;
+      }
+      if (n == 0) first_e = e0 + j;
+      last_e = e0 + j;
+      if (last_e - first_e < 64) seen |= 1ull << (last_e - first_e);
+      n += __popc(m);
+      open = n <= kFewKeys;
+    }
+  }
+  if (row >= kRows) return;
+  const bool few = real && open && n > 0;
+  const uint32_t bits = __ballot_sync(0xffffffffu, few);
+  const int2 span = half_range(few, first_e, last_e);
+  const bool far = span.y - span.x >= 64;
+  uint64_t x = few && !far ? seen << (first_e - span.x) : 0;
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) x |= __shfl_xor_sync(0xffffffffu, x, off);
+  const uint32_t rows = (bits >> (lane & 16)) & 0xFFFFu;
+  if ((lane & 15) == 0 && rows != 0u) {
+    FewPage p;
+    p.page = static_cast<int>(a.order ? __ldg(a.order + item) : item) * 8 + (row >> 4);
+    p.rows = far ? rows | kFewFar : rows;
+    p.first = span.x;
+    p.pad = 0;
+    p.entries = x;
+    p.pad2 = 0;
+    const int i = atomicAdd(a.few.counts, 1);
+    if (i < a.few.cap) a.few.pages[i] = p;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(256) prep_kernel(const PrepArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // Delta of rows with few keys waits on its own
-  if (static_cast<int>(blockIdx.x) >= a.n_delta) {
-    const int64_t first = blockIdx.x - a.n_delta, step = gridDim.x - a.n_delta;
+  const int64_t turns = 2 * min(a.n_scan, static_cast<int64_t>(a.n_delta));
+  const bool scan = blockIdx.x < turns ? (blockIdx.x & 1) == 0 : blockIdx.x - turns / 2 < a.n_scan;
+  if (scan) return scan_few_keys(a, blockIdx.x < turns ? blockIdx.x / 2 : blockIdx.x - turns / 2);
+  const int64_t block = blockIdx.x < turns ? blockIdx.x / 2 : blockIdx.x - a.n_scan;  // of those that form Delta
+  if (block >= a.n_delta) {
+    const int64_t first = block - a.n_delta, step = gridDim.x - a.n_scan - a.n_delta;
     for (int64_t i = first; i < a.q.n * a.q.bh; i += step) fill_rows<D>(a.q, i % a.q.n, i / a.q.n);
     for (int64_t i = first; i < a.k.n * a.k.bh; i += step) fill_rows<D>(a.k, i % a.k.n, i / a.k.n);
     return;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.sched = 0;
+  if (block == 0 && threadIdx.x == 0) *a.sched = 0;
   constexpr int TPR = D / 8;
   const int64_t total = a.rows * TPR, stride = static_cast<int64_t>(a.n_delta) * blockDim.x;
   const int lane = threadIdx.x & 31;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + (threadIdx.x & ~31); t0 < total; t0 += stride) {
+  for (int64_t t0 = block * blockDim.x + (threadIdx.x & ~31); t0 < total; t0 += stride) {
     const int64_t t = t0 + lane;
     float acc = 0.f;
     if (t < total) {
@@ -122,27 +248,29 @@ __global__ void __launch_bounds__(256) prep_kernel(const PrepArgs a) {
 // ----------------------------------------------------------------------------
 // K2b: Delta of rows with few keys (scored forms)
 // ----------------------------------------------------------------------------
-// Delta = dO.O inherits the rounding of O, 2^-9 of |dO| |O| or so.  In a row of many
+// Delta = dO.O inherits the rounding of O, 2^-9 of |dO| |O| or so.  In a row of very many
 // keys O is small against V and that is lost in the rounding of dS; in a row of few,
 // dP - Delta is a difference of like numbers.  Simulated at D = 128 with scores of
-// deviation 1.5, dQ is off by 0.43% with 2 keys, 0.33% with 4, 0.29% with 8 and 0.26% with
-// 16, of which its own roundings are 0.235%.  So a row with up to 16 keys gets
+// deviation 1.5, dQ is off by 0.43% with 2 keys, 0.29% with 8, 0.265% with 16, 0.25% with 64
+// and 0.245% with 256, of which its own roundings are 0.235%.  So a row with up to 127
+// allowed keys, masks included, gets
 //   Delta_i = sum_j P_ij dP_ij / sum_j P_ij
-// from the weights themselves, in fp32.  The rule goes by the row's allowed keys, the
-// masks included: rows at a document's start stand in items whose lists are long.
+// from the weights themselves, in fp32.  Items of short lists get that as a whole, in 128-row
+// tiles (dq_kernel's DELTA form); here are the rows of longer items, such as a
+// document's first ones behind the pages of another.
 //
-// One CTA per query-owned item, one thread per row.  The keys are counted over the
-// item's list, sixteen pages at a time, until every row has more than 16 or the list
-// ends; most rows leave in the first pass.  A row compares pair by pair only in pages
-// that their range leaves open.  The (row, key) pairs that remain are shared out over
-// the CTA, eight lanes each, whose loads are then 128 bytes of a row; a row sums its
-// pairs in list order.  Bound: latency of dependent loads.  K2 and this kernel, 16
-// heads, D = 128: 40 us of a backward of 3140 on 12289 tokens with a prefix (no row of few
-// keys), 81 of 673 on 16384 tokens in documents of 900, 130 of 497 in documents of 60.
-constexpr int kFewKeys = 16;
-constexpr int kFewPages = 16;  // pages per pass
-constexpr int kFewLanes = 8;   // lanes per pair
-
+// The scan lists the 16-row owned pages that hold such rows, in any order, and warps take
+// them from a counter, since they are few, stand together and differ in cost.  A warp walks
+// the entries of the list that have a key of its page's rows, alone, so that a row's sums
+// have one order whatever else the call holds.  S and dP of 16 rows x 16 keys are m16n8k16
+// products whose operands come from global memory in 16-byte pieces (the order of the
+// inner dimension is free as long as both sides have the same).  A tile for tcgen05 would
+// be 128 rows, of which a page is an eighth and its neighbours have other keys; here the
+// loads' latency decides, not the products.
+//
+// 16 heads, D = 128: 18 us on 16384 tokens in documents of 900 (the scan takes 10 beside
+// Delta's 28; the backward went from 664 to 685), 4 where no row has few keys (12289
+// tokens with a prefix: 3090 to 3120).
 struct FewArgs {
   const __nv_bfloat16* q;
   const __nv_bfloat16* k;
@@ -153,193 +281,168 @@ struct FewArgs {
   const int32_t* work;
   const int32_t* pages;
   const uint64_t* masks;
+  FewList few;
   int64_t q_slots, kv_slots;
   int heads, kv_group;
   float scale;
   ScoreArgs sc;
 };
 
-// sum + a.b of eight bf16 pairs
-__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float sum) {
-  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
-    sum = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), sum);
-  }
-  return sum;
+// d += a b, 16 x 8 x 16, bf16 in, fp32 out
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Range over the 16 lanes of a half warp.
-__device__ __forceinline__ int2 half_range(bool live, int x) {
-  int lo = live ? x : 0x7FFFFFFF, hi = live ? x : static_cast<int>(0x80000000);
-#pragma unroll
-  for (int off = 8; off > 0; off >>= 1) {
-    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-  }
-  return make_int2(lo, hi);
-}
+constexpr int kFewThreads = 128;
 
 template <int D>
-__global__ void __launch_bounds__(kRows) few_keys_kernel(const FewArgs a) {
-  constexpr int NC = kFewPages * 16 / kRows;  // columns per thread and pass
-  __shared__ __align__(16) int s_pos[kFewPages * 16];  // positions and documents of a pass
-  __shared__ __align__(16) int s_doc[kFewPages * 16];
-  __shared__ int4 s_rng[kFewPages];
-  __shared__ uint4 s_mask[kFewPages];
-  __shared__ int s_key[kFewKeys][kRows];  // a row's pages with keys (entries of the list), then its keys, then their weights
-  __shared__ union {
-    uint16_t bits[kFewKeys][kRows];  // the pages' keys
-    float dp[kFewKeys][kRows];
-  } s_x;
-  __shared__ uint8_t s_row[kFewKeys * kRows];  // row of a pair
-  __shared__ int s_first[kRows];               // first pair of a row
-  __shared__ int s_total[kRows / 32];
+__global__ void __launch_bounds__(kFewThreads, 3) few_keys_kernel(const FewArgs a) {
+  constexpr int NC = D / 32;  // 64-byte pieces of a row, 16 bytes of each per lane
   const ScoreArgs& sc = a.sc;
-  const Work wk = load_work(a.work, blockIdx.x);
-  const int n_cols = wk.e1 - wk.e0;
-  const int row = threadIdx.x, lane = lane_id();
-  const int64_t k_off = (wk.bh / a.heads) * sc.k_batch;
-  const bool masked = sc.q_last || sc.q_doc;
-  auto page_of = [&](int e) { return e < n_cols ? __ldg(a.pages + wk.e0 + e) : 0; };
-  int page[NC];
+  const int lane = lane_id();
+  const int quad = lane >> 2, part = lane & 3;  // this lane's rows are quad and quad + 8, its keys 2 part, 2 part + 1 (+ 8)
+  const int mine = lane & 15;                   // the row (or column) whose arrays this lane holds
+  // (the pass over short items, which waits for the end of this kernel)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // the list and every row's Delta are there when the kernel before has ended
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int count = min(*reinterpret_cast<volatile int*>(a.few.counts), a.few.cap);
+  if (count == 0) return;
+  for (;;) {
+    int next = 0;
+    if (lane == 0) next = atomicAdd(a.few.counts + 1, 1);
+    next = __shfl_sync(0xffffffffu, next, 0);
+    if (next >= count) break;
+    const FewPage rec = a.few.pages[next];
+    const uint32_t few = rec.rows;
+    const bool far = (few & kFewFar) != 0u;
+    const int first = rec.first;
+    const Work wk = load_work(a.work, rec.page >> 3);
+    const int pg = rec.page & 7;
+    const int batch = wk.bh / a.heads;
+    const int kv_bh = batch * (a.heads / a.kv_group) + (wk.bh % a.heads) / a.kv_group;
+    const int own = wk.own_page(pg);
+    // this lane's row of the page; rows that are not asked for read the first one that is
+    const bool asked = (few >> mine) & 1u;
+    const int64_t slot = pref_slot(own, asked ? mine : __ffs(few) - 1);
+    const int64_t row = static_cast<int64_t>(wk.bh) * a.q_slots + slot;
+    const int seg = asked ? static_cast<int>(wk.row_code(16 * pg + mine)) : 0;
+    const int64_t q_off = batch * sc.q_batch + slot;
+    const int last = sc.q_last ? __ldg(sc.q_last + q_off) : 0, doc = sc.q_doc ? __ldg(sc.q_doc + q_off) : 0;
+    const float pos = sc.slopes ? static_cast<float>(__ldg(sc.q_pos + q_off)) : 0.f, lse = __ldg(a.lse + row);
+    const float slope = sc.slopes ? __ldg(sc.slopes + wk.bh % a.heads) : 0.f;
+    uint4 q[2][NC], d_o[2][NC];
+    float row_pos[2], row_lse[2];
 #pragma unroll
-  for (int h = 0; h < NC; ++h) page[h] = page_of((row >> 4) + 8 * h);
-  auto mask_of = [&](int e) {
-    return row < kFewPages && e < n_cols
-               ? __ldg(reinterpret_cast<const uint4*>(a.masks + 2 * (static_cast<int64_t>(wk.e0) + e)))
-               : make_uint4(0, 0, 0, 0);
-  };
-  uint4 words = mask_of(row);
-  const bool own = row < 16 * wk.n_own;
-  const uint32_t code = own ? wk.row_code(row) : 15u;
-  const int64_t slot = own ? pref_slot(wk.own_page(row >> 4), row & 15) : a.q_slots;
-  const bool real = code < 8u && slot < a.q_slots;
-  bool open = real;  // the row may yet turn out to have few keys
-  int last = 0, doc = -1, n = 0, n_pages = 0;
-  if (open) {
-    const int64_t off = (wk.bh / a.heads) * sc.q_batch + slot;
-    if (sc.q_last) last = __ldg(sc.q_last + off);
-    if (sc.q_doc) doc = __ldg(sc.q_doc + off);
-  }
-  const int4 mine = make_int4(last, last, doc, doc);
-  for (int e0 = 0; e0 < n_cols; e0 += kFewPages) {
-    if (!__syncthreads_or(open)) break;
+    for (int h = 0; h < 2; ++h) {
+      const int64_t r = __shfl_sync(0xffffffffu, row, quad + 8 * h);
+      row_pos[h] = __shfl_sync(0xffffffffu, pos, quad + 8 * h);
+      row_lse[h] = __shfl_sync(0xffffffffu, lse, quad + 8 * h);
 #pragma unroll
-    for (int h = 0; h < NC; ++h) {
-      const int c = row + kRows * h, e = e0 + (c >> 4);
-      const int64_t ks = pref_slot(page[h], row & 15);
-      const bool live = e < n_cols && ks < a.kv_slots;
-      const int64_t off = k_off + (live ? ks : 0);
-      if (sc.q_last) s_pos[c] = __ldg(sc.k_pos + off);
-      if (sc.q_doc) s_doc[c] = __ldg(sc.k_doc + off);
-      if (masked) {
-        const int2 rp = half_range(live, sc.q_last ? s_pos[c] : 0), rd = half_range(live, sc.q_doc ? s_doc[c] : 0);
-        if ((lane & 15) == 0) s_rng[c >> 4] = make_int4(rp.x, rp.y, rd.x, rd.y);
-      }
-      page[h] = page_of(e + kFewPages);
-    }
-    if (row < kFewPages) s_mask[row] = words;
-    words = mask_of(e0 + kFewPages + row);
-    __syncthreads();
-    for (int j = 0; open && j < min(kFewPages, n_cols - e0); ++j) {
-      uint32_t m = reinterpret_cast<const uint16_t*>(&s_mask[j])[code];
-      if (m == 0u) continue;
-      if (masked) {
-        const int4 rg = s_rng[j];
-        if (query_none(sc, rg, mine)) continue;
-        if (!query_all(sc, rg, mine)) m &= column_bits<true, 16>(sc.q_last, sc.q_doc, s_pos + 16 * j, s_doc + 16 * j, last, doc);
-        if (m == 0u) continue;
-      }
-      n += __popc(m);
-      open = n <= kFewKeys;
-      if (open) {
-        s_key[n_pages][row] = e0 + j;
-        s_x.bits[n_pages++][row] = static_cast<uint16_t>(m);
+      for (int c = 0; c < NC; ++c) {
+        q[h][c] = __ldg(reinterpret_cast<const uint4*>(a.q + r * D) + 4 * c + part);
+        d_o[h][c] = __ldg(reinterpret_cast<const uint4*>(a.d_o + r * D) + 4 * c + part);
       }
     }
-  }
-  const bool few = real && open && n > 0;
-  const int mine_n = few ? n : 0;
-  int upto = mine_n;  // pairs of the warp's rows up to this one
+    float sum[2] = {0.f, 0.f}, dsum[2] = {0.f, 0.f};
+    auto entry = [&](int e, int page) {
+      const int64_t ks = pref_slot(page, mine);  // this lane's column
+      const int64_t k_off = batch * sc.k_batch + (ks < a.kv_slots ? ks : 0);
+      const float k_pos = sc.slopes ? static_cast<float>(__ldg(sc.k_pos + k_off)) : 0.f;
+      const int cp = sc.q_last ? __ldg(sc.k_pos + k_off) : 0, cd = sc.q_doc ? __ldg(sc.k_doc + k_off) : 0;
+      uint32_t m = asked ? __ldg(reinterpret_cast<const uint16_t*>(a.masks + 2 * (static_cast<int64_t>(wk.e0) + e)) + seg) : 0u;
+      uint4 kk[2][NC], vv[2][NC];
 #pragma unroll
-  for (int off = 1; off < 32; off *= 2) {
-    const int x = __shfl_up_sync(0xffffffffu, upto, off);
-    if (lane >= off) upto += x;
+      for (int t = 0; t < 2; ++t) {
+        const int64_t kr = static_cast<int64_t>(kv_bh) * a.kv_slots + min(pref_slot(page, quad + 8 * t), a.kv_slots - 1);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) kk[t][c] = __ldg(reinterpret_cast<const uint4*>(a.k + kr * D) + 4 * c + part);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) vv[t][c] = __ldg(reinterpret_cast<const uint4*>(a.v + kr * D) + 4 * c + part);
+      }
+      // this lane's row's allowed columns
+      if (sc.q_last) {
+        uint32_t ok = 0u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ok |= __shfl_sync(0xffffffffu, cp, i) <= last ? 1u << i : 0u;
+        m &= ok;
+      }
+      if (sc.q_doc) {
+        uint32_t ok = 0u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ok |= __shfl_sync(0xffffffffu, cd, i) == doc ? 1u << i : 0u;
+        m &= doc >= 0 ? ok : 0u;
+      }
+      const uint32_t bits[2] = {__shfl_sync(0xffffffffu, m, quad), __shfl_sync(0xffffffffu, m, quad + 8)};
+      float s[2][4] = {}, dp[2][4] = {};
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          mma_16x8x16(s[t], q[0][c].x, q[1][c].x, q[0][c].y, q[1][c].y, kk[t][c].x, kk[t][c].y);
+          mma_16x8x16(s[t], q[0][c].z, q[1][c].z, q[0][c].w, q[1][c].w, kk[t][c].z, kk[t][c].w);
+          mma_16x8x16(dp[t], d_o[0][c].x, d_o[1][c].x, d_o[0][c].y, d_o[1][c].y, vv[t][c].x, vv[t][c].y);
+          mma_16x8x16(dp[t], d_o[0][c].z, d_o[1][c].z, d_o[0][c].w, d_o[1][c].w, vv[t][c].z, vv[t][c].w);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int col = 8 * t + 2 * part + j;
+          const float kp = __shfl_sync(0xffffffffu, k_pos, col);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float z = s[t][2 * h + j] * a.scale;
+            if (sc.cap > 0.f) {
+              const float u = z / sc.cap;
+              if (!(fabsf(u) < 1e-4f)) z = sc.cap * tanhf(u);  // (tanh u = u to 3e-9 there, and u may leave fp32's normals)
+            }
+            if (sc.slopes) z -= slope * fabsf(row_pos[h] - kp);
+            const float p = (bits[h] >> col) & 1u ? expf(z - row_lse[h]) : 0.f;
+            sum[h] += p;
+            if (p != 0.f) dsum[h] = fmaf(p, dp[t][2 * h + j], dsum[h]);
+          }
+        }
+      }
+    };
+    const int n_cols = wk.e1 - wk.e0;
+    for (int w = first; w < (far ? n_cols : first + 1); w += 64) {
+      uint64_t left = far ? ~0ull >> max(0, 64 - (n_cols - w)) : rec.entries;
+      int e = w + __ffsll(left) - 1;
+      int page = left != 0 ? __ldg(a.pages + wk.e0 + e) : 0;
+      while (left != 0) {
+        left &= left - 1;
+        const int e_next = w + __ffsll(left) - 1;
+        const int page_next = left != 0 ? __ldg(a.pages + wk.e0 + e_next) : 0;
+        entry(e, page);
+        e = e_next;
+        page = page_next;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int off = 1; off < 4; off *= 2) {
+        sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], off);
+        dsum[h] += __shfl_xor_sync(0xffffffffu, dsum[h], off);
+      }
+      const int r = quad + 8 * h;
+      const int64_t at = __shfl_sync(0xffffffffu, row, r);
+      if (part == 0 && ((few >> r) & 1u) && sum[h] > 0.f) a.delta[at] = dsum[h] / sum[h];  // (NaN scores: dO.O, which is NaN)
+    }
   }
-  if (lane == 31) s_total[row >> 5] = upto;
+  // the last CTA leaves the counts at zero for the next call
   __syncthreads();
-  int first = upto - mine_n, pairs = 0;
-#pragma unroll
-  for (int w = 0; w < kRows / 32; ++w) {
-    if (w < row >> 5) first += s_total[w];
-    pairs += s_total[w];
-  }
-  // the kernel before writes every row's Delta first; block 0 waits for it in any case,
-  // so that this kernel does not end (and let the stream go on) before that one
-  if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (pairs == 0) return;
-  if (few) {
-    // pages to keys (16 entry + slot), last ones first, so that none is written over unread
-    s_first[row] = first;
-    for (int i = n_pages - 1, k = n; i >= 0; --i) {
-      const int entry = s_key[i][row];
-      for (uint32_t m = s_x.bits[i][row]; m != 0u;) {
-        const int top = 31 - __clz(m);
-        s_key[--k][row] = 16 * entry + top;
-        m ^= 1u << top;
-      }
+  if (threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(a.few.counts + 2, 1) == static_cast<int>(gridDim.x) - 1) {
+      a.few.counts[0] = a.few.counts[1] = a.few.counts[2] = 0;
     }
-    for (int k = 0; k < n; ++k) s_row[first + k] = static_cast<uint8_t>(row);
-  }
-  __syncthreads();
-  const int kv_bh = (wk.bh / a.heads) * (a.heads / a.kv_group) + (wk.bh % a.heads) / a.kv_group;
-  const float slope = sc.slopes ? __ldg(sc.slopes + wk.bh % a.heads) : 0.f;
-  const int part = lane % kFewLanes;
-  for (int w = row / 32 * (32 / kFewLanes); w < pairs; w += kRows / kFewLanes) {  // the warp's four pairs
-    const bool live = w + lane / kFewLanes < pairs;
-    const int i = live ? w + lane / kFewLanes : w;  // (the others repeat the warp's first, which is still a key)
-    const int r = s_row[i], k = i - s_first[r], key = s_key[k][r];
-    const int64_t qs = pref_slot(wk.own_page(r >> 4), r & 15), qrow = static_cast<int64_t>(wk.bh) * a.q_slots + qs;
-    const int64_t ks = pref_slot(__ldg(a.pages + wk.e0 + (key >> 4)), key & 15);
-    const int64_t krow = static_cast<int64_t>(kv_bh) * a.kv_slots + ks;
-    float s = 0.f, dp = 0.f;
-#pragma unroll
-    for (int c = 0; c < D / 8 / kFewLanes; ++c) {
-      const int at = c * kFewLanes + part;
-      s = dot8(__ldg(reinterpret_cast<const uint4*>(a.q + qrow * D) + at), __ldg(reinterpret_cast<const uint4*>(a.k + krow * D) + at), s);
-      dp = dot8(__ldg(reinterpret_cast<const uint4*>(a.d_o + qrow * D) + at), __ldg(reinterpret_cast<const uint4*>(a.v + krow * D) + at), dp);
-    }
-#pragma unroll
-    for (int off = kFewLanes / 2; off > 0; off >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, off);
-      dp += __shfl_xor_sync(0xffffffffu, dp, off);
-    }
-    float z = s * a.scale;
-    if (sc.cap > 0.f) {
-      const float u = z / sc.cap;
-      if (!(fabsf(u) < 1e-4f)) z = sc.cap * tanhf(u);  // (tanh u = u to 3e-9 there, and u may leave fp32's normals)
-    }
-    if (sc.slopes)
-      z -= slope * fabsf(static_cast<float>(__ldg(sc.q_pos + (wk.bh / a.heads) * sc.q_batch + qs)) -
-                         static_cast<float>(__ldg(sc.k_pos + k_off + ks)));
-    const float p = expf(z - __ldg(a.lse + qrow));
-    __syncwarp();
-    if (part == 0 && live) {
-      s_key[k][r] = __float_as_int(p);
-      s_x.dp[k][r] = p != 0.f ? p * dp : 0.f;
-    }
-  }
-  __syncthreads();
-  if (few) {
-    float sum = 0.f, dsum = 0.f;
-    for (int k = 0; k < n; ++k) {
-      sum += __int_as_float(s_key[k][row]);
-      dsum += s_x.dp[k][row];
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (sum > 0.f) a.delta[static_cast<int64_t>(wk.bh) * a.q_slots + slot] = dsum / sum;  // (NaN scores: dO.O, which is NaN)
   }
 }
 
@@ -1124,14 +1227,21 @@ struct DqCfg {
 };
 
 // SC: the scored forms (score.cuh).
-template <int D, int SC>
+//
+// DELTA: no dQ, but Delta_i = sum_j P_ij dP_ij for the rows of an item, from the
+// weights themselves (see K2b, which does that for single rows of longer items).
+// Items of up to 256 listed keys get this pass, every row of them having few; it costs
+// a few steps each (9 of 84 us for two rows of 777 tokens with 4 heads) and overwrites
+// what Delta = dO.O gave.
+template <int D, int SC, bool DELTA>
 __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     dq_kernel(const __nv_bfloat16* __restrict__ q, const __grid_constant__ TmaPages tm_do,
               const __grid_constant__ TmaPages tm_k, const __grid_constant__ TmaPages tm_v,
               const int32_t* __restrict__ work, const int32_t* __restrict__ col_pages,
               const uint64_t* __restrict__ col_masks, const float* __restrict__ lse, const float* __restrict__ delta,
               __nv_bfloat16* __restrict__ out_dq, int64_t q_slots, float sl2, float scale, int heads, int kv_group,
-              int* err, const ScoreArgs sc, int64_t kv_slots, const int32_t* __restrict__ order) {
+              int* err, const ScoreArgs sc, int64_t kv_slots, const int32_t* __restrict__ order, int short_entries,
+              float* __restrict__ out_delta) {
   using C = DqCfg<D>;
   constexpr bool kScored = SC != kScoreNone, kCap = SC == kScoreCap;
   using W = BwdWarps<kScored>;
@@ -1175,6 +1285,12 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
   const int n_cols = wk.e1 - wk.e0;
   const int n_steps = (n_cols + NP - 1) / NP;
   const int warp = warp_id(), lane = lane_id();
+  if constexpr (DELTA) {
+    if (n_cols > short_entries || n_cols == 0) {  // (a row without keys keeps its 0)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      return;
+    }
+  }
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -1347,7 +1463,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       const uint64_t bk = sdesc_add(dkm, ks * C::kStageTile + half * kHalfStage);
 #pragma unroll
       for (int j = 0; j < NP; ++j)
-        if (j < n) umma_ts_w(tDQ, tPk(p) + 8 * j, sdesc_add(bk, j * 2048), idesc_acc, (st > 0 || j > 0) ? 1u : 0u);
+        if (!DELTA && j < n) umma_ts_w(tDQ, tPk(p) + 8 * j, sdesc_add(bk, j * 2048), idesc_acc, (st > 0 || j > 0) ? 1u : 0u);
       if (stage_end) umma_commit_w(&k_empty[ks]);
       umma_commit_w(&dq_done[p]);
     }
@@ -1393,7 +1509,8 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     }
     const float lse_row = (valid_slot && seg >= 0) ? __ldg(lse + roff) : 0.f;
     const float nlse2 = lse_row == -INFINITY ? -INFINITY : -lse_row * kLog2e;  // -inf: no key, every weight 0
-    const float dl = (valid_slot && seg >= 0) ? __ldg(delta + roff) : 0.f;
+    const float dl = (!DELTA && valid_slot && seg >= 0) ? __ldg(delta + roff) : 0.f;
+    float delta_sum = 0.f;  // DELTA: this group's part of the row's sum
     // this row's side of the masks and the bias
     int row_last = 0, row_doc = -1;
     float row_pos = 0.f, slope = 0.f;
@@ -1464,14 +1581,16 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       tc_fence_before();
       mbar_arrive(&s_free[b]);
       if (active) {
+        if constexpr (!DELTA) {
 #pragma unroll
-        for (int i = 0; i < CW; i += 2) {
-          float x0, x1;
-          f2_unpack(f2_add(f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), ndl), x0, x1);
-          d[i] = __float_as_uint(x0);
-          d[i + 1] = __float_as_uint(x1);
+          for (int i = 0; i < CW; i += 2) {
+            float x0, x1;
+            f2_unpack(f2_add(f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), ndl), x0, x1);
+            d[i] = __float_as_uint(x0);
+            d[i + 1] = __float_as_uint(x1);
+          }
         }
-        if constexpr (kCap) cap_scores<true>(a, d, sc.c, m != 0u);
+        if constexpr (kCap) cap_scores<!DELTA>(a, d, sc.c, m != 0u);
         if (sc.slopes) bias_scores(a, col_posf(ks) + 64 * (st % SPS) + CW * grp, row_pos, slope);
 #pragma unroll
         for (int i = 0; i < CW; i += 2) {
@@ -1480,7 +1599,13 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
           a[i] = __float_as_uint(x0);
           a[i + 1] = __float_as_uint(x1);
         }
-        weights_and_ds(a, d, m, pd);
+        if constexpr (DELTA) {
+#pragma unroll
+          for (int i = 0; i < CW; ++i)
+            if ((m >> i) & 1u) delta_sum = fmaf(ex2(__uint_as_float(a[i])), __uint_as_float(d[i]), delta_sum);
+        } else {
+          weights_and_ds(a, d, m, pd);
+        }
       }
       // Packed set b still feeds dQ(st-2).  Every row thread waits, active or not:
       // dq_done(st-2) implies that ds_full finished the phase of step st-2.
@@ -1489,7 +1614,7 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
         break;
       }
       tc_fence_after();
-      if (active) {
+      if (!DELTA && active) {
         tmem_st8(tPk(b) + lane_off + grp * (CW / 2), pd);
         tmem_wait_st();
       }
@@ -1500,7 +1625,9 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, ab));
       tc_fence_after();
     }
-    if (ok) {
+    // (the dO tile's last readers, the products of the last step, are done)
+    if constexpr (DELTA) reinterpret_cast<float*>(sDO)[128 * grp + row] = delta_sum;
+    if (!DELTA && ok) {
       // group g writes columns [g*D/4, (g+1)*D/4) of dQ
       constexpr int kOut = D / NG;  // 32 or 16
       const int col = grp * kOut;
@@ -1653,9 +1780,19 @@ __global__ void __launch_bounds__(BwdWarps<SC != kScoreNone>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // launched beside the dK / dV kernel: what follows in the stream waits for this
-  // kernel only, so this one ends after that one
+  // launched beside the dK / dV kernel (DELTA: beside the one that writes every
+  // row's Delta first): what follows in the stream waits for this kernel only, so
+  // this one ends after that one
   if constexpr (kScored) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (DELTA) {
+    const int row = threadIdx.x;
+    if (row < 16 * wk.n_own && wk.row_code(row) < 8u && !*abort_flag) {
+      const int64_t slot = pref_slot(wk.own_page(row >> 4), row & 15);
+      const float* part = reinterpret_cast<const float*>(sDO) + row;
+      if (slot < q_slots)
+        out_delta[static_cast<int64_t>(wk.bh) * q_slots + slot] = (part[0] + part[128]) + (part[256] + part[384]);
+    }
+  }
 }
 
 }  // namespace
@@ -1673,16 +1810,18 @@ cudaError_t launch_delta(int head_dim, const __nv_bfloat16* o, const __nv_bfloat
 }
 
 cudaError_t launch_prep(int head_dim, const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* delta, int64_t rows,
-                        int* sched, const FillArgs& q, const FillArgs& k, cudaStream_t st) {
-  PrepArgs a{o, d_o, delta, rows, 0, sched, q, k};
+                        const TileArgs& a, int64_t n_long, int short_entries, const ScoreArgs& sc, const FewList& few,
+                        const FillArgs& q, const FillArgs& k, cudaStream_t st) {
   const int64_t blocks = std::min<int64_t>((rows * (head_dim / 8) + 255) / 256, 148 * 16);
-  a.n_delta = static_cast<int>(std::max<int64_t>(blocks, 1));
+  const int n_delta = static_cast<int>(std::max<int64_t>(blocks, 1));
   const int64_t fills = std::min<int64_t>(std::max(q.n * q.bh, k.n * k.bh), 148 * 16);
-  const unsigned grid = static_cast<unsigned>(a.n_delta + fills);
+  const PrepArgs p{o,      d_o,     delta,   rows,        n_long,      short_entries, n_delta, a.sched, q, k,
+                   a.work, a.pages, a.masks, a.own_slots, a.col_slots, a.heads,       a.order, few,     sc};
+  const unsigned grid = static_cast<unsigned>(n_long + n_delta + fills);
   if (head_dim == 128)
-    prep_kernel<128><<<grid, 256, 0, st>>>(a);
+    prep_kernel<128><<<grid, 256, 0, st>>>(p);
   else
-    prep_kernel<64><<<grid, 256, 0, st>>>(a);
+    prep_kernel<64><<<grid, 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -1707,16 +1846,17 @@ static cudaError_t launch_dkdv_t(const TmaPages& tk, const TmaPages& tv, const T
   return cudaGetLastError();
 }
 
-template <int D, int SC>
+template <int D, int SC, bool DELTA>
 static cudaError_t launch_dq_t(const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
                                const TmaPages& tv, const TileArgs& a, const ScoreArgs& sc, const float* lse,
-                               const float* delta, __nv_bfloat16* dq, cudaStream_t st) {
+                               const float* delta, __nv_bfloat16* dq, int64_t n_items, int short_entries,
+                               float* out_delta, cudaStream_t st) {
   using C = DqCfg<D>;
   constexpr int kSmem = C::kSmem + (SC != kScoreNone ? C::kScoreBytes : 0);
-  cudaError_t e = cudaFuncSetAttribute(dq_kernel<D, SC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess || a.n_work == 0) return e;
+  cudaError_t e = cudaFuncSetAttribute(dq_kernel<D, SC, DELTA>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess || n_items == 0) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.n_work));
+  cfg.gridDim = dim3(static_cast<unsigned>(n_items));
   cfg.blockDim = dim3(BwdWarps<SC != kScoreNone>::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
@@ -1725,9 +1865,11 @@ static cudaError_t launch_dq_t(const __nv_bfloat16* q, const TmaPages& tdo, cons
   beside.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &beside;
   cfg.numAttrs = a.beside ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, dq_kernel<D, SC>, q, tdo, tk, tv, a.work, a.pages, a.masks, lse, delta, dq,
+  // short items are the last ones of the order
+  const int32_t* order = DELTA && a.order ? a.order + (a.n_work - n_items) : a.order;
+  return cudaLaunchKernelEx(&cfg, dq_kernel<D, SC, DELTA>, q, tdo, tk, tv, a.work, a.pages, a.masks, lse, delta, dq,
                             a.own_slots, a.scale * kLog2e, a.scale, a.heads, a.kv_group, a.err, sc, a.col_slots,
-                            a.order);
+                            order, short_entries, out_delta);
 }
 
 // Calls `go` with the head size and the form of the scores as constants.
@@ -1756,21 +1898,32 @@ cudaError_t launch_dq(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo,
                       const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, const float* lse,
                       const float* delta, __nv_bfloat16* dq, cudaStream_t st) {
   const auto go = [&](auto d, auto form) {
-    return launch_dq_t<decltype(d)::value, decltype(form)::value>(q, tdo, tk, tv, a, sc ? *sc : ScoreArgs(), lse, delta,
-                                                                  dq, st);
+    return launch_dq_t<decltype(d)::value, decltype(form)::value, false>(q, tdo, tk, tv, a, sc ? *sc : ScoreArgs(), lse,
+                                                                         delta, dq, a.n_work, 0, nullptr, st);
+  };
+  return by_form(head_dim, sc, go);
+}
+
+cudaError_t launch_delta_exact(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
+                               const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, int64_t n_short,
+                               int short_entries, const float* lse, float* delta, cudaStream_t st) {
+  const auto go = [&](auto d, auto form) {
+    constexpr int kForm = decltype(form)::value == kScoreNone ? kScoreMask : decltype(form)::value;  // always scored
+    return launch_dq_t<decltype(d)::value, kForm, true>(q, tdo, tk, tv, a, *sc, lse, nullptr, nullptr,
+                                                        a.order ? n_short : a.n_work, short_entries, delta, st);
   };
   return by_form(head_dim, sc, go);
 }
 
 cudaError_t launch_few_keys(int head_dim, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                            const __nv_bfloat16* d_o, const TileArgs& a, const ScoreArgs& sc, const float* lse,
-                            float* delta, cudaStream_t st) {
-  if (a.n_work == 0) return cudaSuccess;
-  const FewArgs f{q,           k,           v,           d_o,     lse,        delta,   a.work, a.pages,
-                  a.masks,     a.own_slots, a.col_slots, a.heads, a.kv_group, a.scale, sc};
+                            const __nv_bfloat16* d_o, const TileArgs& a, int64_t n_long, const ScoreArgs& sc,
+                            const FewList& few, const float* lse, float* delta, cudaStream_t st) {
+  if (n_long == 0) return cudaSuccess;
+  const FewArgs f{q,       k,   v,           d_o,         lse,     delta,      a.work,  a.pages,
+                  a.masks, few, a.own_slots, a.col_slots, a.heads, a.kv_group, a.scale, sc};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.n_work));
-  cfg.blockDim = dim3(kRows);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(8 * n_long, 148 * 3)));
+  cfg.blockDim = dim3(kFewThreads);
   cfg.stream = st;
   cudaLaunchAttribute behind = {};
   behind.id = cudaLaunchAttributeProgrammaticStreamSerialization;

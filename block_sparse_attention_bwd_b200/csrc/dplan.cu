@@ -488,6 +488,11 @@ int device_replan(spattn_plan_s* P, const int64_t* row_ptr, const int32_t* kv_gr
         ensure(&wl.d_pages, wl.cap_pages, total) != cudaSuccess ||
         ensure(&wl.d_masks, wl.cap_masks, total * kMaskWords) != cudaSuccess)
       return SPATTN_ERR_OOM;
+    if (pass == 0) {
+      const cudaError_t grown = ensure(&P->few.pages, P->cap_few, 8 * n_work);
+      P->few.cap = static_cast<int>(std::min<int64_t>(P->cap_few, INT32_MAX));
+      if (grown != cudaSuccess) return SPATTN_ERR_OOM;
+    }
     la[pass].out_work = wl.d_work;
     la[pass].out_pages = wl.d_pages;
     la[pass].out_masks = wl.d_masks;

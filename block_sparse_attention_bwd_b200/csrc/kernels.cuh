@@ -57,7 +57,7 @@ struct TileArgs {
   int heads = 1, kv_heads = 1, kv_group = 1;
   const uint16_t* col_heads = nullptr;
   // launch_dq right behind launch_dkdv, both scored, and launch_few_keys behind
-  // launch_prep: it may run beside that kernel
+  // launch_prep, launch_delta_exact behind those: it may run beside that kernel
   bool beside = false;
   const int32_t* order = nullptr;  // the items longest first over all heads (scored forms; null: as listed)
   // some query-owned item takes the 64-row route (the forward then runs the
@@ -103,16 +103,45 @@ struct FillArgs {
   float* lse = nullptr;
 };
 
-// Delta, the zeroed work-item counter of launch_dkdv and the fills of a scored
-// backward, in one launch.
-cudaError_t launch_prep(int head_dim, const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* delta, int64_t rows,
-                        int* sched, const FillArgs& q, const FillArgs& k, cudaStream_t st);
+// An owned page that holds rows of few allowed keys: its number (8 item + page of the
+// item), those rows (bits; kFewFar: their keys are spread over more than 64 entries of the
+// item's list), the first entry with one of their keys, and which of the 64 from there
+// on have one.
+struct FewPage {
+  int page;
+  uint32_t rows;
+  int first, pad;
+  uint64_t entries, pad2;
+};
+constexpr uint32_t kFewFar = 0x10000u;
+// The pages that a scored backward's scan finds, in any order (room for 8 per
+// query-owned item), and three counts that are zero between calls: found, taken, CTAs done.
+struct FewList {
+  FewPage* pages = nullptr;
+  int* counts = nullptr;
+  int cap = 0;
+};
 
-// K2b: Delta from the weights for the rows of at most 16 allowed keys, over the
-// query-owned items, right behind launch_prep and (a.beside) beside it.
+// Start of a scored backward in one launch: Delta, the zeroed work-item counter of
+// launch_dkdv, the fills, and the scan of the query-owned items `a` of more than
+// `short_entries` entries for rows with at most 127 allowed keys (the first n_long of
+// a.order; without an order n_long is all items).
+cudaError_t launch_prep(int head_dim, const __nv_bfloat16* o, const __nv_bfloat16* d_o, float* delta, int64_t rows,
+                        const TileArgs& a, int64_t n_long, int short_entries, const ScoreArgs& sc, const FewList& few,
+                        const FillArgs& q, const FillArgs& k, cudaStream_t st);
+
+// K2b: Delta from the weights for the rows that the scan found, right behind
+// launch_prep and (a.beside) beside it.
 cudaError_t launch_few_keys(int head_dim, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                            const __nv_bfloat16* d_o, const TileArgs& a, const ScoreArgs& sc, const float* lse,
-                            float* delta, cudaStream_t st);
+                            const __nv_bfloat16* d_o, const TileArgs& a, int64_t n_long, const ScoreArgs& sc,
+                            const FewList& few, const float* lse, float* delta, cudaStream_t st);
+
+// Delta from the weights for every row of the query-owned items of at most
+// `short_entries` entries (`n_short`: how many the end of a.order holds; without an order
+// every item is looked at), right behind launch_few_keys or launch_prep and beside it.
+cudaError_t launch_delta_exact(int head_dim, const __nv_bfloat16* q, const TmaPages& tdo, const TmaPages& tk,
+                               const TmaPages& tv, const TileArgs& a, const ScoreArgs* sc, int64_t n_short,
+                               int short_entries, const float* lse, float* delta, cudaStream_t st);
 
 // K1: O, LSE for every query-owned work item; `sc` (may be null) modifies the scores,
 // and with it the launch also does `fill`.

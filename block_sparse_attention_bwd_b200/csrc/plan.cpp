@@ -1033,6 +1033,8 @@ void free_plan_device(spattn_plan_s* P) {
   cudaFree(P->d_err);
   cudaFree(P->d_sched);
   cudaFree(P->d_delta);
+  cudaFree(P->few.pages);
+  cudaFree(P->few.counts);
   for (auto& e : P->events) {
     cudaEventDestroy(e.start);
     cudaEventDestroy(e.stop);
@@ -1196,6 +1198,7 @@ int build_plan(const spattn_layout* L, const spattn_graph* G, spattn_plan_s* P) 
       std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return len(a) > len(b); });
       if ((st = upload(order, &w->d_order, bytes, &w->cap_order))) return st;
       w->ordered = true;
+      w->n_short = std::count_if(order.begin(), order.end(), [&](int32_t i) { return len(i) <= kShortEntries; });
     }
   }
   if ((st = upload(P->q_fill, &P->d_q_fill, bytes))) return st;
@@ -1205,7 +1208,13 @@ int build_plan(const spattn_layout* L, const spattn_graph* G, spattn_plan_s* P) 
   if (cudaMemset(P->d_err, 0, sizeof(int)) != cudaSuccess) return SPATTN_ERR_CUDA;
   const size_t delta_bytes = static_cast<size_t>(L->batch) * L->heads * L->q_slots * sizeof(float);
   if (cudaMalloc(reinterpret_cast<void**>(&P->d_delta), delta_bytes) != cudaSuccess) return SPATTN_ERR_OOM;
-  P->device_bytes = bytes + static_cast<int64_t>(delta_bytes) + static_cast<int64_t>(sizeof(int));
+  P->cap_few = std::max<int64_t>(8 * P->wq.n_work, 1);
+  const size_t few_bytes = static_cast<size_t>(P->cap_few) * sizeof(FewPage);
+  if (cudaMalloc(reinterpret_cast<void**>(&P->few.pages), few_bytes) != cudaSuccess) return SPATTN_ERR_OOM;
+  P->few.cap = static_cast<int>(std::min<int64_t>(P->cap_few, INT32_MAX));
+  if (cudaMalloc(reinterpret_cast<void**>(&P->few.counts), 3 * sizeof(int)) != cudaSuccess) return SPATTN_ERR_OOM;
+  if (cudaMemset(P->few.counts, 0, 3 * sizeof(int)) != cudaSuccess) return SPATTN_ERR_CUDA;
+  P->device_bytes = bytes + static_cast<int64_t>(delta_bytes + few_bytes) + static_cast<int64_t>(sizeof(int));
   P->plan_ms = std::chrono::duration<double, std::milli>(std::chrono::steady_clock::now() - t0).count();
   return SPATTN_OK;
 }

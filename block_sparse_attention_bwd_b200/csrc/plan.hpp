@@ -8,6 +8,7 @@
 
 #include <cuda_runtime.h>
 
+#include "kernels.cuh"
 #include "spattn.h"
 
 namespace spattn {
@@ -76,6 +77,7 @@ struct WorkList {
   int32_t* d_order = nullptr;
   int64_t cap_order = 0;
   bool ordered = false;
+  int64_t n_short = 0;  // items of at most kShortEntries entries, the last ones of d_order
   // capacities of the device arrays (elements) and, after a device re-plan,
   // the number of entries on the device
   int64_t cap_work = 0, cap_pages = 0, cap_masks = 0, cap_heads = 0;
@@ -89,6 +91,10 @@ struct WorkList {
 // tokens, 16 query heads over 4: forward 630 -> 540, dK / dV 1360 -> 1140; on 16384
 // tokens of short documents, 16 heads: 111 -> 94 and 201 -> 186.
 constexpr int64_t kOrderMax = 32 * 148;
+
+// Query-owned items of up to this many entries (256 keys) get Delta from their
+// weights as a whole in a scored backward, in longer ones single rows do (see the kernels).
+constexpr int32_t kShortEntries = 16;
 
 // Work item templates of one pass for the device planner: the slot-order
 // tiles of the layout split into items, without their column lists.
@@ -148,6 +154,8 @@ struct spattn_plan_s {
   int* d_err = nullptr;        // device error word
   int* d_sched = nullptr;      // work-item counter of the persistent dK/dV kernel
   float* d_delta = nullptr;    // [batch, heads, q_slots] rowsum(dO * O)
+  spattn::FewList few;         // pages with rows of few keys (scored backward), room for 8 per query-owned item
+  int64_t cap_few = 0;
   spattn::DevPlanner dp;        // device planner state
   bool host_stale = false;      // the work lists / graph were rebuilt on the device
   int64_t graph_nnz = 0;        // entries of the graph the device lists follow
