@@ -22,9 +22,11 @@
 // Scored forms (spattn_score): P from the modified scores z, dS = P (dP - Delta)
 // (1 - tanh^2), four warp groups of 16 columns, -LSE, positions and documents of the
 // columns in lines beside the stages.  Bound: the row threads' instructions and the
-// latency of a step (tensor pipe busy 0.40 to 0.45).  12289 causal tokens with a
-// prefix and a cap of 50, 16 heads over 4, D = 128: dK / dV 1695 us and dQ 1435
-// (masks alone 1455 and 1040, unmodified 1240 and 905).
+// latency of a step (tensor pipe busy 0.39 in dK / dV and 0.30 in dQ; with 96 registers a
+// thread the D = 128 forms of dK / dV spill, 80 bytes of stores and 52 of loads).  12289
+// causal tokens with a prefix and a cap of 50, 16 heads over 4, D = 128: dK / dV 1740 us
+// and dQ 1475 in a long run (1695 and 1435 in a short one; there masks alone take 1455
+// and 1040, unmodified 1240 and 905).
 #include <algorithm>
 #include <type_traits>
 

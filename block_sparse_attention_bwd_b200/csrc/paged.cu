@@ -23,10 +23,13 @@
 // ranges of `chunk` keys; split rows go to a workspace in fp32 with their
 // reference and sum, and paged_join_kernel adds them.
 //
-// Measured (head_dim 128): 64 decoding sequences of 500 .. 9000 keys, 32 heads over
-// 8, in 241 us (5.4 TB/s); 2048 tokens over 131072 keys, 16 heads over 4, in
-// 2185 us (1.0 PFLOP/s); 777 keys of one sequence in 16 us, of which the launches and
-// the host are most.
+// Measured (head_dim 128, bounds equal to the lengths): 64 decoding sequences of 500 ..
+// 9000 keys, 32 heads over 8, in 254 us of a long run (5.2 TB/s; 230 to 241 in short
+// ones, before the board's power limit takes clocks); 2048 tokens over 131072 keys,
+// 16 heads over 4, in 2450 us (0.9 PFLOP/s; 2185 in short runs); 777 keys of one sequence
+// in 17 us, of which the launches and the host are most.  Ranges are sized from the
+// bounds: with max_kv = 131072 the 64 sequences take 371 us (short runs), and one token
+// over 8000 keys 41, not 20.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -56,10 +59,11 @@ constexpr float kRescale = 8.0f;  // rescale O when the running maximum grows by
 // a long run the board's power: products of 128 rows, four of them live and the others
 // whatever stood in shared memory, throttled the clocks to 1.57 GHz (64 sequences:
 // 235 us in a short run, 280 in one of a second).  So the products have 64 rows, and
-// all but the live ones are zeros, which cost little (241 and 255 us).  Q takes 4 KB per
-// chunk and 4 KB of zeros behind them (rows 32 .. 63 of a chunk are what follows it), and the K
-// and V rings are a stage deeper.  Row r of an M = 64 product is TMEM lane
-// r % 16 + 32 (r / 16).
+// most of the dead ones are zeros, which cost little (241 and 255 us).  Q takes 4 KB per
+// chunk of 64 columns and 4 KB of zeros behind the last: rows 32 .. 63 of a chunk are what
+// follows it, which for the first of two (head_dim 128) is the second's rows, live ones
+// among them.  Products of those rows are never read.  The K and V rings are a stage deeper.
+// Row r of an M = 64 product is TMEM lane r % 16 + 32 (r / 16).
 template <int D, int FORM, bool SMALL>
 struct PagedCfg {
   static constexpr int kNch = D / 64;

@@ -6,8 +6,9 @@
 // the gradient is the same with -t.  Elements from rot on are copied.
 //
 // The angle is formed in fp64 as a fraction of a turn (pos * freq / 2 pi,
-// less its nearest integer), which keeps 1e-7 rad at position 2^31; only the
-// fraction is rounded to fp32.  Rotation is fp32, rounded once on the store.
+// less its nearest integer): off by 2^-52 or so of the turns, at worst 3.2e-7 rad at
+// position 2^31 with freq 1, and 1e-7 more by the fraction's rounding to fp32.
+// Rotation is fp32, rounded once on the store.
 //
 // Bound: memory (each element read and written once, 3 flops per element): 75600
 // slots of 40 + 40 heads, D = 128, bf16, three axes take 490 us (6.3 TB/s); a row

@@ -267,8 +267,11 @@ typedef struct {
  * No gradient of slopes is formed.  Rows that the masks leave without a pair,
  * of Q and dO as of K and V, may like padded ones hold any finite values.
  * Weights relative to a fixed reference reach 2^80 in rows whose LSE does not
- * pass 55, so V has to stay below 2^46 there.  A score that modifies nothing
- * runs the plain kernels.  One plan serves one stream at a time, replays of
+ * pass 55, so V has to stay below 2^46 there.  A call in which some row's LSE
+ * does pass +-55 is right but slower (its tiles run up to three times).  The
+ * last bits of a row may depend on the other rows of its 128-row tile (never on
+ * other heads or batch entries).  A score that modifies nothing runs the plain
+ * kernels.  One plan serves one stream at a time, replays of
  * captured graphs included.  (Score caps, distance biases and packed documents have no
  * counterpart in the paper.) */
 int spattn_fwd_scored(const void* q, const void* k, const void* v, spattn_plan_t plan, const spattn_score* score,
@@ -332,7 +335,8 @@ typedef struct {
   int32_t page_slots;      /* multiple of 16 */
   int32_t max_seqs;        /* bounds of any call: sequences, */
   int32_t max_q;           /* new tokens of one sequence (1: decoding), */
-  int32_t max_kv;          /* cache slots of one sequence */
+  int32_t max_kv;          /* cache slots of one sequence.  The work of a call is cut up
+                            * by these bounds: far above the lengths they cost time */
   float scale;             /* softmax scale > 0; 0 selects 1/sqrt(head_dim) */
   float softcap;           /* > 0, or 0 for none */
 } spattn_paged_layout;
@@ -373,7 +377,10 @@ int spattn_paged_workspace(spattn_paged_t paged, int64_t n_seqs, int64_t* bytes)
  * lengths leave the bounds, whose rows leave q, whose cache is shorter than
  * its new tokens or longer than its table is skipped, and a page outside the
  * pool is read as page 0; both are reported by spattn_paged_check.  Cache slots
- * behind kv_len may hold anything, NaN included.  (The paper has no
+ * behind kv_len may hold anything, NaN included.  With a softcap of up to 55
+ * weights are relative to a fixed reference and may be as large as 2^80: V has to
+ * stay below 2^46 there.  The last bits of a row depend on how the call is cut up
+ * (the bounds and n_seqs).  (The paper has no
  * counterpart; pages are gathered as the KPage abstract's 16-row pages are,
  * zhuanzhiai.com paper page.) */
 int spattn_paged_fwd(spattn_paged_t paged, const spattn_paged_call* call, void* stream);
