@@ -158,3 +158,72 @@ def test_profiled_calls_give_the_same_bits():
         for x, y in zip(r, runs[0]):
             assert torch.equal(x, y)
     sp.spattn_check(plan)
+
+
+def _backward_of(p, t, plan, sc):
+    o, lse = sp.spattn_fwd_scored(t["q"], t["k"], t["v"], plan, sc)
+    return (o, lse) + tuple(sp.spattn_bwd_scored(t["q"], t["k"], t["v"], o, lse, t["do"], plan, sc))
+
+
+def test_replays_with_other_documents():
+    """A captured pass lists its rows of few keys anew: documents that change between replays, none among them."""
+    n = 700
+    p = _tokens(n, 3, 128, 1)
+    t = {k: v.cuda() for k, v in W.make_tensors(p).items()}
+    doc = _i32(_docs(n, 30, 1))
+    plan, sc = sp.Plan.from_problem(p), sp.Score(q_doc=doc, k_doc=doc)
+    _backward_of(p, t, plan, sc)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = _backward_of(p, t, plan, sc)
+    for other in (_docs(n, 200, 2), np.zeros(n), _docs(n, 3, 3), np.full(n, -1), _docs(n, 60, 4)):
+        doc.copy_(_i32(other))
+        for _ in range(2):
+            g.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in captured]
+        for x, y in zip(got, _backward_of(p, t, plan, sc)):
+            assert torch.equal(x, y)
+    sp.spattn_check(plan)
+
+
+def test_two_plans_on_two_streams():
+    work = []
+    for n, longest in ((900, 40), (640, 7)):
+        p = _tokens(n, 4, 64, 2)
+        t = {k: v.cuda() for k, v in W.make_tensors(p).items()}
+        doc = _i32(_docs(n, longest, n))
+        work.append((p, t, sp.Plan.from_problem(p), sp.Score(softcap=9.0, q_doc=doc, k_doc=doc)))
+    want = [_backward_of(*w) for w in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    got = []
+    for _ in range(20):
+        for w, st in zip(work, streams):
+            with torch.cuda.stream(st):
+                got.append((w, _backward_of(*w)))
+    torch.cuda.synchronize()
+    for i, (_, r) in enumerate(got):
+        for x, y in zip(r, want[i % 2]):
+            assert torch.equal(x, y)
+    for w in work:
+        sp.spattn_check(w[2])
+
+
+def test_more_items_than_are_ordered():
+    """Lists without an order (their number is above the limit for one): each item is looked at by both passes."""
+    n, heads, batch = 320, 20, 80  # 4800 items of 20 pages
+    p = _tokens(n, heads, 64, 20, batch=batch)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    t = {k: torch.randn((batch, heads, n, 64), generator=gen, device="cuda").bfloat16() for k in ("q", "k", "v", "do")}
+    doc = _i32(_docs(n, 20, 5))
+    plan = sp.Plan.from_problem(p)
+    assert plan.stats()["n_work_fwd"] == 4800
+    got = _backward_of(p, t, plan, sp.Score(q_doc=doc, k_doc=doc))
+    one = sp.Plan.from_problem(_tokens(n, heads, 64, 20))
+    for b in (0, 41, 79):
+        alone = _backward_of(p, {k: v[b:b + 1].contiguous() for k, v in t.items()}, one, sp.Score(q_doc=doc, k_doc=doc))
+        for x, y in zip(got, alone):
+            assert torch.equal(x[b:b + 1], y)
+    sp.spattn_check(plan)
